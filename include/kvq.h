@@ -72,8 +72,11 @@ typedef enum {
     KVQ_INT4_PER_GROUP = 5,    /* 4-bit codes in [-7, 7] ([KVC] §2.3 lists INT4 beside
                                   INT8/FP8), scale = absmax/7 per `group` channels as
                                   for KVQ_INT8_PER_GROUP; two codes per byte         */
-    KVQ_FP8_E5M2 = 6           /* e5m2 codes of the values themselves, no scale
+    KVQ_FP8_E5M2 = 6,          /* e5m2 codes of the values themselves, no scale
                                   ([P312] §三: kv_cache_dtype fp8_e5m2); saturating  */
+    KVQ_INT8_PER_BLOCK = 7,    /* one fp32 scale per (block, kv head, K|V): the
+                                  absmax of the block's tokens over 127              */
+    KVQ_FP8_E4M3_PER_BLOCK = 8 /* the same with e4m3 codes, absmax / 448             */
 } kvq_dtype;
 
 typedef struct kvq_pool kvq_pool; /* opaque; one per layer */
@@ -84,9 +87,10 @@ typedef struct kvq_pool kvq_pool; /* opaque; one per layer */
 typedef struct {
     size_t total_bytes;  /* everything kvq_alloc_pool needs (header + regions)  */
     size_t code_bytes;   /* 2 * num_blocks * block_size * kv_heads * head_dim * elem */
-    size_t scale_bytes;  /* fp32 scales of every format that has them           */
+    size_t scale_bytes;  /* fp32 scales of every format that has them (per-block
+                            formats: 16 per page, two scales and padding)       */
     size_t header_bytes; /* device error word and padding                       */
-    size_t page_bytes;   /* bytes of one (block, kv head) page: K+V codes (+ group scales) */
+    size_t page_bytes;   /* bytes of one (block, kv head) page: K+V codes (+ group or block scales) */
 } kvq_pool_layout;
 
 /* Byte accounting for the given geometry, without allocating.  Returns
@@ -118,7 +122,8 @@ size_t kvq_pool_bytes(int64_t num_blocks, int block_size, int kv_heads, int head
  *                cudaFree) the pool on the current device.
  *   out        : host pointer that receives the handle.
  * The pool's contents are unspecified until written by kvq_append, except
- * that the error word is cleared and per-channel scales are set to zero.
+ * that the error word is cleared and per-channel and per-block scales are set
+ * to zero.
  * Synchronous.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 kvq_status kvq_alloc_pool(int64_t num_blocks, int block_size, int kv_heads, int head_dim,
                           kvq_dtype dtype, int group, void* device_buf, size_t buf_bytes,
@@ -153,16 +158,119 @@ kvq_status kvq_calibrate_channel_scales(kvq_pool* pool, const kvq_half* k, const
  * e4m3 round-to-nearest-even saturating for FP8; an all-zero group stores s=0
  * and zero codes.  Per-channel uses the pool's static scales.  FP16 stores x.
  * Two tokens with the same slot in one call race (result unspecified).
+ * Formats with one scale per block quantize a block's tokens together, so the
+ * tokens of one call that fall into one block must stand next to each other in
+ * slot_mapping (as every mapping made sequence by sequence has them; otherwise
+ * that block's contents are unspecified).  The block's scale becomes
+ * s = max(s_old, absmax of the call's tokens in it / 127 (448)); a token at
+ * offset 0 starts the block anew, with no s_old and nothing kept of what it
+ * held.  Where s grew, the block's other codes are rounded again at the new
+ * scale: code' = round(code * s_old / s) in fp32.  The append owns the whole
+ * block: no other work may read or write it meanwhile.
  * Device errors: a slot >= num_blocks*block_size sets OUT_OF_RANGE and the
  * token is skipped. */
 kvq_status kvq_append(kvq_pool* pool, const kvq_half* k, const kvq_half* v,
                       const int64_t* slot_mapping, int64_t T, cudaStream_t stream);
 
+/* ---- Query/key norms and rotary positions.  Before keys are appended and
+ * queries attend, a model's attention layer norms each head of them (in some
+ * models) and rotates pairs of their channels by angles that grow with the
+ * token's position.  The pages do not describe this step; it is here so that
+ * the rows of a layer's projection can go to the cache directly. */
+
+#define KVQ_ROPE_MAX_PAIRS 64
+
+typedef enum {
+    KVQ_ROPE_HALF = 0,       /* pair i is channels i and i + rotary_dim/2 */
+    KVQ_ROPE_INTERLEAVED = 1 /* pair i is channels 2i and 2i + 1          */
+} kvq_rope_layout;
+
+/* How the frequencies f_i = base^(-2i/r), r = rotary_dim, radians per position,
+ * are changed so that a model reaches past the length it was trained for. */
+typedef enum {
+    KVQ_ROPE_NONE = 0,
+    KVQ_ROPE_LINEAR = 1, /* f_i / factor                                          */
+    KVQ_ROPE_BASE = 2,   /* base replaced by base * factor^(r / (r - 2))          */
+    KVQ_ROPE_PARTS = 3,  /* f_i for pairs that turn more than `high` times over
+                            orig_len positions, f_i / factor below `low` turns, in
+                            between a ramp linear in i, its ends rounded outwards
+                            to whole pairs                                        */
+    KVQ_ROPE_BANDS = 4   /* the same with a ramp linear in the number of turns    */
+} kvq_rope_scaling;
+
+typedef struct {
+    int rotary_dim;   /* rotated channels of a head, its first ones: a multiple of
+                         16, <= 128 */
+    int layout;       /* kvq_rope_layout  */
+    int scaling;      /* kvq_rope_scaling */
+    double base;      /* > 1, e.g. 10000  */
+    double factor;    /* >= 1; KVQ_ROPE_NONE ignores it             */
+    double orig_len;  /* >= 1; KVQ_ROPE_PARTS and KVQ_ROPE_BANDS only */
+    double low, high; /* 0 < low < high; the same two               */
+    double magnitude; /* factor on cosine and sine; 0 takes 1, or for
+                         KVQ_ROPE_PARTS 0.1 ln(factor) + 1          */
+} kvq_rope_config;
+
+/* A rotation ready for the kernels: plain data that the caller owns (no device
+ * memory), good for any position, stream and device. */
+typedef struct {
+    int rotary_dim, layout;
+    float magnitude;
+    int reserved;
+    uint64_t turns[KVQ_ROPE_MAX_PAIRS]; /* f_i / 2 pi as a 64-bit fraction */
+} kvq_rope_plan;
+
+/* Fill *out from *config.  Host only; needs no GPU.  Errors: INVALID_ARG for a
+ * value outside the ranges above, UNSUPPORTED for a rotary_dim that is no
+ * multiple of 16. */
+kvq_status kvq_rope_init(const kvq_rope_config* config, kvq_rope_plan* out);
+
+typedef enum { KVQ_X_FP16 = 0, KVQ_X_BF16 = 1 } kvq_x_type;
+
+/* Norm and rotate query and key rows:
+ *   y = x / sqrt(mean(x^2) + eps) * weight   over each head, if a weight is given
+ *   out = fp16(rotate(y, position))          channels >= rotary_dim are only normed
+ *   plan        : host pointer; NULL = no rotation (positions may then be NULL)
+ *   q, k        : [T][heads][head_dim] fp16 or bf16 (x_type), heads contiguous,
+ *                 token t's row row_stride elements after token t-1's (at least
+ *                 heads*head_dim, a multiple of 8), 16-byte aligned.  A head
+ *                 count of 0 leaves that side out (its pointers may be NULL)
+ *   head_dim    : 64 or 128, >= rotary_dim
+ *   positions   : int64 [T]; any value, a negative one turns backwards
+ *   q_weight, k_weight : fp32 [head_dim] or NULL
+ *   eps         : >= 0
+ *   q_out, k_out : fp16, laid out like q and k with strides of their own.  An
+ *                 out may be its own input (same pointer and stride); any other
+ *                 overlap gives unspecified results
+ * The arithmetic is fp32, rounded once to fp16; a cosine or sine is within 2^-20
+ * at any position.  Errors: INVALID_ARG, UNSUPPORTED (head_dim), CUDA. */
+kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
+                    int64_t q_row_stride, int num_q_heads, const void* k, int64_t k_row_stride,
+                    int num_k_heads, int head_dim, const int64_t* positions, int64_t T,
+                    const float* q_weight, const float* k_weight, float eps, kvq_half* q_out,
+                    int64_t q_out_row_stride, kvq_half* k_out, int64_t k_out_row_stride,
+                    cudaStream_t stream);
+
+/* kvq_rope of queries and keys and kvq_append of keys and values in one kernel:
+ * the normed and rotated keys are quantized from fp32 (an append of kvq_rope's
+ * k_out would first have rounded them to fp16) and reach memory only as codes.
+ *   k, v        : [T][kv_heads][head_dim] of the pool, fp16 or bf16, strided as
+ *                 above; v is neither normed nor rotated
+ *   slot_mapping : as for kvq_append, with its rule for per-block formats; the
+ *                 query row of a token that is not stored is computed all the same
+ * The other arguments are those of kvq_rope; num_q_heads may be 0. */
+kvq_status kvq_rope_append(kvq_pool* pool, const kvq_rope_plan* plan, kvq_x_type x_type,
+                           const void* q, int64_t q_row_stride, int num_q_heads, const void* k,
+                           int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                           const int64_t* positions, const int64_t* slot_mapping, int64_t T,
+                           const float* q_weight, const float* k_weight, float eps,
+                           kvq_half* q_out, int64_t q_out_row_stride, cudaStream_t stream);
+
 /* Copy whole blocks ([KVC] §4.4: a request that must write into a block it
  * shares with others first gets its own copy -- copy-on-write).
  *   src_blocks, dst_blocks : int32 [n]; block dst_blocks[i] becomes a copy of
  *                            block src_blocks[i]: every kv head's K and V codes,
- *                            their per-group scales, and (per-token formats)
+ *                            their per-group or per-block scales, and (per-token formats)
  *                            the block's token scales
  * Pairs run in parallel: a destination must not be another pair's source or
  * destination.  Device errors: an id outside the pool sets OUT_OF_RANGE and
@@ -394,11 +502,19 @@ kvq_status kvq_selftest_decode_timeout(const kvq_pool* pool, const kvq_half* q, 
                                        int max_context_len, float* out, void* workspace,
                                        size_t ws_bytes, int wait_tries, cudaStream_t stream);
 
+/* The cached K and V of n slots as fp16 values, code * scale in fp32 rounded
+ * once: k_out, v_out [n][kv_heads][head_dim], 16-byte aligned.  A negative slot
+ * leaves its rows as they were; a slot outside the pool does too and sets
+ * OUT_OF_RANGE. */
+kvq_status kvq_read_values(const kvq_pool* pool, const int64_t* slots, int64_t n, kvq_half* k_out,
+                           kvq_half* v_out, cudaStream_t stream);
+
 /* Read back n slots in a canonical layout (for tests and debugging).
  *   codes_out  : [n][2][kv_heads][head_dim] elements of the pool's code type
  *                (int8, e4m3 byte, or fp16; INT4 codes come back one per int8)
  *   scales_out : per-group [n][2][kv_heads][head_dim/group] fp32;
- *                per-token [n][2] fp32; may be NULL (and is ignored) for
+ *                per-token [n][2] fp32; per-block [n][2][kv_heads] fp32 (the
+ *                slot's block's scales); may be NULL (and is ignored) for
  *                FP16 and per-channel pools
  * A slot outside the pool sets OUT_OF_RANGE and its output is left untouched. */
 kvq_status kvq_read_slots(const kvq_pool* pool, const int64_t* slots, int64_t n,

@@ -30,7 +30,22 @@ KVQ_INT8_PER_GROUP = 3
 KVQ_FP8_E4M3_PER_TOKEN = 4
 KVQ_INT4_PER_GROUP = 5
 KVQ_FP8_E5M2 = 6
+KVQ_INT8_PER_BLOCK = 7
+KVQ_FP8_E4M3_PER_BLOCK = 8
 GROUP_FORMATS = (KVQ_INT8_PER_GROUP, KVQ_INT4_PER_GROUP)
+BLOCK_FORMATS = (KVQ_INT8_PER_BLOCK, KVQ_FP8_E4M3_PER_BLOCK)
+
+# kvq_rope_layout, kvq_rope_scaling, kvq_x_type
+KVQ_ROPE_HALF = 0
+KVQ_ROPE_INTERLEAVED = 1
+KVQ_ROPE_NONE = 0
+KVQ_ROPE_LINEAR = 1
+KVQ_ROPE_BASE = 2
+KVQ_ROPE_PARTS = 3
+KVQ_ROPE_BANDS = 4
+KVQ_ROPE_MAX_PAIRS = 64
+KVQ_X_FP16 = 0
+KVQ_X_BF16 = 1
 
 # kvq_status
 KVQ_OK = 0
@@ -55,6 +70,21 @@ class _Layout(ctypes.Structure):
     _fields_ = [("total_bytes", ctypes.c_size_t), ("code_bytes", ctypes.c_size_t),
                 ("scale_bytes", ctypes.c_size_t), ("header_bytes", ctypes.c_size_t),
                 ("page_bytes", ctypes.c_size_t)]
+
+
+class _RopeConfig(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_len", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class RopePlan(ctypes.Structure):
+    """kvq_rope_plan: a rotation made by kvq_rope_init (plain host data)."""
+
+    _fields_ = [("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int),
+                ("turns", ctypes.c_uint64 * KVQ_ROPE_MAX_PAIRS)]
 
 
 def header_functions() -> list[str]:
@@ -107,6 +137,12 @@ def _declare(L):
         "kvq_cascade_decode": (i32, [P, P, i32, i32, P, i32, P, i32, i32, f32, P, P, sz, P]),
         "kvq_cascade_decode_step": (i32, [P, P, P, P, i32, i32, P, i32, P, i32, i32, f32, P, P, sz,
                                           P]),
+        "kvq_rope_init": (i32, [ctypes.POINTER(_RopeConfig), ctypes.POINTER(RopePlan)]),
+        "kvq_rope": (i32, [ctypes.POINTER(RopePlan), i32, P, i64, i32, P, i64, i32, i32, P, i64, P, P,
+                           f32, P, i64, P, i64, P]),
+        "kvq_rope_append": (i32, [P, ctypes.POINTER(RopePlan), i32, P, i64, i32, P, i64, P, i64, P,
+                                  P, i64, P, P, f32, P, i64, P]),
+        "kvq_read_values": (i32, [P, P, i64, P, P, P]),
         "kvq_read_slots": (i32, [P, P, i64, P, P, P]),
         "kvq_get_error": (i32, [P, P]),
         "kvq_status_string": (ctypes.c_char_p, [i32]),
@@ -222,6 +258,112 @@ def kvq_append_strided(pool, k, v, slot_mapping, stream=None) -> None:
         raise ValueError("k and v must be equal-shaped views with the same row stride")
     _check(lib().kvq_append_strided(pool, kp, vp, ks, _ptr(slot_mapping, torch.int64, "slot_mapping"),
                                     k.shape[0], _stream(stream)), "kvq_append_strided")
+
+
+def kvq_rope_init(rotary_dim, interleaved=False, scaling=KVQ_ROPE_NONE, base=10000.0, factor=1.0,
+                  orig_len=0.0, low=0.0, high=0.0, magnitude=0.0) -> RopePlan:
+    """A rotation for kvq_rope and kvq_rope_append (kvq_rope_init in include/kvq.h)."""
+    cfg = _RopeConfig(rotary_dim, KVQ_ROPE_INTERLEAVED if interleaved else KVQ_ROPE_HALF, scaling,
+                      base, factor, orig_len, low, high, magnitude)
+    plan = RopePlan()
+    _check(lib().kvq_rope_init(ctypes.byref(cfg), ctypes.byref(plan)), "kvq_rope_init")
+    return plan
+
+
+def _x_rows(t, ref, name):
+    """_rows_view of fp16 or bf16 rows that agree with `ref` in type and tokens."""
+    if t.dtype != ref.dtype or t.shape[0] != ref.shape[0] or t.shape[-1] != ref.shape[-1]:
+        raise ValueError("%s must have the type, tokens and head_dim of the other rows" % name)
+    return _rows_view(t, ref.dtype, name)
+
+
+def _x_type(t, name):
+    import torch
+
+    if t.dtype == torch.float16:
+        return KVQ_X_FP16
+    if t.dtype == torch.bfloat16:
+        return KVQ_X_BF16
+    raise ValueError("%s must be float16 or bfloat16, got %s" % (name, t.dtype))
+
+
+def _weight(w, head_dim, name):
+    import torch
+
+    if w is None:
+        return None
+    if w.numel() != head_dim:
+        raise ValueError("%s must be [head_dim]" % name)
+    return _ptr(w, torch.float32, name)
+
+
+def _positions(plan, positions, T):
+    import torch
+
+    if plan is None:
+        return None, None
+    if positions is None or positions.numel() != T:
+        raise ValueError("positions must be [T]")
+    return ctypes.byref(plan), _ptr(positions, torch.int64, "positions")
+
+
+def kvq_rope(plan, q, k, positions, q_out=None, k_out=None, q_weight=None, k_weight=None, eps=1e-6,
+             stream=None) -> None:
+    """Per-head norm (where a weight is given) and rotation (where a plan is
+    given) of query rows q [T, Hq, D] and key rows k [T, Hk, D], fp16 or bf16,
+    into fp16 rows q_out and k_out (kvq_rope in include/kvq.h).  q or k may be
+    None; fp16 rows without an out are turned in place."""
+    import torch
+
+    ref = q if q is not None else k
+    if ref is None:
+        raise ValueError("q or k must be given")
+    x_type = _x_type(ref, "q" if q is not None else "k")
+    T, _, D = ref.shape
+    args = []
+    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            args.append((None, 0, 0, None, 0))
+            continue
+        xp, xs = _x_rows(x, ref, name)
+        out = x if out is None else out
+        op, os_ = _rows_view(out, torch.float16, name + "_out")
+        if out.shape != x.shape:
+            raise ValueError("%s_out must have the shape of %s" % (name, name))
+        args.append((xp, xs, x.shape[1], op, os_))
+    pl, pos = _positions(plan, positions, T)
+    (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
+    _check(lib().kvq_rope(pl, x_type, qp, qs, hq, kp, ks, hk, D, pos, T,
+                          _weight(q_weight, D, "q_weight"), _weight(k_weight, D, "k_weight"),
+                          float(eps), qo, qos, ko, kos, _stream(stream)), "kvq_rope")
+
+
+def kvq_rope_append(pool, plan, q, k, v, positions, slot_mapping, q_out=None, q_weight=None,
+                    k_weight=None, eps=1e-6, stream=None) -> None:
+    """kvq_rope of q (into fp16 q_out; in place if None) and k, and the append of
+    the rotated k and of v to the pool, in one kernel (kvq_rope_append in
+    include/kvq.h).  q may be None."""
+    import torch
+
+    x_type = _x_type(k, "k")
+    T, _, D = k.shape
+    if v.shape != k.shape or slot_mapping.numel() != T:
+        raise ValueError("k, v must be [T, kv_heads, head_dim] and slot_mapping [T]")
+    kp, ks = _rows_view(k, k.dtype, "k")
+    vp, vs = _x_rows(v, k, "v")
+    qp, qs, hq, qo, qos = None, 0, 0, None, 0
+    if q is not None:
+        qp, qs = _x_rows(q, k, "q")
+        q_out = q if q_out is None else q_out
+        qo, qos = _rows_view(q_out, torch.float16, "q_out")
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        hq = q.shape[1]
+    pl, pos = _positions(plan, positions, T)
+    _check(lib().kvq_rope_append(pool, pl, x_type, qp, qs, hq, kp, ks, vp, vs, pos,
+                                 _ptr(slot_mapping, torch.int64, "slot_mapping"), T,
+                                 _weight(q_weight, D, "q_weight"), _weight(k_weight, D, "k_weight"),
+                                 float(eps), qo, qos, _stream(stream)), "kvq_rope_append")
 
 
 def kvq_paged_decode_strided(pool, q, block_table, context_lens, max_context_len, sm_scale, out,
@@ -408,6 +550,19 @@ def kvq_read_slots(pool, slots, codes_out, scales_out=None, stream=None) -> None
            "kvq_read_slots")
 
 
+def kvq_read_values(pool, slots, k_out, v_out, stream=None) -> None:
+    """Cached K and V of the slots as fp16 values, [n, kv_heads, head_dim] each
+    (kvq_read_values in include/kvq.h)."""
+    import torch
+
+    if k_out.shape != v_out.shape or k_out.shape[0] != slots.numel():
+        raise ValueError("k_out, v_out must be [n, kv_heads, head_dim]")
+    _check(lib().kvq_read_values(pool, _ptr(slots, torch.int64, "slots"), slots.numel(),
+                                 _ptr(k_out, torch.float16, "k_out"),
+                                 _ptr(v_out, torch.float16, "v_out"), _stream(stream)),
+           "kvq_read_values")
+
+
 def kvq_get_error(pool, stream=None) -> int:
     """Synchronises the stream; returns (and clears) the pool's device error status."""
     return int(lib().kvq_get_error(pool, _stream(stream)))
@@ -461,6 +616,17 @@ class KVPool:
     def append(self, k, v, slot_mapping, stream=None):
         kvq_append(self.handle, k, v, slot_mapping, stream)
 
+    def rope_append(self, plan, q, k, v, positions, slot_mapping, q_out=None, q_weight=None,
+                    k_weight=None, eps=1e-6, stream=None):
+        """Rotated (and normed) fp16 queries; keys and values go to the pool."""
+        import torch
+
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+        kvq_rope_append(self.handle, plan, q, k, v, positions, slot_mapping, q_out, q_weight,
+                        k_weight, eps, stream)
+        return q_out
+
     def decode(self, q, block_table, context_lens, max_context_len, sm_scale=None, out=None,
                split_blocks=0, stream=None):
         import torch
@@ -511,7 +677,8 @@ class KVPool:
 
         n = slots.numel()
         cdt = torch.float16 if self.dtype == KVQ_FP16 else (
-            torch.uint8 if self.dtype in (KVQ_FP8_E4M3_PER_TOKEN, KVQ_FP8_E5M2) else torch.int8)
+            torch.uint8 if self.dtype in (KVQ_FP8_E4M3_PER_TOKEN, KVQ_FP8_E5M2,
+                                          KVQ_FP8_E4M3_PER_BLOCK) else torch.int8)
         codes = torch.empty((n, 2, self.kv_heads, self.head_dim), dtype=cdt, device=slots.device)
         scales = None
         if self.dtype in GROUP_FORMATS:
@@ -519,8 +686,19 @@ class KVPool:
                                  dtype=torch.float32, device=slots.device)
         elif self.dtype in (KVQ_INT8_PER_TOKEN, KVQ_FP8_E4M3_PER_TOKEN):
             scales = torch.empty((n, 2), dtype=torch.float32, device=slots.device)
+        elif self.dtype in BLOCK_FORMATS:
+            scales = torch.empty((n, 2, self.kv_heads), dtype=torch.float32, device=slots.device)
         kvq_read_slots(self.handle, slots, codes, scales, stream)
         return codes, scales
+
+    def read_values(self, slots, stream=None):
+        import torch
+
+        k = torch.empty((slots.numel(), self.kv_heads, self.head_dim), dtype=torch.float16,
+                        device=slots.device)
+        v = torch.empty_like(k)
+        kvq_read_values(self.handle, slots, k, v, stream)
+        return k, v
 
     def error(self, stream=None) -> int:
         return kvq_get_error(self.handle, stream)

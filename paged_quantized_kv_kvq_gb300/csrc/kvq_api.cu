@@ -42,7 +42,7 @@ namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-bool valid_dtype(int d) { return d >= KVQ_FP16 && d <= KVQ_FP8_E5M2; }
+bool valid_dtype(int d) { return d >= KVQ_FP16 && d <= KVQ_FP8_E4M3_PER_BLOCK; }
 
 // Geometry check + byte accounting.  Fills `view` offsets relative to base 0.
 kvq_status layout_for(int64_t num_blocks, int bs, int Hkv, int D, int dtype, int group,
@@ -70,7 +70,8 @@ kvq_status layout_for(int64_t num_blocks, int bs, int Hkv, int D, int dtype, int
   // bytes of one 16-token sub-tile of K (or V) codes: INT4 packs two per byte
   const int sub_bytes = dtype == KVQ_INT4_PER_GROUP ? 8 * D : 16 * D * esize;
   const size_t code_bytes = (size_t)bs * sub_bytes / 16;  // K (or V) codes of one page
-  const size_t page_scale = grouped ? 2 * (size_t)bs * ng * 4 : 0;
+  const size_t page_scale = grouped ? 2 * (size_t)bs * ng * 4
+                                     : kvq::fmt_block(dtype) ? kvq::kBlockScaleBytes : 0;
   const size_t page_bytes = 2 * code_bytes + page_scale;
   const size_t n_pages = (size_t)num_blocks * Hkv;
   size_t off = kvq::kHeaderBytes;
@@ -122,6 +123,24 @@ int device_sms() {
 
 kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
+constexpr int kMaxRopeHeads = 1 << 16;
+
+// Checks shared by kvq_rope and kvq_rope_append.
+bool rope_args_ok(const kvq_rope_plan* plan, int x_type, int head_dim, float eps) {
+  if (x_type != KVQ_X_FP16 && x_type != KVQ_X_BF16) return false;
+  if (!(eps >= 0.f)) return false;
+  if (plan == nullptr) return true;
+  return plan->rotary_dim >= 16 && plan->rotary_dim % 16 == 0 && plan->rotary_dim <= head_dim &&
+         (plan->layout == KVQ_ROPE_HALF || plan->layout == KVQ_ROPE_INTERLEAVED);
+}
+
+// [T][heads][head_dim] 16-bit rows that the kernels read or write in 16-byte chunks.
+bool rows_ok(const void* x, int64_t row_stride, int heads, int head_dim) {
+  if (heads == 0) return true;
+  return x != nullptr && (reinterpret_cast<uintptr_t>(x) & 15) == 0 &&
+         row_stride >= (int64_t)heads * head_dim && row_stride % 8 == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -162,10 +181,13 @@ kvq_status kvq_alloc_pool(int64_t num_blocks, int block_size, int kv_heads, int 
     if (buf_bytes < lay.total_bytes || (reinterpret_cast<uintptr_t>(base) & 255) != 0)
       return KVQ_ERR_INVALID_ARG;
   }
-  // Clear the header (error word) and the per-channel scales.
+  // Clear the header (error word), the per-channel scales and the per-block ones.
   cudaError_t e = cudaMemset(base, 0, kvq::kHeaderBytes);
   if (e == cudaSuccess && dtype == KVQ_INT8_PER_CHANNEL)
     e = cudaMemset(static_cast<char*>(base) + oc, 0, 2 * (size_t)kv_heads * head_dim * 4);
+  if (e == cudaSuccess && kvq::fmt_block(dtype))
+    e = cudaMemset2D(static_cast<char*>(base) + op + 2 * (size_t)view.code_bytes, lay.page_bytes, 0,
+                     kvq::kBlockScaleBytes, (size_t)num_blocks * kv_heads);
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     if (owned) cudaFree(base);
@@ -231,6 +253,85 @@ kvq_status kvq_append(kvq_pool* pool, const kvq_half* k, const kvq_half* v,
   if ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) return KVQ_ERR_INVALID_ARG;
   return from_cuda(kvq::launch_append(pool->view, reinterpret_cast<const __half*>(k),
                                       reinterpret_cast<const __half*>(v), slot_mapping, T, stream));
+}
+
+kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
+                    int64_t q_row_stride, int num_q_heads, const void* k, int64_t k_row_stride,
+                    int num_k_heads, int head_dim, const int64_t* positions, int64_t T,
+                    const float* q_weight, const float* k_weight, float eps, kvq_half* q_out,
+                    int64_t q_out_row_stride, kvq_half* k_out, int64_t k_out_row_stride,
+                    cudaStream_t stream) {
+  if (T < 0 || num_q_heads < 0 || num_k_heads < 0 || head_dim < 1) return KVQ_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
+  if (!rope_args_ok(plan, x_type, head_dim, eps)) return KVQ_ERR_INVALID_ARG;
+  if (T == 0 || num_q_heads + (int64_t)num_k_heads == 0) return KVQ_OK;
+  if (plan != nullptr && positions == nullptr) return KVQ_ERR_INVALID_ARG;
+  if (!rows_ok(q, q_row_stride, num_q_heads, head_dim) ||
+      !rows_ok(k, k_row_stride, num_k_heads, head_dim) ||
+      !rows_ok(q_out, q_out_row_stride, num_q_heads, head_dim) ||
+      !rows_ok(k_out, k_out_row_stride, num_k_heads, head_dim))
+    return KVQ_ERR_INVALID_ARG;
+  if (T > 0x7fffffffLL || num_q_heads > kMaxRopeHeads || num_k_heads > kMaxRopeHeads)
+    return KVQ_ERR_UNSUPPORTED;
+  kvq::RopeArgs a;
+  a.x[0] = q;
+  a.x[1] = k;
+  a.x_stride[0] = q_row_stride;
+  a.x_stride[1] = k_row_stride;
+  a.out[0] = reinterpret_cast<__half*>(q_out);
+  a.out[1] = reinterpret_cast<__half*>(k_out);
+  a.out_stride[0] = q_out_row_stride;
+  a.out_stride[1] = k_out_row_stride;
+  a.heads[0] = num_q_heads;
+  a.heads[1] = num_k_heads;
+  a.weight[0] = q_weight;
+  a.weight[1] = k_weight;
+  a.bf16 = x_type == KVQ_X_BF16;
+  a.positions = positions;
+  a.T = T;
+  a.D = head_dim;
+  a.eps = eps;
+  a.plan = plan;
+  return from_cuda(kvq::launch_rope(a, stream));
+}
+
+kvq_status kvq_rope_append(kvq_pool* pool, const kvq_rope_plan* plan, kvq_x_type x_type,
+                           const void* q, int64_t q_row_stride, int num_q_heads, const void* k,
+                           int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                           const int64_t* positions, const int64_t* slot_mapping, int64_t T,
+                           const float* q_weight, const float* k_weight, float eps,
+                           kvq_half* q_out, int64_t q_out_row_stride, cudaStream_t stream) {
+  if (pool == nullptr || T < 0 || num_q_heads < 0) return KVQ_ERR_INVALID_ARG;
+  const int D = pool->view.D, Hkv = pool->view.Hkv;
+  if (!rope_args_ok(plan, x_type, D, eps)) return KVQ_ERR_INVALID_ARG;
+  if (T == 0) return KVQ_OK;
+  if (slot_mapping == nullptr || (plan != nullptr && positions == nullptr))
+    return KVQ_ERR_INVALID_ARG;
+  if (!rows_ok(q, q_row_stride, num_q_heads, D) || !rows_ok(k, k_row_stride, Hkv, D) ||
+      !rows_ok(v, v_row_stride, Hkv, D) || !rows_ok(q_out, q_out_row_stride, num_q_heads, D))
+    return KVQ_ERR_INVALID_ARG;
+  if (T > 0x7fffffffLL || num_q_heads > kMaxRopeHeads) return KVQ_ERR_UNSUPPORTED;
+  kvq::IngestArgs a;
+  a.pool = pool->view;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_row_stride;
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.bf16 = x_type == KVQ_X_BF16;
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.T = T;
+  a.Hq = num_q_heads;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.eps = eps;
+  a.q_out = reinterpret_cast<__half*>(q_out);
+  a.q_out_stride = q_out_row_stride;
+  a.plan = plan;
+  const cudaError_t e = kvq::launch_ingest(a, stream, /*dependent=*/false);
+  return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
 }
 
 kvq_status kvq_copy_blocks(kvq_pool* pool, const int32_t* src_blocks, const int32_t* dst_blocks,
@@ -561,9 +662,24 @@ kvq_status kvq_read_slots(const kvq_pool* pool, const int64_t* slots, int64_t n,
   if (slots == nullptr || codes_out == nullptr || n > 0x7fffffffLL) return KVQ_ERR_INVALID_ARG;
   const int f = pool->view.fmt;
   const bool has_scales = f == KVQ_INT8_PER_GROUP || f == KVQ_INT4_PER_GROUP ||
-                          f == KVQ_INT8_PER_TOKEN || f == KVQ_FP8_E4M3_PER_TOKEN;
+                          f == KVQ_INT8_PER_TOKEN || f == KVQ_FP8_E4M3_PER_TOKEN ||
+                          kvq::fmt_block(f);
   return from_cuda(kvq::launch_read_slots(pool->view, slots, n, codes_out,
                                           has_scales ? scales_out : nullptr, stream));
+}
+
+kvq_status kvq_read_values(const kvq_pool* pool, const int64_t* slots, int64_t n, kvq_half* k_out,
+                           kvq_half* v_out, cudaStream_t stream) {
+  if (pool == nullptr || n < 0) return KVQ_ERR_INVALID_ARG;
+  if (n == 0) return KVQ_OK;
+  if (slots == nullptr || k_out == nullptr || v_out == nullptr || n > 0x7fffffffLL)
+    return KVQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 15)
+    return KVQ_ERR_INVALID_ARG;
+  const cudaError_t e = kvq::launch_read_values(pool->view, slots, n,
+                                                reinterpret_cast<__half*>(k_out),
+                                                reinterpret_cast<__half*>(v_out), stream);
+  return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
 }
 
 kvq_status kvq_get_error(kvq_pool* pool, cudaStream_t stream) {

@@ -18,6 +18,7 @@
 #include "kvq_common.cuh"
 #include "kvq_context.h"
 #include "kvq_internal.h"
+#include "kvq_quant.cuh"
 
 namespace kvq {
 
@@ -35,45 +36,6 @@ struct AppendParams {
   int max_blocks, max_ctx;
   int64_t x_stride;  // elements between consecutive tokens of k and v
 };
-
-__device__ __forceinline__ float absmax8(const __half2 (&x)[4]) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    a = fmaxf(a, fabsf(__low2float(x[i])));
-    a = fmaxf(a, fabsf(__high2float(x[i])));
-  }
-  return a;
-}
-
-// INT8 code, returned biased (c + 128) as stored in the pool.
-__device__ __forceinline__ uint8_t quant_i8(float x, float s) {
-  if (s == 0.f) return static_cast<uint8_t>(kInt8Bias);
-  float q = rintf(__fdiv_rn(x, s));
-  q = fminf(fmaxf(q, -127.f), 127.f);
-  return static_cast<uint8_t>(static_cast<int>(q) + 128);
-}
-
-// INT4 code, returned biased (c + 8) as stored in the pool.
-__device__ __forceinline__ uint32_t quant_i4(float x, float s) {
-  if (s == 0.f) return kInt4Bias;
-  float q = rintf(__fdiv_rn(x, s));
-  q = fminf(fmaxf(q, -7.f), 7.f);
-  return static_cast<uint32_t>(static_cast<int>(q) + 8);
-}
-
-// Replace the nibbles under `mask` of a shared 32-bit word: other tokens own
-// the word's other nibbles and may be written by other CTAs at the same time.
-__device__ __forceinline__ void store_nibbles(char* word, uint32_t mask, uint32_t val) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(word);
-  atomicAnd(w, ~mask);
-  atomicOr(w, val);
-}
-
-__device__ __forceinline__ uint8_t quant_e4m3(float x, float s) {
-  if (s == 0.f) return 0;
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(__fdiv_rn(x, s), __NV_SATFINITE, __NV_E4M3));
-}
 
 // One CTA per (token, K|V).  Each thread owns 8 consecutive channels of one
 // kv head per iteration (a 16-byte load).
@@ -304,7 +266,7 @@ __global__ void kvq_read_slots_kernel(PoolView pool, const int64_t* slots, int64
     else  // INT8 codes are stored biased; hand back the signed code
       reinterpret_cast<uint8_t*>(codes_out)[dst] =
           *reinterpret_cast<const uint8_t*>(tile + o) ^
-          (pool.fmt == FMT_FP8_TOKEN || pool.fmt == FMT_FP8_E5M2 ? 0u : kInt8Bias);
+          (fmt_e4m3(pool.fmt) || pool.fmt == FMT_FP8_E5M2 ? 0u : kInt8Bias);
   }
   if (scales_out == nullptr) return;
   if (pool.fmt == FMT_INT8_GROUP || pool.fmt == FMT_INT4_GROUP) {
@@ -314,6 +276,12 @@ __global__ void kvq_read_slots_kernel(PoolView pool, const int64_t* slots, int64
       const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
       const float* sc = reinterpret_cast<const float*>(page + 2 * pool.code_bytes);
       scales_out[(i * 2 + kv) * ns + c] = sc[(kv * pool.bs + off) * pool.ng + gi];
+    }
+  } else if (fmt_block(pool.fmt)) {  // the scale of the slot's block, per head
+    for (int h = threadIdx.x; h < pool.Hkv; h += blockDim.x) {
+      const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
+      scales_out[(i * 2 + kv) * pool.Hkv + h] =
+          reinterpret_cast<const float*>(page + 2 * pool.code_bytes)[kv];
     }
   } else if (pool.fmt == FMT_INT8_TOKEN || pool.fmt == FMT_FP8_TOKEN) {
     if (threadIdx.x == 0) scales_out[i * 2 + kv] = pool.tok_scales[(blk * 2 + kv) * pool.bs + off];
@@ -375,6 +343,20 @@ cudaError_t launch_step_append(const PoolView& pool, const __half* k, const __ha
                                int max_blocks, int max_ctx, cudaStream_t st, bool dependent,
                                int64_t x_stride) {
   if (T == 0) return cudaSuccess;
+  if (fmt_block(pool.fmt)) {  // a block's tokens are quantized together
+    IngestArgs a;
+    a.pool = pool;
+    a.k = k;
+    a.v = v;
+    a.k_stride = a.v_stride = x_stride > 0 ? x_stride : (int64_t)pool.Hkv * pool.D;
+    a.slots = slots;
+    a.table = table;
+    a.lens = lens;
+    a.max_blocks = max_blocks;
+    a.max_ctx = max_ctx;
+    a.T = T;
+    return launch_ingest(a, st, dependent);
+  }
   AppendParams p{pool, k, v, slots, T, table, lens, max_blocks, max_ctx,
                  x_stride > 0 ? x_stride : (int64_t)pool.Hkv * pool.D};
   dim3 grid(static_cast<unsigned>(T), 2);

@@ -16,6 +16,7 @@
 //                   V codes : block_size/16 sub-tiles
 //                   K scales: [block_size][D/group] fp32   (per-group only)
 //                   V scales: [block_size][D/group] fp32   (per-group only)
+//                   K scale, V scale fp32, 8 B padding     (per-block only)
 //   token scales: [num_blocks][2][block_size] fp32         (per-token only)
 //   chan scales : [2][kv_heads][D] fp32                    (per-channel only)
 //
@@ -43,6 +44,8 @@ enum Fmt : int {
   FMT_FP8_TOKEN = 4,
   FMT_INT4_GROUP = 5,
   FMT_FP8_E5M2 = 6,
+  FMT_INT8_BLOCK = 7,
+  FMT_FP8_BLOCK = 8,
 };
 
 enum ErrBits : int {
@@ -53,6 +56,15 @@ enum ErrBits : int {
 constexpr int kHeaderBytes = 256;
 constexpr int kWaitTries = 4000;  // bound of a pipeline wait: tries of <= 1 ms each, ~4 s
 constexpr int kMaxDevicesApi = 64;
+
+// Formats with one K and one V scale per (block, kv head), behind its codes.
+__host__ __device__ constexpr bool fmt_block(int fmt) {
+  return fmt == FMT_INT8_BLOCK || fmt == FMT_FP8_BLOCK;
+}
+__host__ __device__ constexpr bool fmt_e4m3(int fmt) {
+  return fmt == FMT_FP8_TOKEN || fmt == FMT_FP8_BLOCK;
+}
+constexpr int kBlockScaleBytes = 16;  // the two scales, padded so that pages stay 16-byte aligned
 
 __host__ __device__ constexpr int fmt_esize(int fmt) { return fmt == FMT_FP16 ? 2 : 1; }
 
@@ -132,7 +144,7 @@ struct PoolView {
   int sub_bytes;    // bytes of one 16-token sub-tile: 16 * D * esize (INT4: 8 * D)
   int code_bytes;   // bytes of K (or V) codes in one page = bs * sub_bytes / 16
                     // (block size 8: half a sub-tile)
-  int page_bytes;   // 2*code_bytes + (per-group) 2*bs*ng*4
+  int page_bytes;   // 2*code_bytes + (per-group) 2*bs*ng*4 or (per-block) 16
 };
 
 __device__ __forceinline__ void set_error(int* err, int bits) { atomicOr(err, bits); }

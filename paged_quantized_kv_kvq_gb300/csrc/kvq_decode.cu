@@ -116,6 +116,7 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
   l.smem = plan.smem_bytes;
   l.st = st;
   l.dependent = dependent;
+  if (fmt_block(a.pool.fmt)) return launch_decode_block(l);
   if (a.pool.bs == 8)
     return a.pool.fmt == FMT_INT8_GROUP ? launch_decode_bs8_group(l) : launch_decode_bs8_misc(l);
   switch (a.pool.fmt) {

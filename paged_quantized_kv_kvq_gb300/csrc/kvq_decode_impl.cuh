@@ -116,9 +116,10 @@ struct FmtTraits {
   static constexpr bool one_byte = FMT != FMT_FP16;
   static constexpr bool group_scales = FMT == FMT_INT8_GROUP || FMT == FMT_INT4_GROUP;
   static constexpr bool token_scales = FMT == FMT_INT8_TOKEN || FMT == FMT_FP8_TOKEN;
-  static constexpr bool row_scales = group_scales || token_scales;  // per-(token[,group]) K/V scales
+  static constexpr bool block_scales = fmt_block(FMT);  // one K and one V scale per page
+  static constexpr bool row_scales = group_scales || token_scales || block_scales;  // K/V scales beside the codes
   static constexpr bool channel = FMT == FMT_INT8_CHANNEL;
-  static constexpr bool maybe_nan = FMT == FMT_FP16 || FMT == FMT_FP8_TOKEN || FMT == FMT_FP8_E5M2;
+  static constexpr bool maybe_nan = FMT == FMT_FP16 || fmt_e4m3(FMT) || FMT == FMT_FP8_E5M2;
 };
 
 // 32-bit words a lane holds of one 16-token sub-tile of K (or V).
@@ -133,7 +134,7 @@ __device__ __forceinline__ void word_to_h2(const uint32_t* words, int w, uint32_
   if constexpr (FMT == FMT_FP16) {
     lo = words[2 * w];
     hi = words[2 * w + 1];
-  } else if constexpr (FMT == FMT_FP8_TOKEN) {
+  } else if constexpr (fmt_e4m3(FMT)) {
     e4m3x4_to_h2x2(words[w], lo, hi);
   } else if constexpr (FMT == FMT_FP8_E5M2) {
     e5m2x4_to_h2x2(words[w], lo, hi);
@@ -257,7 +258,13 @@ __device__ __forceinline__ void load_tile(PairRegs<FMT, D, NG>& r, int t, const 
   const int g = lane >> 2;
   load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, r.kw[t]);
   r.vtile[t] = stage + pool.code_bytes + sub * pool.sub_bytes;
-  if constexpr (T::row_scales) {
+  if constexpr (T::block_scales) {
+    const float2 sc = *reinterpret_cast<const float2*>(stage + 2 * pool.code_bytes);
+    r.ks[t][0][0] = r.ks[t][1][0] = sc.x;
+    // an empty tile may read a stage that no copy has filled: its products are
+    // zero, and so must be what multiplies them
+    r.vs[t][0][0] = r.vs[t][1][0] = rows > 0 ? sc.y : 0.f;
+  } else if constexpr (T::row_scales) {
     const float* ks;
     const float* vs;
     if constexpr (T::group_scales) {
@@ -298,7 +305,15 @@ __device__ __forceinline__ void load_tile8(PairRegs<FMT, D, NG>& r, int t, const
   }
   r.vtile[t] = A + pool.code_bytes;
   r.vtile_b[t] = B != nullptr ? B + pool.code_bytes : nullptr;
-  if constexpr (T::row_scales) {
+  if constexpr (T::block_scales) {
+    const float2 a = *reinterpret_cast<const float2*>(A + 2 * pool.code_bytes);
+    const float2 b = B != nullptr ? *reinterpret_cast<const float2*>(B + 2 * pool.code_bytes)
+                                  : make_float2(0.f, 0.f);
+    r.ks[t][0][0] = a.x;
+    r.ks[t][1][0] = b.x;
+    r.vs[t][0][0] = a.y;
+    r.vs[t][1][0] = b.y;
+  } else if constexpr (T::row_scales) {
     // scales of token g of each page: [bs][NS] per group, [2][bs] per token
     const int ko = T::group_scales ? 2 * pool.code_bytes : pool.page_bytes;
     const int vo = T::group_scales ? 8 * NG * 4 : 8 * 4;
@@ -329,6 +344,18 @@ __device__ __forceinline__ void load_tile8(PairRegs<FMT, D, NG>& r, int t, const
 // heads of a unit.  Lane (g = lane/4, j = lane%4) holds the scores of tokens g
 // and g+8 of each tile for heads 2j and 2j+1, and O^T rows 16mt+g, 16mt+g+8
 // for the same two heads.  Tile 1 may be empty (rows = 0).
+//
+// One scale per block (16-token pages and larger): a tile has one V scale, so
+// the weights enter P.V without it (E stays 14) and the tile's product, summed
+// from zero, is added to O times that scale in fp32.  That is one multiply-add
+// per output instead of a multiply per weight, and O never passes through the
+// tensor core's accumulator, whose truncated sums drift with the tokens of a
+// range (3e-5 at 2048 tokens).  Two 8-token pages in a tile have two scales:
+// there they are folded into the weights as for the other formats.
+template <int FMT, bool BS8>
+constexpr bool tile_scale() {
+  return fmt_block(FMT) && !BS8;
+}
 template <int FMT, int D, int NG, bool BS8 = false>
 __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
                                              const uint32_t (&qb)[D / 16][2],
@@ -408,7 +435,7 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
       pr[t][3] = fast_exp2(z[t][3] - ms1);
     }
     int dE = 0;
-    if constexpr (T::row_scales) {
+    if constexpr (T::row_scales && !tile_scale<FMT, BS8>()) {
       float vmax = 0.f;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -454,7 +481,7 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
 #pragma unroll
       for (int gi = 0; gi < NB; ++gi) {
         float fA = sc, fB = sc;
-        if constexpr (T::row_scales) {
+        if constexpr (T::row_scales && !tile_scale<FMT, BS8>()) {
           fA *= r.vs[t][0][gi];
           fB *= r.vs[t][1][gi];
         }
@@ -544,8 +571,17 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
           v_frag8<FMT>(vwp[t], mt, a0, a1, a2, a3);
         else
           v_frag<FMT>(vwp[t], mt, a0, a1, a2, a3);
-        mma_16816(o[mt], a0, a1, a2, a3, bh0[t][gi], bh1[t][gi]);
-        mma_16816(o[mt], a0, a1, a2, a3, bl0[t][gi], bl1[t][gi]);
+        if constexpr (T::block_scales) {
+          float c[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_16816(c, a0, a1, a2, a3, bh0[t][gi], bh1[t][gi]);
+          mma_16816(c, a0, a1, a2, a3, bl0[t][gi], bl1[t][gi]);
+          const float s = tile_scale<FMT, BS8>() ? r.vs[t][0][0] : 1.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[mt][e] = fmaf(c[e], s, o[mt][e]);
+        } else {
+          mma_16816(o[mt], a0, a1, a2, a3, bh0[t][gi], bh1[t][gi]);
+          mma_16816(o[mt], a0, a1, a2, a3, bl0[t][gi], bl1[t][gi]);
+        }
       }
     }
   }
@@ -894,7 +930,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
     load_q<FMT, D>(p, cc.s, cc.lu / p.n_ht, cc.lu % p.n_ht, lane, qb, ql, csc);
     m[0] = m[1] = kNegInf;
     l[0] = l[1] = 0.f;
-    E = T::row_scales ? 100 : 14;
+    E = T::row_scales && !tile_scale<FMT, BS8>() ? 100 : 14;
 #pragma unroll
     for (int mt = 0; mt < KS; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
     seg_pi0 = cc.pi;

@@ -1,0 +1,431 @@
+// kvq_ingest_impl.cuh -- new tokens into the cache in one kernel: query rows
+// normed and rotated to fp16; key rows normed, rotated and quantized straight
+// from fp32; value rows quantized; keys and values stored in their slots.
+//
+// A CTA either turns query rows (kvq_rope_math.cuh) or takes runs of tokens: a
+// run is a maximal stretch of the call's tokens whose slots lie in one block,
+// and the CTA that owns its first token quantizes and stores the whole run,
+// K or V, for `hpc` kv heads.  So
+//  * the one scale of a (block, head) is an absmax inside one CTA, with no
+//    atomics and no second kernel, whatever number of tokens the call brings;
+//  * a 16-token sub-tile that the run covers is assembled in shared memory and
+//    leaves as 16-byte stores, although its bytes interleave tokens.
+// Bounds: HBM for prompts (fp16 rows in, codes out), latency for a decode step
+// (one token per run: slot -> rows -> absmax -> codes).
+//
+// One scale per (block, head): s = max(s_old, absmax / top) in fp32, where top
+// is 127 or 448 and s_old the block's scale, unless the run writes offset 0,
+// which starts the block anew.  Where s grew, the codes the block keeps are
+// rounded again: code' = rne(code * s_old / s).
+#pragma once
+#include <cstdint>
+
+#include "kvq_context.h"
+#include "kvq_internal.h"
+#include "kvq_quant.cuh"
+#include "kvq_rope_math.cuh"
+
+namespace kvq {
+
+constexpr int kIngestThreads = 128;
+constexpr int kIngestWarps = kIngestThreads / 32;
+constexpr int kMaxBlock = 64;  // largest block size
+
+struct IngestParams {
+  PoolView pool;
+  RopeRows q;
+  int Hq;
+  const void* x[2];     // k, v
+  int64_t stride[2];
+  const float* k_weight;
+  const int64_t* positions;
+  const int64_t* slots;  // null: the decode-step form, from table and lens
+  const int* table;
+  const int* lens;
+  int max_blocks, max_ctx;
+  int64_t T;
+  float eps;
+  bool bf16;
+  int bs_log2;
+  int tpc, hpc, hsplit;  // tokens and heads per K/V CTA, CTAs over the heads
+  int64_t kv_ctas;       // CTAs 0 .. kv_ctas-1 take K/V, the rest query rows
+  int q_tpc, q_parts;
+  kvq_rope_plan plan;
+};
+
+// Shared memory of a K/V CTA; `tile` and `cs` follow it.
+struct IngestShared {
+  int blk[2 * kMaxBlock + 1];  // block of window token i - 1 (-1: none)
+  uint8_t off[2 * kMaxBlock];  // its offset in the block
+  uint32_t cut[4];             // bit i: token i begins a new block
+  uint32_t has[2];             // offsets the run writes
+  float red[kIngestWarps];
+  uint32_t tok[kMaxBlock];     // per-token absmax, as bits
+};
+
+// Slot of token t, or -1 (nothing to store).
+__device__ __forceinline__ int64_t ingest_slot(const IngestParams& p, int64_t t) {
+  if (p.slots != nullptr) return p.slots[t];
+  const int L = p.lens[t];  // the decode flags a length beyond max_ctx; nothing is stored
+  if (L <= 0 || L > p.max_ctx) return -1;
+  const int b = p.table[t * p.max_blocks + ((L - 1) >> p.bs_log2)];
+  return b < 0 ? p.pool.num_blocks * p.pool.bs
+               : ((int64_t)b << p.bs_log2) + ((L - 1) & (p.pool.bs - 1));
+}
+
+// Store 8 codes of channels d0 .. d0+7 of token offset `off` into K (or V)
+// codes at `base` (a page's, or its image in shared memory).
+__device__ __forceinline__ void store_codes8(char* base, int kv, int off, int d0, int D, int bs,
+                                             int sub_bytes, const uint8_t (&c)[8]) {
+  char* tile = base + (off >> 4) * sub_bytes;
+  const int tt = off & 15;
+  if (kv == 0) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<uint32_t*>(tile + k_tile_offset(tt, d0 + 4 * h, D, 1)) =
+          c[4 * h] | (c[4 * h + 1] << 8) | (c[4 * h + 2] << 16) | ((uint32_t)c[4 * h + 3] << 24);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      tile[v_code_offset(tt, d0 + i, D, 1, bs)] = static_cast<char>(c[i]);
+  }
+}
+
+template <int FMT>
+__device__ __forceinline__ uint8_t quant_byte(float x, float s) {
+  if constexpr (fmt_e4m3(FMT))
+    return quant_e4m3(x, s);
+  else if constexpr (FMT == FMT_FP8_E5M2)
+    return static_cast<uint8_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E5M2));
+  else
+    return quant_i8(x, s);
+}
+
+template <int FMT>
+__device__ __forceinline__ float code_value(uint8_t c) {
+  if constexpr (fmt_e4m3(FMT))
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+  else
+    return static_cast<float>(static_cast<int>(c) - 128);
+}
+
+// One run: tokens t0 .. t0+n-1 of the call (window indices w0 ..), block blk.
+template <int FMT, int D, int CPT>
+__device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& sh, char* tile,
+                                           float2* cs, int64_t t0, int n, int w0, int64_t blk,
+                                           int h0, int h1, int kv) {
+  constexpr int LPH = D / 8, RPP = kIngestThreads / LPH;
+  constexpr bool kBlock = fmt_block(FMT);
+  constexpr bool kToken = FMT == FMT_INT8_TOKEN || FMT == FMT_FP8_TOKEN;
+  constexpr float kTop = fmt_e4m3(FMT) ? 448.f : FMT == FMT_INT4_GROUP ? 7.f : 127.f;
+  constexpr int ES = FMT == FMT_FP16 ? 2 : 1;
+  const PoolView& pool = p.pool;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ci = tid % LPH, r0 = tid / LPH, d0 = 8 * ci;
+  const int bs = pool.bs;
+  const int r = p.plan.rotary_dim, rp = r >> 1;
+  const bool turn = kv == 0 && r > 0, norm = kv == 0 && p.k_weight != nullptr;
+
+  if (tid < 2) sh.has[tid] = 0;
+  if (kToken && tid < kMaxBlock) sh.tok[tid] = 0;
+  __syncthreads();
+  if (tid < n) {
+    const int off = sh.off[w0 + tid];
+    atomicOr(&sh.has[off >> 5], 1u << (off & 31));
+  }
+  if (turn)
+    for (int i = tid; i < n * rp; i += kIngestThreads)
+      cs[i] = rope_cs(p.plan.turns[i % rp], p.positions[t0 + i / rp], p.plan.magnitude);
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = norm ? p.k_weight[d0 + i] : 1.f;
+  __syncthreads();
+  const uint64_t has = (uint64_t)sh.has[1] << 32 | sh.has[0];
+  const bool fresh = has & 1;
+  // sub-tiles (8-token pages: the page) whose every token the run writes
+  auto covered = [&](int off) {
+    const uint64_t m = bs == 8 ? 0xFFull : 0xFFFFull;
+    return (~has >> (off & ~15) & m) == 0;
+  };
+
+  float x[CPT][8];
+  int off[CPT];
+  auto load_head = [&](int h) {  // rows of head h, normed and rotated
+    uint4 raw[CPT];
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      const int row = c * RPP + r0;
+      off[c] = row < n ? sh.off[w0 + row] : -1;
+      raw[c] = row < n ? *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.x[kv]) +
+                                                         (t0 + row) * p.stride[kv] + h * D + d0)
+                       : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      widen8(raw[c], p.bf16, x[c]);
+      if (norm) norm8<D>(x[c], w, p.eps);
+      if (turn)
+        rotate8<D>(x[c], ci, r, p.plan.layout == KVQ_ROPE_INTERLEAVED,
+                   cs + min(c * RPP + r0, n - 1) * rp);
+    }
+  };
+  auto absmax = [&](const float (&v)[8]) {
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(v[i]));
+    return a;
+  };
+
+  if constexpr (kToken) {  // the scale of a token spans every head: a first pass over them
+    for (int h = 0; h < pool.Hkv; ++h) {
+      load_head(h);
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        float a = absmax(x[c]);
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        if (ci == 0 && off[c] >= 0) atomicMax(&sh.tok[c * RPP + r0], __float_as_uint(a));
+      }
+    }
+    __syncthreads();
+    if (tid < n)
+      pool.tok_scales[(blk * 2 + kv) * bs + sh.off[w0 + tid]] =
+          __fdiv_rn(__uint_as_float(sh.tok[tid]), kTop);
+  }
+
+  for (int h = h0; h < h1; ++h) {
+    char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
+    char* codes = page + (kv == 0 ? 0 : pool.code_bytes);
+    float* scales = reinterpret_cast<float*>(page + 2 * pool.code_bytes);
+    load_head(h);
+    float s_block = 0.f;
+    if constexpr (kBlock) {
+      float a = 0.f;
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) a = fmaxf(a, absmax(x[c]));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+      const float s_old = fresh ? 0.f : scales[kv];
+      if (lane == 0) sh.red[warp] = a;
+      __syncthreads();  // (also: the previous head's tile has left)
+      a = sh.red[0];
+#pragma unroll
+      for (int i = 1; i < kIngestWarps; ++i) a = fmaxf(a, sh.red[i]);
+      s_block = fmaxf(s_old, __fdiv_rn(a, kTop));
+      // the codes the block keeps
+      const uint32_t zero = fmt_e4m3(FMT) ? 0u : 0x80808080u;
+      for (int i = tid; i < pool.code_bytes / 4; i += kIngestThreads) {
+        uint32_t v = fresh ? zero : reinterpret_cast<const uint32_t*>(codes)[i];
+        if (!fresh && s_block > s_old) {
+          uint32_t out = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            out |= (uint32_t)quant_byte<FMT>(code_value<FMT>(v >> (8 * e) & 0xFF) * s_old, s_block)
+                   << (8 * e);
+          v = out;
+        }
+        reinterpret_cast<uint32_t*>(tile)[i] = v;
+      }
+      if (tid == 0) scales[kv] = s_block;
+    } else if constexpr (FMT == FMT_INT4_GROUP) {
+      __syncthreads();
+      for (int i = tid; i < pool.code_bytes / 4; i += kIngestThreads)
+        reinterpret_cast<uint32_t*>(tile)[i] = 0;
+    }
+    __syncthreads();
+
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      const bool act = off[c] >= 0;
+      const bool staged = kBlock || (act && covered(off[c]));
+      char* dst = staged ? tile : codes;
+      if constexpr (FMT == FMT_FP16) {
+        if (!act) continue;
+        const uint4 o = narrow8(x[c]);
+        char* t = dst + (off[c] >> 4) * pool.sub_bytes;
+        const int tt = off[c] & 15;
+        if (kv == 0) {
+          *reinterpret_cast<uint2*>(t + k_tile_offset(tt, d0, D, 2)) = make_uint2(o.x, o.y);
+          *reinterpret_cast<uint2*>(t + k_tile_offset(tt, d0 + 4, D, 2)) = make_uint2(o.z, o.w);
+        } else {
+          const uint16_t* hb = reinterpret_cast<const uint16_t*>(&o);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint16_t*>(t + v_code_offset(tt, d0 + i, D, 2, bs)) = hb[i];
+        }
+        continue;
+      }
+      float s = 0.f;
+      if constexpr (FMT == FMT_INT8_GROUP || FMT == FMT_INT4_GROUP) {
+        // a group is group/8 consecutive lanes
+        float a = absmax(x[c]);
+        for (int o = pool.group >> 4; o > 0; o >>= 1)
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        s = __fdiv_rn(a, kTop);
+        if (act && d0 % pool.group == 0)
+          scales[(kv * bs + off[c]) * pool.ng + d0 / pool.group] = s;
+      } else if constexpr (kToken) {
+        s = act ? __fdiv_rn(__uint_as_float(sh.tok[c * RPP + r0]), kTop) : 0.f;
+      } else if constexpr (kBlock) {
+        s = s_block;
+      }
+      if (!act) continue;
+      if constexpr (FMT == FMT_INT4_GROUP) {
+        char* t = dst + (off[c] >> 4) * pool.sub_bytes;
+        const int tt = off[c] & 15;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          int sh4;
+          const int o = kv == 0 ? k_nibble(tt, d0 + i, sh4) : v_nibble(tt, d0 + i, sh4);
+          const uint32_t val = quant_i4(x[c][i], s) << sh4;
+          if (staged)
+            atomicOr(reinterpret_cast<uint32_t*>(t + o), val);
+          else
+            store_nibbles(t + o, 0xFu << sh4, val);
+        }
+      } else {
+        uint8_t q[8];
+        if constexpr (FMT == FMT_INT8_CHANNEL) {
+          const float* chs = pool.chan_scales + ((int64_t)kv * pool.Hkv + h) * D + d0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[i] = quant_byte<FMT>(x[c][i], chs[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) q[i] = quant_byte<FMT>(x[c][i], s);
+        }
+        store_codes8(dst, kv, off[c], d0, D, bs, pool.sub_bytes, q);
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < pool.code_bytes / 16; i += kIngestThreads) {
+      const int sub = i * 16 / pool.sub_bytes;
+      if (kBlock || covered(16 * sub))
+        reinterpret_cast<uint4*>(codes)[i] = reinterpret_cast<const uint4*>(tile)[i];
+    }
+    if constexpr (!kBlock) __syncthreads();
+  }
+  if constexpr (kBlock) __syncthreads();
+  (void)ES;
+}
+
+template <int FMT, int D, int CPT>
+__global__ void __launch_bounds__(kIngestThreads) kvq_ingest_kernel(const __grid_constant__ IngestParams p) {
+  extern __shared__ __align__(16) char smem[];
+  // The decode-step form launches as a programmatic dependent: wait for what
+  // ran before, then let the decode launch (see kvq_append_kernel).
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x >= p.kv_ctas) {
+    const int64_t b = blockIdx.x - p.kv_ctas;
+    const int64_t t0 = b / p.q_parts * p.q_tpc;
+    rope_tokens<D, kIngestThreads>(p.q, p.Hq, RopeRows{}, 0, p.bf16, p.positions, t0,
+                                   static_cast<int>(min((int64_t)p.q_tpc, p.T - t0)),
+                                   static_cast<int>(b % p.q_parts), p.q_parts, p.eps, p.plan,
+                                   reinterpret_cast<float2*>(smem));
+    return;
+  }
+  __shared__ IngestShared sh;
+  const PoolView& pool = p.pool;
+  const int kv = static_cast<int>(blockIdx.x & 1);
+  const int64_t b = blockIdx.x >> 1;
+  const int h0 = static_cast<int>(b % p.hsplit) * p.hpc;
+  const int64_t c0 = b / p.hsplit * p.tpc;
+  // Window of tokens c0 .. c0+tpc+bs-1: the runs that begin among the first tpc
+  // and, for the last of them, as far as a run can go.
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int win = static_cast<int>(min((int64_t)p.tpc + pool.bs, p.T - c0));
+  for (int i = tid; i <= win; i += kIngestThreads) {
+    const int64_t t = c0 + i - 1;
+    int blk = -1;
+    if (t >= 0) {
+      const int64_t slot = ingest_slot(p, t);
+      if (slot >= pool.num_blocks * pool.bs) {
+        if (i > 0 && i <= p.tpc && h0 == 0) set_error(pool.err, ERR_RANGE);
+      } else if (slot >= 0) {
+        blk = static_cast<int>(slot >> p.bs_log2);
+        if (i > 0) sh.off[i - 1] = static_cast<uint8_t>(slot & (pool.bs - 1));
+      }
+    }
+    sh.blk[i] = blk;
+  }
+  __syncthreads();
+  {
+    // the step form's tokens are of different sequences: each is a run
+    const bool cut = tid >= win || sh.blk[tid] != sh.blk[tid + 1] || p.slots == nullptr;
+    const uint32_t m = __ballot_sync(0xffffffffu, cut);
+    if (lane == 0) sh.cut[tid >> 5] = m;
+  }
+  __syncthreads();
+  char* tile = smem;
+  float2* cs = reinterpret_cast<float2*>(smem + pool.code_bytes);
+  const int h1 = min(h0 + p.hpc, pool.Hkv);
+  const int nown = min(p.tpc, win);
+  for (int i = 0; i < nown;) {
+    if (!(sh.cut[i >> 5] >> (i & 31) & 1)) {  // belongs to a run of an earlier CTA
+      ++i;
+      continue;
+    }
+    int e = i + 1;
+    while (e < win && e < i + pool.bs && !(sh.cut[e >> 5] >> (e & 31) & 1)) ++e;
+    const int blk = sh.blk[i + 1];
+    if (blk >= 0)
+      ingest_run<FMT, D, CPT>(p, sh, tile, cs, c0 + i, e - i, i, blk, h0, h1, kv);
+    i = e;
+  }
+}
+
+// Shared memory of a launch: the tile image and the run's cosines and sines (the
+// query CTAs use kRopeTokens tokens' worth).
+inline int ingest_smem(const PoolView& pool, int rotary_dim) {
+  const int kv = pool.code_bytes + pool.bs * rotary_dim / 2 * 8;
+  const int q = kRopeTokens * rotary_dim / 2 * 8;
+  return kv > q ? kv : q;
+}
+
+struct IngestLaunch {
+  IngestParams p;
+  unsigned grid;
+  int smem;
+  cudaStream_t st;
+  bool dependent;
+};
+
+template <int FMT, int D, int CPT>
+cudaError_t run_ingest_c(const IngestLaunch& l) {
+  if (l.smem > 48 * 1024) {
+    const cudaError_t e = allow_big_smem<kvq_ingest_kernel<FMT, D, CPT>>();
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(l.grid);
+  cfg.blockDim = dim3(kIngestThreads);
+  cfg.dynamicSmemBytes = l.smem;
+  cfg.stream = l.st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = l.dependent ? 1 : 0;
+  return phase_mark(l.st, cudaLaunchKernelEx(&cfg, kvq_ingest_kernel<FMT, D, CPT>, l.p));
+}
+
+// CPT: 16-byte chunks of a whole block's rows of one head per thread.
+template <int FMT>
+cudaError_t run_ingest(const IngestLaunch& l) {
+  const int chunks = l.p.pool.bs * l.p.pool.D / 8;
+  if (l.p.pool.D == 64) {
+    if (chunks <= kIngestThreads) return run_ingest_c<FMT, 64, 1>(l);
+    if (chunks <= 2 * kIngestThreads) return run_ingest_c<FMT, 64, 2>(l);
+    return run_ingest_c<FMT, 64, 4>(l);
+  }
+  if (chunks <= 2 * kIngestThreads) return run_ingest_c<FMT, 128, 2>(l);
+  if (chunks <= 4 * kIngestThreads) return run_ingest_c<FMT, 128, 4>(l);
+  return run_ingest_c<FMT, 128, 8>(l);
+}
+
+cudaError_t launch_ingest_block(const IngestLaunch& l);
+cudaError_t launch_ingest_group(const IngestLaunch& l);
+cudaError_t launch_ingest_token(const IngestLaunch& l);
+cudaError_t launch_ingest_misc(const IngestLaunch& l);
+
+}  // namespace kvq

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime_api.h>
 
+#include "kvq.h"
 #include "kvq_common.cuh"
 
 namespace kvq {
@@ -27,6 +28,55 @@ cudaError_t launch_calibrate(const PoolView& pool, const __half* k, const __half
                              cudaStream_t st);
 cudaError_t launch_read_slots(const PoolView& pool, const int64_t* slots, int64_t n,
                               void* codes_out, float* scales_out, cudaStream_t st);
+
+// Norm, rotation, quantization and scatter of new tokens in one kernel
+// (kvq_ingest_impl.cuh).  Q rows (when there are any) are normed, rotated and
+// written as fp16; K rows are normed, rotated, quantized from fp32 and stored
+// with V in the pool.  With `slots` null the slots come from table / lens as in
+// launch_step_append.
+struct IngestArgs {
+  PoolView pool;
+  const void* q = nullptr;
+  const void* k = nullptr;
+  const void* v = nullptr;
+  int64_t q_stride = 0, k_stride = 0, v_stride = 0;  // elements between tokens
+  bool bf16 = false;                                 // q, k, v are bfloat16 (else fp16)
+  const int64_t* positions = nullptr;
+  const int64_t* slots = nullptr;
+  const int* table = nullptr;
+  const int* lens = nullptr;
+  int max_blocks = 0, max_ctx = 0;
+  int64_t T = 0;
+  int Hq = 0;
+  const float* q_weight = nullptr;  // null: no norm
+  const float* k_weight = nullptr;
+  float eps = 0.f;
+  __half* q_out = nullptr;
+  int64_t q_out_stride = 0;
+  const kvq_rope_plan* plan = nullptr;  // null: no rotation
+};
+cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent);
+
+// Norm and rotation of Q and K rows to fp16 (kvq_rope.cu).
+struct RopeArgs {
+  const void* x[2] = {};  // q, k
+  int64_t x_stride[2] = {};
+  __half* out[2] = {};
+  int64_t out_stride[2] = {};
+  int heads[2] = {};
+  const float* weight[2] = {};
+  bool bf16 = false;
+  const int64_t* positions = nullptr;
+  int64_t T = 0;
+  int D = 0;
+  float eps = 0.f;
+  const kvq_rope_plan* plan = nullptr;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+
+// Dequantized fp16 K and V of n slots, [n][Hkv][D] each.
+cudaError_t launch_read_values(const PoolView& pool, const int64_t* slots, int64_t n, __half* k,
+                               __half* v, cudaStream_t st);
 
 // Launch geometry of one decode call.
 struct DecodePlan {
@@ -124,5 +174,6 @@ cudaError_t launch_decode_channel(const DecodeLaunch& l);
 cudaError_t launch_decode_e5m2(const DecodeLaunch& l);
 cudaError_t launch_decode_bs8_group(const DecodeLaunch& l);  // block size 8, INT8 per-group
 cudaError_t launch_decode_bs8_misc(const DecodeLaunch& l);   // block size 8, the other formats
+cudaError_t launch_decode_block(const DecodeLaunch& l);      // one scale per block, every block size
 
 }  // namespace kvq

@@ -407,7 +407,13 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
         tok_ok = ok;
         sk = 0.f;
         sv = ok ? 1.f : 0.f;
-        if constexpr (T::group_scales) {
+        if constexpr (T::block_scales) {
+          if (ok) {
+            const float2 sc = *reinterpret_cast<const float2*>(page_of(ph[pg]) + 2 * pool.code_bytes);
+            sk = sc.x;
+            sv = sc.y;
+          }
+        } else if constexpr (T::group_scales) {
           if (ok) {
             const float* sc = reinterpret_cast<const float*>(page_of(ph[pg]) + 2 * pool.code_bytes);
             sk = sc[off];

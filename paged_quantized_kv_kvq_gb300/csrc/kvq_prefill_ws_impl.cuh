@@ -125,7 +125,11 @@ __global__ void __launch_bounds__(128) kvq_prefill_stage_kernel(const StageParam
     const bool ok = page != nullptr;
     float sk = 0.f, sv = ok ? 1.f : 0.f;
     if (ok) {
-      if constexpr (T::group_scales) {
+      if constexpr (T::block_scales) {
+        const float2 sc = *reinterpret_cast<const float2*>(page + 2 * pool.code_bytes);
+        sk = sc.x;
+        sv = sc.y;
+      } else if constexpr (T::group_scales) {
         const float* sc = reinterpret_cast<const float*>(page + 2 * pool.code_bytes);
         sk = sc[off];
         sv = sc[bs + off];

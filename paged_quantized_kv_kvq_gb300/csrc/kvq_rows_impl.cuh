@@ -232,7 +232,14 @@ __global__ void __launch_bounds__(kRowsThreads) kvq_rows_kernel(const RowsParams
       const int nvalid = min(16, wlim - t0);
       // ---- scales of this lane's tokens 2j, 2j+1, 8+2j, 9+2j
       float ks[4][NS], vs[4][NS];
-      if constexpr (T::row_scales) {
+      if constexpr (T::block_scales) {
+        const float2 sc = *reinterpret_cast<const float2*>(stage + 2 * pool.code_bytes);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          ks[x][0] = sc.x;
+          vs[x][0] = sc.y;
+        }
+      } else if constexpr (T::row_scales) {
         const float* ksp;
         const float* vsp;
         if constexpr (T::group_scales) {
