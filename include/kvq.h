@@ -502,6 +502,73 @@ kvq_status kvq_selftest_decode_timeout(const kvq_pool* pool, const kvq_half* q, 
                                        int max_context_len, float* out, void* workspace,
                                        size_t ws_bytes, int wait_tries, cudaStream_t stream);
 
+/* ---- Eviction by accumulated attention weight: over the decode steps each
+ * cached token collects the attention paid to it, and when a sequence outgrows
+ * its budget the blocks that collected least are dropped.  The pages name cache
+ * eviction only as a scheduler's business; these three calls are what it needs
+ * from the kernels. */
+
+/* kvq_paged_decode_ex that also writes each row's log-sum-exp:
+ *   lse : fp32 [num_seqs][num_q_heads], ln sum_t exp(q . k^_t * sm_scale); -inf
+ *         for a sequence with L == 0
+ * Results in `out` are those of kvq_paged_decode_ex, bit for bit. */
+kvq_status kvq_paged_decode_lse(const kvq_pool* pool, const kvq_half* q, int num_seqs,
+                                int num_q_heads, const int32_t* block_table,
+                                int max_blocks_per_seq, const int32_t* context_lens,
+                                int max_context_len, float sm_scale, float* out, float* lse,
+                                void* workspace, size_t ws_bytes, int split_blocks,
+                                cudaStream_t stream);
+
+/* Attention weights of the cached tokens, accumulated:
+ *   scores[s][h][t] = decay * prev[s][h][t] + sum over the Q heads of kv head h
+ *                     of exp(q . k^_t * sm_scale - lse),   t < context_lens[s]
+ *   lse    : fp32 [num_seqs][num_q_heads] of the same q over the same tokens
+ *            (kvq_paged_decode_lse); a row whose lse is -inf weighs nothing
+ *   prev   : fp32 like scores, or NULL (zeros); may be scores itself
+ *   scores : fp32 [num_seqs][kv_heads][score_stride], score_stride >=
+ *            max_context_len; values at t >= context_lens[s] are left as they were
+ * The other arguments are those of kvq_paged_decode.  A token new in this step
+ * has no history: its prev must hold 0.  Device errors as for kvq_paged_decode; a
+ * skipped block's scores are left as they were. */
+kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int num_seqs,
+                                 int num_q_heads, const int32_t* block_table,
+                                 int max_blocks_per_seq, const int32_t* context_lens,
+                                 int max_context_len, float sm_scale, const float* lse,
+                                 float decay, const float* prev, float* scores,
+                                 int64_t score_stride, cudaStream_t stream);
+
+/* Choose the blocks that stay and permute each sequence's table row.  A block
+ * weighs the sum of its tokens' scores over the kv heads, rounded once to fp32.
+ * Of a sequence with more than budget_blocks blocks the first sink_blocks and
+ * the last recent_blocks stay, and the heaviest of the others up to
+ * budget_blocks in all (equal weights: the lower index stays; NaN weighs -inf).
+ * No cached data moves.  Keys are cached with their positions' rotation in them,
+ * so attention over the kept blocks needs no more than the new row.
+ *   pool          : only its block size, kv heads and error word are used
+ *   scores        : fp32 [num_seqs][kv_heads][score_stride], score_stride >=
+ *                   max_context_len (those of kvq_attention_weights)
+ *   budget_blocks >= sink_blocks + recent_blocks, sink_blocks >= 0,
+ *   recent_blocks >= 1 (the last block may be partly filled)
+ *   table_out     : int32 [num_seqs][max_blocks_per_seq]: the kept blocks in their
+ *                   order, then the evicted ones in theirs (free for the caller,
+ *                   or the sequence's next blocks), the rest of the row as it
+ *                   was; may be block_table itself
+ *   lens_out      : int32 [num_seqs] tokens left; may be context_lens itself
+ *   kept          : int32 [num_seqs][budget_blocks] indices of the kept blocks in
+ *                   the old row, -1 behind them; may be NULL
+ *   scores_out    : fp32 [num_seqs][kv_heads][out_stride], out_stride >=
+ *                   budget_blocks * block_size: the scores of the tokens left;
+ *                   values behind them are left as they were.  Must not overlap
+ *                   scores; may be NULL
+ * Device errors: context_lens[s] > max_context_len sets OUT_OF_RANGE (clamped).
+ * UNSUPPORTED beyond 28672 blocks per sequence. */
+kvq_status kvq_evict_blocks(const kvq_pool* pool, const float* scores, int64_t score_stride,
+                            int num_seqs, const int32_t* block_table, int max_blocks_per_seq,
+                            const int32_t* context_lens, int max_context_len, int budget_blocks,
+                            int sink_blocks, int recent_blocks, int32_t* table_out,
+                            int32_t* lens_out, int32_t* kept, float* scores_out,
+                            int64_t out_stride, cudaStream_t stream);
+
 /* The cached K and V of n slots as fp16 values, code * scale in fp32 rounded
  * once: k_out, v_out [n][kv_heads][head_dim], 16-byte aligned.  A negative slot
  * leaves its rows as they were; a slot outside the pool does too and sets

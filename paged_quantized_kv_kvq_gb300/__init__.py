@@ -142,6 +142,9 @@ def _declare(L):
                            f32, P, i64, P, i64, P]),
         "kvq_rope_append": (i32, [P, ctypes.POINTER(RopePlan), i32, P, i64, i32, P, i64, P, i64, P,
                                   P, i64, P, P, f32, P, i64, P]),
+        "kvq_paged_decode_lse": (i32, [P, P, i32, i32, P, i32, P, i32, f32, P, P, P, sz, i32, P]),
+        "kvq_attention_weights": (i32, [P, P, i32, i32, P, i32, P, i32, f32, P, f32, P, P, i64, P]),
+        "kvq_evict_blocks": (i32, [P, P, i64, i32, P, i32, P, i32, i32, i32, i32, P, P, P, P, i64, P]),
         "kvq_read_values": (i32, [P, P, i64, P, P, P]),
         "kvq_read_slots": (i32, [P, P, i64, P, P, P]),
         "kvq_get_error": (i32, [P, P]),
@@ -412,6 +415,72 @@ def kvq_paged_decode(pool, q, block_table, context_lens, max_context_len, sm_sca
         int(split_blocks), _stream(stream)), "kvq_paged_decode")
 
 
+def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm_scale, out, lse,
+                         workspace=None, split_blocks=0, stream=None) -> None:
+    """kvq_paged_decode that also writes each row's log-sum-exp, lse [S, Hq] fp32
+    (kvq_paged_decode_lse in include/kvq.h)."""
+    import torch
+
+    S, Hq, _ = q.shape
+    if lse.shape != (S, Hq):
+        raise ValueError("lse must be [num_seqs, num_q_heads]")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().kvq_paged_decode_lse(
+        pool, _ptr(q, torch.float16, "q"), S, Hq, _ptr(block_table, torch.int32, "block_table"),
+        block_table.shape[1], _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
+        float(sm_scale), _ptr(out, torch.float32, "out"), _ptr(lse, torch.float32, "lse"),
+        _ptr(workspace, None, "workspace") if workspace is not None else None, ws_bytes,
+        int(split_blocks), _stream(stream)), "kvq_paged_decode_lse")
+
+
+def kvq_attention_weights(pool, q, block_table, context_lens, max_context_len, sm_scale, lse, scores,
+                          prev=None, decay=1.0, stream=None) -> None:
+    """Attention weights of the cached tokens, summed over each kv head's Q heads and
+    added to decay * prev: scores [S, Hkv, >= max_context_len] fp32
+    (kvq_attention_weights in include/kvq.h).  prev may be scores itself."""
+    import torch
+
+    S, Hq, _ = q.shape
+    if scores.dim() != 3 or scores.shape[0] != S or lse.shape != (S, Hq):
+        raise ValueError("scores must be [num_seqs, kv_heads, tokens] and lse [num_seqs, num_q_heads]")
+    if prev is not None and prev.shape != scores.shape:
+        raise ValueError("prev must have the shape of scores")
+    _check(lib().kvq_attention_weights(
+        pool, _ptr(q, torch.float16, "q"), S, Hq, _ptr(block_table, torch.int32, "block_table"),
+        block_table.shape[1], _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
+        float(sm_scale), _ptr(lse, torch.float32, "lse"), float(decay),
+        _ptr(prev, torch.float32, "prev"), _ptr(scores, torch.float32, "scores"), scores.shape[2],
+        _stream(stream)), "kvq_attention_weights")
+
+
+def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, budget_blocks,
+                     sink_blocks, recent_blocks, table_out, lens_out, kept=None, scores_out=None,
+                     stream=None) -> None:
+    """Keep each sequence's heaviest budget_blocks blocks and permute its table row
+    (kvq_evict_blocks in include/kvq.h): scores [S, Hkv, >= max_context_len], kept
+    int32 [S, budget_blocks], scores_out [S, Hkv, >= budget_blocks * block_size].
+    table_out and lens_out may be block_table and context_lens themselves."""
+    import torch
+
+    S = context_lens.numel()
+    if scores.dim() != 3 or scores.shape[0] != S or block_table.shape[0] != S:
+        raise ValueError("scores must be [num_seqs, kv_heads, tokens] and block_table [num_seqs, blocks]")
+    if table_out.shape != block_table.shape or lens_out.numel() != S:
+        raise ValueError("table_out and lens_out must be shaped like block_table and context_lens")
+    if kept is not None and kept.shape != (S, budget_blocks):
+        raise ValueError("kept must be [num_seqs, budget_blocks]")
+    if scores_out is not None and (scores_out.dim() != 3 or scores_out.shape[:2] != scores.shape[:2]):
+        raise ValueError("scores_out must be [num_seqs, kv_heads, tokens]")
+    _check(lib().kvq_evict_blocks(
+        pool, _ptr(scores, torch.float32, "scores"), scores.shape[2], S,
+        _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
+        _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len), int(budget_blocks),
+        int(sink_blocks), int(recent_blocks), _ptr(table_out, torch.int32, "table_out"),
+        _ptr(lens_out, torch.int32, "lens_out"), _ptr(kept, torch.int32, "kept"),
+        _ptr(scores_out, torch.float32, "scores_out"),
+        0 if scores_out is None else scores_out.shape[2], _stream(stream)), "kvq_evict_blocks")
+
+
 def kvq_decode_step(pool, k_new, v_new, q, block_table, context_lens, max_context_len, sm_scale,
                     out, workspace=None, stream=None) -> None:
     """Append each sequence's new token at position context_lens[s]-1, then
@@ -656,6 +725,47 @@ class KVPool:
         kvq_decode_step(self.handle, k_new, v_new, q, block_table, context_lens, max_context_len,
                         sm_scale, out, ws, stream)
         return out
+
+    def decode_lse(self, q, block_table, context_lens, max_context_len, sm_scale=None, stream=None):
+        """decode's output and each row's log-sum-exp [S, Hq]."""
+        import torch
+
+        S, Hq, D = q.shape
+        out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
+        lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
+        nws = kvq_decode_workspace_bytes(self.handle, S, Hq, max_context_len)
+        ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
+        kvq_paged_decode_lse(self.handle, q, block_table, context_lens, max_context_len,
+                             D ** -0.5 if sm_scale is None else sm_scale, out, lse, ws, 0, stream)
+        return out, lse
+
+    def accumulate_weights(self, q, block_table, context_lens, max_context_len, lse, scores,
+                           decay=1.0, sm_scale=None, stream=None):
+        """scores = decay * scores + this step's attention weights, in place."""
+        self._check_heads(scores)
+        kvq_attention_weights(self.handle, q, block_table, context_lens, max_context_len,
+                              q.shape[2] ** -0.5 if sm_scale is None else sm_scale, lse, scores,
+                              scores, decay, stream)
+        return scores
+
+    def evict_blocks(self, scores, block_table, context_lens, max_context_len, budget_blocks,
+                     sink_blocks=0, recent_blocks=1, stream=None):
+        """(table, lens, kept, scores) after the eviction, in new tensors."""
+        import torch
+
+        self._check_heads(scores)
+        S = context_lens.numel()
+        table, lens = torch.empty_like(block_table), torch.empty_like(context_lens)
+        kept = torch.empty((S, budget_blocks), dtype=torch.int32, device=scores.device)
+        out = torch.zeros((S, self.kv_heads, max(budget_blocks * self.block_size, scores.shape[2])),
+                          dtype=torch.float32, device=scores.device)
+        kvq_evict_blocks(self.handle, scores, block_table, context_lens, max_context_len,
+                         budget_blocks, sink_blocks, recent_blocks, table, lens, kept, out, stream)
+        return table, lens, kept, out
+
+    def _check_heads(self, scores):
+        if scores.shape[1] != self.kv_heads:
+            raise ValueError("scores must have the pool's %d kv heads" % self.kv_heads)
 
     def cascade_decode(self, q, block_table, context_lens, max_context_len, prefix_blocks,
                        sm_scale=None, out=None, stream=None):

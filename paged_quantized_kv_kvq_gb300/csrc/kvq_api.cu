@@ -430,6 +430,101 @@ kvq_status kvq_paged_decode_ex(const kvq_pool* pool, const kvq_half* q, int num_
   return from_cuda(kvq::launch_decode(a, plan, stream));
 }
 
+kvq_status kvq_paged_decode_lse(const kvq_pool* pool, const kvq_half* q, int num_seqs,
+                                int num_q_heads, const int32_t* block_table,
+                                int max_blocks_per_seq, const int32_t* context_lens,
+                                int max_context_len, float sm_scale, float* out, float* lse,
+                                void* workspace, size_t ws_bytes, int split_blocks,
+                                cudaStream_t stream) {
+  kvq::DecodeArgs a;
+  kvq::DecodePlan plan;
+  const kvq_status st =
+      prepare_decode(pool, q, num_seqs, num_q_heads, block_table, max_blocks_per_seq, context_lens,
+                     max_context_len, sm_scale, out, workspace, ws_bytes, split_blocks, &a, &plan);
+  if (st != KVQ_OK || num_seqs == 0) return st;
+  if (lse == nullptr) return KVQ_ERR_INVALID_ARG;
+  a.lse = lse;
+  return from_cuda(kvq::launch_decode(a, plan, stream));
+}
+
+kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int num_seqs,
+                                 int num_q_heads, const int32_t* block_table,
+                                 int max_blocks_per_seq, const int32_t* context_lens,
+                                 int max_context_len, float sm_scale, const float* lse,
+                                 float decay, const float* prev, float* scores,
+                                 int64_t score_stride, cudaStream_t stream) {
+  if (pool == nullptr || num_seqs < 0 || num_q_heads < 1 || max_blocks_per_seq < 1 ||
+      max_context_len < 0 || score_stride < max_context_len)
+    return KVQ_ERR_INVALID_ARG;
+  if (num_q_heads % pool->view.Hkv != 0) return KVQ_ERR_INVALID_ARG;
+  if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * pool->view.bs) return KVQ_ERR_INVALID_ARG;
+  if (!(sm_scale == sm_scale) || !(decay == decay)) return KVQ_ERR_INVALID_ARG;
+  if (num_seqs == 0 || max_context_len == 0) return KVQ_OK;
+  if (q == nullptr || block_table == nullptr || context_lens == nullptr || lse == nullptr ||
+      scores == nullptr)
+    return KVQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(q) & 15) return KVQ_ERR_INVALID_ARG;
+  kvq::WeightsArgs a;
+  a.pool = pool->view;
+  a.q = reinterpret_cast<const __half*>(q);
+  a.table = block_table;
+  a.lens = context_lens;
+  a.lse = lse;
+  a.prev = prev;
+  a.scores = scores;
+  a.stride = score_stride;
+  a.decay = decay;
+  a.S = num_seqs;
+  a.Hq = num_q_heads;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_ctx = max_context_len;
+  a.sm_scale = sm_scale;
+  const cudaError_t e = kvq::launch_weights(a, stream);
+  return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+kvq_status kvq_evict_blocks(const kvq_pool* pool, const float* scores, int64_t score_stride,
+                            int num_seqs, const int32_t* block_table, int max_blocks_per_seq,
+                            const int32_t* context_lens, int max_context_len, int budget_blocks,
+                            int sink_blocks, int recent_blocks, int32_t* table_out,
+                            int32_t* lens_out, int32_t* kept, float* scores_out,
+                            int64_t out_stride, cudaStream_t stream) {
+  if (pool == nullptr || num_seqs < 0 || max_blocks_per_seq < 1 || max_context_len < 0 ||
+      score_stride < max_context_len || sink_blocks < 0 || recent_blocks < 1 ||
+      (int64_t)sink_blocks + recent_blocks > budget_blocks)
+    return KVQ_ERR_INVALID_ARG;
+  if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * pool->view.bs) return KVQ_ERR_INVALID_ARG;
+  if (scores_out != nullptr && out_stride < (int64_t)budget_blocks * pool->view.bs)
+    return KVQ_ERR_INVALID_ARG;
+  if (num_seqs == 0) return KVQ_OK;
+  if (scores == nullptr || block_table == nullptr || context_lens == nullptr ||
+      table_out == nullptr || lens_out == nullptr || scores_out == scores)
+    return KVQ_ERR_INVALID_ARG;
+  if (((int64_t)max_context_len + pool->view.bs - 1) / pool->view.bs > kvq::kEvictMaxBlocks)
+    return KVQ_ERR_UNSUPPORTED;
+  kvq::EvictArgs a;
+  a.scores = scores;
+  a.stride = score_stride;
+  a.lens = context_lens;
+  a.table = block_table;
+  a.table_out = table_out;
+  a.lens_out = lens_out;
+  a.kept = kept;
+  a.scores_out = scores_out;
+  a.out_stride = out_stride;
+  a.err = pool->view.err;
+  a.S = num_seqs;
+  a.Hkv = pool->view.Hkv;
+  a.bs = pool->view.bs;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_ctx = max_context_len;
+  a.budget = budget_blocks;
+  a.sink = sink_blocks;
+  a.recent = recent_blocks;
+  const cudaError_t e = kvq::launch_evict(a, stream);
+  return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
+}
+
 kvq_status kvq_selftest_decode_timeout(const kvq_pool* pool, const kvq_half* q, int num_seqs,
                                        int num_q_heads, const int32_t* block_table,
                                        int max_blocks_per_seq, const int32_t* context_lens,

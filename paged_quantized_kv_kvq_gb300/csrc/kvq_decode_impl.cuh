@@ -69,6 +69,7 @@ struct DecodeParams {
   // otherwise.
   const float* pre;
   int skip;
+  float* lse;          // [S][Hq] natural log of each row's softmax denominator, or null
   int S, Hq, G, n_ht, max_blocks, max_ctx;
   int ppw_fixed;       // pages per warp; 0 = balance the pages over all warps
   int nstage;          // shared-memory stages per warp
@@ -87,6 +88,12 @@ __device__ __forceinline__ float pow2f(int e) {  // 2^e for e in [-126, 127]
 
 __device__ __forceinline__ int exponent_of(float x) {  // floor(log2 x) for normal x > 0
   return ((__float_as_int(x) >> 23) & 0xFF) - 127;
+}
+
+// Natural log of sum exp(z) from a base-2 running maximum and sum; -inf for an
+// empty row.
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000u);
 }
 
 __device__ __forceinline__ float warp_max_over_rows(float v) {  // reduce over lane>>2
@@ -727,6 +734,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
     for (int s = gw; s < p.S; s += nwarps) {
       if (PS[s + 1] != PS[s]) continue;
       float* o = p.out + (int64_t)s * p.out_stride;
+      if (p.lse != nullptr)
+        for (int i = lane; i < p.Hq; i += 32) p.lse[(int64_t)s * p.Hq + i] = kNegInf;
       if (p.pre == nullptr) {
         for (int i = lane; i < p.Hq * D; i += 32) o[i] = 0.f;
       } else {
@@ -944,9 +953,13 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
     const float lt0 = warp_sum_over_rows(l[0]), lt1 = warp_sum_over_rows(l[1]);
     const float inv2E = pow2f(-E);
     const float* vch = T::channel ? pool.chan_scales + ((int64_t)pool.Hkv + h) * D : nullptr;
-    const int64_t row0 = (int64_t)u.s * p.Hq + h * p.G + 8 * ht;  // (prefix partial rows)
+    const int64_t row0 = (int64_t)u.s * p.Hq + h * p.G + 8 * ht;  // (prefix partials, lse)
     float* obase = p.out + (int64_t)u.s * p.out_stride + (int64_t)(h * p.G + 8 * ht) * D;
     if (seg_pi0 == 0 && seg_end == u.Ps) {
+      if (p.lse != nullptr && g == 0) {
+        if (2 * j < Gt) p.lse[row0 + 2 * j] = row_lse(m[0], lt0);
+        if (2 * j + 1 < Gt) p.lse[row0 + 2 * j + 1] = row_lse(m[1], lt1);
+      }
       if (p.pre == nullptr) {
         const float f0 = lt0 > 0.f ? inv2E / lt0 : 0.f, f1 = lt1 > 0.f ? inv2E / lt1 : 0.f;
 #pragma unroll
@@ -1280,6 +1293,7 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const DecodePa
       }
       M = cm;
     }
+    if (p.lse != nullptr && lane == 0) p.lse[orow] = row_lse(M, Lsum);
     float* dst = p.out + (int64_t)s * p.out_stride + (int64_t)(h * p.G + 8 * ht + rr) * D;
 #pragma unroll
     for (int i = 0; i < NE; ++i) dst[lane + 32 * i] = Lsum > 0.f ? acc[i] / Lsum : 0.f;

@@ -78,6 +78,40 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
 cudaError_t launch_read_values(const PoolView& pool, const int64_t* slots, int64_t n, __half* k,
                                __half* v, cudaStream_t st);
 
+// Attention weights of the cached tokens (kvq_weights_impl.cuh), from the
+// log-sum-exps of a decode of the same rows.
+struct WeightsArgs {
+  PoolView pool;
+  const __half* q;
+  const int* table;
+  const int* lens;
+  const float* lse;   // [S][Hq]
+  const float* prev;  // [S][Hkv][stride] or null
+  float* scores;      // [S][Hkv][stride]
+  int64_t stride;
+  float decay;
+  int S, Hq, max_blocks, max_ctx;
+  float sm_scale;
+};
+cudaError_t launch_weights(const WeightsArgs& a, cudaStream_t st);
+
+// Blocks with the least accumulated weight leave their sequences (kvq_evict.cu).
+constexpr int kEvictMaxBlocks = 28672;  // of one sequence: two words each in shared memory
+struct EvictArgs {
+  const float* scores;  // [S][Hkv][stride]
+  int64_t stride;
+  const int* lens;
+  const int* table;
+  int* table_out;
+  int* lens_out;
+  int* kept;          // [S][budget] or null
+  float* scores_out;  // [S][Hkv][out_stride] or null
+  int64_t out_stride;
+  int* err;
+  int S, Hkv, bs, max_blocks, max_ctx, budget, sink, recent;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t st);
+
 // Launch geometry of one decode call.
 struct DecodePlan {
   int grid = 0;         // persistent CTAs
@@ -111,6 +145,7 @@ struct DecodeArgs {
   int skip = 0;
   const float* pre = nullptr;
   int64_t q_stride = 0, out_stride = 0;  // elements between sequences' rows; 0 = Hq * D
+  float* lse = nullptr;  // [S][Hq] log of the softmax denominators; null = not wanted
   int wait_tries = kWaitTries;  // bound of each pipeline wait, in ~1 ms tries
   int fault_issue = -1;   // self-test only: withhold warp 0's copy of this index
 };
