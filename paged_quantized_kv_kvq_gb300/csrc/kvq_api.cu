@@ -123,7 +123,7 @@ int device_sms() {
 
 kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
-constexpr int kMaxRopeHeads = 1 << 16;
+constexpr int kMaxRopeHeads = 1 << 13;
 
 // Checks shared by kvq_rope and kvq_rope_append.
 bool rope_args_ok(const kvq_rope_plan* plan, int x_type, int head_dim, float eps) {

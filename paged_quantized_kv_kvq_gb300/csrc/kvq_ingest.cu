@@ -121,6 +121,7 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   if (a.Hq > 0) {
     const int rpp = kIngestThreads / (a.pool.D / 8);
     p.q_parts = a.T >= 512 ? 1 : (a.Hq + rpp - 1) / rpp;
+    p.q_inv = rope_inverse(a.Hq);
     p.q_tpc = a.T >= 4096 ? kRopeTokens : 1;
     q_ctas = (a.T + p.q_tpc - 1) / p.q_tpc * p.q_parts;
   }

@@ -50,6 +50,7 @@ struct IngestParams {
   int tpc, hpc, hsplit;  // tokens and heads per K/V CTA, CTAs over the heads
   int64_t kv_ctas;       // CTAs 0 .. kv_ctas-1 take K/V, the rest query rows
   int q_tpc, q_parts;
+  uint32_t q_inv;
   kvq_rope_plan plan;
 };
 
@@ -318,10 +319,9 @@ __global__ void __launch_bounds__(kIngestThreads) kvq_ingest_kernel(const __grid
   if (blockIdx.x >= p.kv_ctas) {
     const int64_t b = blockIdx.x - p.kv_ctas;
     const int64_t t0 = b / p.q_parts * p.q_tpc;
-    rope_tokens<D, kIngestThreads>(p.q, p.Hq, RopeRows{}, 0, p.bf16, p.positions, t0,
+    rope_tokens<D, kIngestThreads>(p.q, p.Hq, RopeRows{}, 0, p.q_inv, p.bf16, p.positions, t0,
                                    static_cast<int>(min((int64_t)p.q_tpc, p.T - t0)),
-                                   static_cast<int>(b % p.q_parts), p.q_parts, p.eps, p.plan,
-                                   reinterpret_cast<float2*>(smem));
+                                   static_cast<int>(b % p.q_parts), p.q_parts, p.eps, p.plan, smem);
     return;
   }
   __shared__ IngestShared sh;
@@ -375,10 +375,10 @@ __global__ void __launch_bounds__(kIngestThreads) kvq_ingest_kernel(const __grid
 }
 
 // Shared memory of a launch: the tile image and the run's cosines and sines (the
-// query CTAs use kRopeTokens tokens' worth).
+// query CTAs' own, if that is more).
 inline int ingest_smem(const PoolView& pool, int rotary_dim) {
   const int kv = pool.code_bytes + pool.bs * rotary_dim / 2 * 8;
-  const int q = kRopeTokens * rotary_dim / 2 * 8;
+  const int q = rope_smem(rotary_dim, pool.D);
   return kv > q ? kv : q;
 }
 

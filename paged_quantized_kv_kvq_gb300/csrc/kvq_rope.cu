@@ -21,17 +21,18 @@ struct RopeParams {
   int64_t T;
   int tpc;    // tokens per CTA
   int parts;  // CTAs a token's rows are spread over
+  uint32_t inv;
   float eps;
   kvq_rope_plan plan;
 };
 
 template <int D>
 __global__ void __launch_bounds__(kRopeThreads) kvq_rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ __align__(16) float2 cs[kRopeTokens * D / 2];
+  __shared__ __align__(16) char smem[rope_smem(D, D)];
   const int64_t t0 = (blockIdx.x / p.parts) * (int64_t)p.tpc;
-  rope_tokens<D, kRopeThreads>(p.rows[0], p.heads[0], p.rows[1], p.heads[1], p.bf16, p.positions,
-                               t0, static_cast<int>(min((int64_t)p.tpc, p.T - t0)),
-                               blockIdx.x % p.parts, p.parts, p.eps, p.plan, cs);
+  rope_tokens<D, kRopeThreads>(p.rows[0], p.heads[0], p.rows[1], p.heads[1], p.inv, p.bf16,
+                               p.positions, t0, static_cast<int>(min((int64_t)p.tpc, p.T - t0)),
+                               blockIdx.x % p.parts, p.parts, p.eps, p.plan, smem);
 }
 
 }  // namespace
@@ -49,8 +50,10 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   if (a.plan != nullptr) p.plan = *a.plan;
   // Few tokens: spread a token's rows over CTAs so that every thread has one
   // chunk; many: several tokens per CTA share its set-up.
+  const int H = a.heads[0] + a.heads[1];
+  p.inv = rope_inverse(H);
   const int rpp = kRopeThreads / (a.D / 8);
-  const int passes = (a.heads[0] + a.heads[1] + rpp - 1) / rpp;
+  const int passes = (H + rpp - 1) / rpp;
   p.parts = a.T >= 512 ? 1 : passes;
   p.tpc = a.T >= 4096 ? kRopeTokens : 1;
   const int64_t grid = (a.T + p.tpc - 1) / p.tpc * p.parts;

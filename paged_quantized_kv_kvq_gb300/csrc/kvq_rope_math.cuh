@@ -122,71 +122,133 @@ struct RopeRows {
   const float* weight;  // null: no norm
 };
 
-// Tokens t0 .. t0+nt-1 (nt <= kRopeTokens) of sets A (hA heads) and B (hB
-// heads), head rows `part`, part + parts, ... of each; `cs` is shared memory for
-// nt * r/2 pairs.
 constexpr int kRopeTokens = 4;
 
+// Shared memory of rope_tokens: cosines and sines of its tokens, both sets' weights.
+__host__ __device__ constexpr int rope_smem(int rotary_dim, int D) {
+  return kRopeTokens * rotary_dim / 2 * 8 + 2 * D * 4;
+}
+
+// ceil(2^32 / h), h > 1: the high word of row * that is row / h for row * h < 2^32
+// (here row < kRopeTokens * h + 2 * 32 and h <= 2^14).
+inline uint32_t rope_inverse(int h) {
+  return h > 1 ? static_cast<uint32_t>((0x100000000ull + h - 1) / h) : 0;
+}
+
+// Tokens t0 .. t0+nt-1 (nt <= kRopeTokens) of sets A (hA heads) and B (hB
+// heads), every parts-th stretch of their rows; `inv` = rope_inverse(hA + hB).
+//
+// A pass of the CTA takes one row per D/8 lanes.  In the half layout a lane
+// holds channels 4c .. 4c+3 and, where they are rotated, their partners r/2
+// further on, so that a rotation stays within a lane (two 8-byte accesses, each
+// still whole sectors over the row); otherwise channels 8c .. 8c+7 (one 16-byte
+// access).  Either way its pairs are 4c .. 4c+3.
+// The kernel that uses this is bound by its instructions as much as by HBM: a
+// row's lane costs about 90 of them for its 32 bytes, so the row index is split
+// by a multiplication, and the weights come from shared memory.
 template <int D, int THREADS>
 __device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const RopeRows& B, int hB,
-                                            bool bf16, const int64_t* positions, int64_t t0, int nt,
-                                            int part, int parts, float eps,
-                                            const kvq_rope_plan& plan, float2* cs) {
+                                            uint32_t inv, bool bf16, const int64_t* positions,
+                                            int64_t t0, int nt, int part, int parts, float eps,
+                                            const kvq_rope_plan& plan, char* smem) {
   constexpr int LPH = D / 8, RPP = THREADS / LPH;  // lanes per head, rows per pass
   const int r = plan.rotary_dim, rp = r >> 1;
+  float2* cs = reinterpret_cast<float2*>(smem);
+  float* wsm = reinterpret_cast<float*>(cs + kRopeTokens * rp);
   for (int i = threadIdx.x; i < nt * rp; i += THREADS)
     cs[i] = rope_cs(plan.turns[i % rp], positions[t0 + i / rp], plan.magnitude);
-  const int ci = threadIdx.x % LPH, row0 = threadIdx.x / LPH;
-  float wA[8], wB[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    wA[i] = A.weight != nullptr ? A.weight[8 * ci + i] : 1.f;
-    wB[i] = B.weight != nullptr ? B.weight[8 * ci + i] : 1.f;
+  for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
+    const float* w = i < D ? A.weight : B.weight;
+    wsm[i] = w != nullptr ? w[i % D] : 1.f;
   }
+  const int ci = threadIdx.x % LPH, row0 = threadIdx.x / LPH;
+  const bool inter = plan.layout == KVQ_ROPE_INTERLEAVED, rot = 8 * ci < r;
+  const bool norm = A.weight != nullptr || B.weight != nullptr;
+  const int da = !inter && rot ? 4 * ci : 8 * ci, db = !inter && rot ? 4 * ci + rp : 8 * ci + 4;
+  const __half* xA = static_cast<const __half*>(A.x) + t0 * A.x_stride;
+  const __half* xB = static_cast<const __half*>(B.x) + t0 * B.x_stride - hA * D;
+  __half* oA = A.out + t0 * A.out_stride;
+  __half* oB = B.out + t0 * B.out_stride - hA * D;
   __syncthreads();
   const int H = hA + hB, rows = nt * H;
   constexpr int U = 2;  // rows in flight per thread
   for (int base = part * RPP; base < rows; base += parts * RPP * U) {
-    uint4 raw[U];
+    uint2 raw[U][2];
     int tok[U], head[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int row = base + u * parts * RPP + row0;
-      tok[u] = row < rows ? row / H : -1;
-      head[u] = row - (row / H) * H;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (tok[u] >= 0) {
+      tok[u] = H > 1 ? static_cast<int>(__umulhi(row, inv)) : row;
+      head[u] = row - tok[u] * H;
+      raw[u][0] = raw[u][1] = make_uint2(0, 0);
+      if (row < rows) {
         const bool b = head[u] >= hA;
-        const RopeRows& R = b ? B : A;
-        raw[u] = *reinterpret_cast<const uint4*>(
-            static_cast<const __half*>(R.x) + (t0 + tok[u]) * R.x_stride +
-            (b ? head[u] - hA : head[u]) * D + 8 * ci);
+        const __half* x = (b ? xB : xA) + tok[u] * (b ? B.x_stride : A.x_stride) + head[u] * D;
+        if (inter) {
+          const uint4 v = *reinterpret_cast<const uint4*>(x + da);
+          raw[u][0] = make_uint2(v.x, v.y);
+          raw[u][1] = make_uint2(v.z, v.w);
+        } else {
+          raw[u][0] = *reinterpret_cast<const uint2*>(x + da);
+          raw[u][1] = *reinterpret_cast<const uint2*>(x + db);
+        }
+      } else {
+        tok[u] = -1;
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool b = head[u] >= hA;
-      const RopeRows& R = b ? B : A;
-      float x[8], w[8];
-      widen8(raw[u], bf16, x);
-      // a row's lanes agree on its set; a warp may hold rows of both, so all of
-      // its lanes reduce and only those with a weight take the result
-      if (A.weight != nullptr || B.weight != nullptr) {
-        float y[8];
+      float x[8];
+      widen8(make_uint4(raw[u][0].x, raw[u][0].y, raw[u][1].x, raw[u][1].y), bf16, x);
+      if (norm) {
+        float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = x[i];
-          w[i] = b ? wB[i] : wA[i];
-        }
-        norm8<D>(y, w, eps);
-        if (R.weight != nullptr)
+        for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = y[i];
+        for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        const float f = (b ? B.weight : A.weight) != nullptr ? rsqrtf(fmaf(s, 1.f / D, eps)) : 1.f;
+        const float4 wa = *reinterpret_cast<const float4*>(wsm + (b ? D : 0) + da);
+        const float4 wb = *reinterpret_cast<const float4*>(wsm + (b ? D : 0) + db);
+        x[0] *= f * wa.x;
+        x[1] *= f * wa.y;
+        x[2] *= f * wa.z;
+        x[3] *= f * wa.w;
+        x[4] *= f * wb.x;
+        x[5] *= f * wb.y;
+        x[6] *= f * wb.z;
+        x[7] *= f * wb.w;
       }
-      if (r > 0) rotate8<D>(x, ci, r, plan.layout == KVQ_ROPE_INTERLEAVED, cs + max(tok[u], 0) * rp);
-      if (tok[u] >= 0)
-        *reinterpret_cast<uint4*>(R.out + (t0 + tok[u]) * R.out_stride +
-                                  (b ? head[u] - hA : head[u]) * D + 8 * ci) = narrow8(x);
+      if (rot) {
+        const float4* t = reinterpret_cast<const float4*>(cs + max(tok[u], 0) * rp + 4 * ci);
+        const float4 c0 = t[0], c1 = t[1];
+        const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
+        if (inter) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = x[2 * i], d = x[2 * i + 1];
+            x[2 * i] = fmaf(a, c[i], -d * s[i]);
+            x[2 * i + 1] = fmaf(a, s[i], d * c[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = x[i], d = x[4 + i];
+            x[i] = fmaf(a, c[i], -d * s[i]);
+            x[4 + i] = fmaf(a, s[i], d * c[i]);
+          }
+        }
+      }
+      if (tok[u] >= 0) {
+        __half* out = (b ? oB : oA) + tok[u] * (b ? B.out_stride : A.out_stride) + head[u] * D;
+        const uint4 o = narrow8(x);
+        if (inter) {
+          *reinterpret_cast<uint4*>(out + da) = o;
+        } else {
+          *reinterpret_cast<uint2*>(out + da) = make_uint2(o.x, o.y);
+          *reinterpret_cast<uint2*>(out + db) = make_uint2(o.z, o.w);
+        }
+      }
     }
   }
 }
