@@ -237,7 +237,7 @@ typedef enum { KVQ_X_FP16 = 0, KVQ_X_BF16 = 1 } kvq_x_type;
  *                 count of 0 leaves that side out (its pointers may be NULL)
  *   head_dim    : 64 or 128, >= rotary_dim
  *   positions   : int64 [T]; any value, a negative one turns backwards
- *   q_weight, k_weight : fp32 [head_dim] or NULL
+ *   q_weight, k_weight : fp32 [head_dim], 16-byte aligned, or NULL
  *   eps         : >= 0
  *   q_out, k_out : fp16, laid out like q and k with strides of their own.  An
  *                 out may be its own input (same pointer and stride); any other

@@ -123,10 +123,13 @@ int device_sms() {
 
 kvq_status from_cuda(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA; }
 
-constexpr int kMaxRopeHeads = 1 << 13;
+constexpr int kMaxRopeHeads = 8192;
 
 // Checks shared by kvq_rope and kvq_rope_append.
-bool rope_args_ok(const kvq_rope_plan* plan, int x_type, int head_dim, float eps) {
+bool rope_args_ok(const kvq_rope_plan* plan, int x_type, int head_dim, float eps,
+                  const float* q_weight, const float* k_weight) {
+  // (read 16 bytes at a time)
+  if ((reinterpret_cast<uintptr_t>(q_weight) | reinterpret_cast<uintptr_t>(k_weight)) & 15) return false;
   if (x_type != KVQ_X_FP16 && x_type != KVQ_X_BF16) return false;
   if (!(eps >= 0.f)) return false;
   if (plan == nullptr) return true;
@@ -263,7 +266,7 @@ kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
                     cudaStream_t stream) {
   if (T < 0 || num_q_heads < 0 || num_k_heads < 0 || head_dim < 1) return KVQ_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return KVQ_ERR_UNSUPPORTED;
-  if (!rope_args_ok(plan, x_type, head_dim, eps)) return KVQ_ERR_INVALID_ARG;
+  if (!rope_args_ok(plan, x_type, head_dim, eps, q_weight, k_weight)) return KVQ_ERR_INVALID_ARG;
   if (T == 0 || num_q_heads + (int64_t)num_k_heads == 0) return KVQ_OK;
   if (plan != nullptr && positions == nullptr) return KVQ_ERR_INVALID_ARG;
   if (!rows_ok(q, q_row_stride, num_q_heads, head_dim) ||
@@ -303,7 +306,7 @@ kvq_status kvq_rope_append(kvq_pool* pool, const kvq_rope_plan* plan, kvq_x_type
                            kvq_half* q_out, int64_t q_out_row_stride, cudaStream_t stream) {
   if (pool == nullptr || T < 0 || num_q_heads < 0) return KVQ_ERR_INVALID_ARG;
   const int D = pool->view.D, Hkv = pool->view.Hkv;
-  if (!rope_args_ok(plan, x_type, D, eps)) return KVQ_ERR_INVALID_ARG;
+  if (!rope_args_ok(plan, x_type, D, eps, q_weight, k_weight)) return KVQ_ERR_INVALID_ARG;
   if (T == 0) return KVQ_OK;
   if (slot_mapping == nullptr || (plan != nullptr && positions == nullptr))
     return KVQ_ERR_INVALID_ARG;

@@ -19,6 +19,7 @@
 // rounded again: code' = rne(code * s_old / s).
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "kvq_context.h"
 #include "kvq_internal.h"
@@ -30,6 +31,7 @@ namespace kvq {
 constexpr int kIngestThreads = 128;
 constexpr int kIngestWarps = kIngestThreads / 32;
 constexpr int kMaxBlock = 64;  // largest block size
+constexpr int kIngestRounds = 4;  // of ingest_whole per CTA
 
 struct IngestParams {
   PoolView pool;
@@ -49,8 +51,7 @@ struct IngestParams {
   int bs_log2;
   int tpc, hpc, hsplit;  // tokens and heads per K/V CTA, CTAs over the heads
   int64_t kv_ctas;       // CTAs 0 .. kv_ctas-1 take K/V, the rest query rows
-  int q_tpc, q_parts;
-  uint32_t q_inv;
+  int q_parts;           // CTAs a token's query rows are spread over
   kvq_rope_plan plan;
 };
 
@@ -119,7 +120,6 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
   constexpr bool kBlock = fmt_block(FMT);
   constexpr bool kToken = FMT == FMT_INT8_TOKEN || FMT == FMT_FP8_TOKEN;
   constexpr float kTop = fmt_e4m3(FMT) ? 448.f : FMT == FMT_INT4_GROUP ? 7.f : 127.f;
-  constexpr int ES = FMT == FMT_FP16 ? 2 : 1;
   const PoolView& pool = p.pool;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ci = tid % LPH, r0 = tid / LPH, d0 = 8 * ci;
@@ -134,9 +134,7 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
     const int off = sh.off[w0 + tid];
     atomicOr(&sh.has[off >> 5], 1u << (off & 31));
   }
-  if (turn)
-    for (int i = tid; i < n * rp; i += kIngestThreads)
-      cs[i] = rope_cs(p.plan.turns[i % rp], p.positions[t0 + i / rp], p.plan.magnitude);
+  if (turn) rope_table<kIngestThreads>(p.plan, p.positions + t0, n, cs);
   float w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = norm ? p.k_weight[d0 + i] : 1.f;
@@ -306,11 +304,235 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
     if constexpr (!kBlock) __syncthreads();
   }
   if constexpr (kBlock) __syncthreads();
-  (void)ES;
 }
 
+// Four codes (channel or token neighbours) of one scale, as a 32-bit word.
+// (Not inlined: it would be there some thirty times, and is reached for one word
+// in thousands where quant4_i8 serves.)
+template <int FMT>
+__device__ __noinline__ uint32_t quant_word(float x0, float x1, float x2, float x3, float s) {
+  return quant_byte<FMT>(x0, s) | (uint32_t)quant_byte<FMT>(x1, s) << 8 |
+         (uint32_t)quant_byte<FMT>(x2, s) << 16 | (uint32_t)quant_byte<FMT>(x3, s) << 24;
+}
+
+// The same with the scale's reciprocal where the format is INT8 (see quant4_i8).
+template <int FMT>
+__device__ __forceinline__ uint32_t quant_word_fast(const float (&x)[4], float s, float inv) {
+  if constexpr (FMT == FMT_INT8_BLOCK || FMT == FMT_INT8_GROUP) {
+    bool ok = inv > 0.f;
+    const uint32_t w = quant4_i8(x, inv, ok);
+    if (ok) return w;
+  }
+  return quant_word<FMT>(x[0], x[1], x[2], x[3], s);
+}
+
+// A whole block of tokens (t0 .. t0+bs-1 in the order of their slots).  A lane
+// holds 8 channels of the four tokens that share V words (2j, 2j+1, 2j+8, 2j+9 of
+// a sub-tile), so that both K words (4 channels of a token) and V words (those 4
+// tokens of a channel) are complete in one lane and go straight to the page, a
+// sector per 8 of them; only the one scale of a block passes through shared
+// memory.  A warp's unit is 8 such tokens of one head of 128 channels (16 of one of
+// 64): 32 values a lane.  (Whole sub-tiles, 64 values, left an SM 16 warps and the
+// kernel waiting for its loads: 75 us for 16384 tokens x 8 heads.)
+template <int FMT>
+constexpr bool whole_blocks() {
+  return FMT != FMT_INT4_GROUP && FMT != FMT_INT8_TOKEN && FMT != FMT_FP8_TOKEN;
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared& sh, float2* cs,
+                                             int64_t t0, int64_t blk, int h0, int h1, int kv) {
+  constexpr int LPH = D / 8, RG = 32 / LPH;
+  constexpr int UPT = 4 / RG;  // units per sub-tile
+  constexpr bool kBlock = fmt_block(FMT);
+  constexpr float kTop = fmt_e4m3(FMT) ? 448.f : 127.f;
+  const PoolView& pool = p.pool;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ci = lane % LPH, rg = lane / LPH;
+  const int bs = pool.bs;
+  const int units = (bs >> 4) * UPT;                  // of one head
+  const int wph = min(units, kIngestWarps);           // warps per head
+  const int upw = units / wph;                        // units per warp: 1, or 2 (64 tokens x 128)
+  const int hpi = kIngestWarps / wph;                 // heads at a time
+  const int r = p.plan.rotary_dim, rp = r >> 1;
+  const bool turn = kv == 0 && r > 0, norm = kv == 0 && p.k_weight != nullptr;
+  const bool inter = p.plan.layout == KVQ_ROPE_INTERLEAVED;
+  // Half layout: a lane takes both channels of its pairs (as in rope_tokens),
+  // unless scale groups are narrower than the head, whose lanes must adjoin.
+  const bool split = turn && !inter && (FMT != FMT_INT8_GROUP || pool.ng == 1) && 8 * ci < r;
+  const int da = split ? 4 * ci : 8 * ci, db = split ? 4 * ci + rp : 8 * ci + 4;
+  if (turn) rope_table<kIngestThreads>(p.plan, p.positions + t0, bs, cs);
+  float w[8];
+  if (norm)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = p.k_weight[da + i];
+      w[4 + i] = p.k_weight[db + i];
+    }
+  // K words of token 2j + (c & 1) + 8 (c >> 1): 64 bytes further for c & 1, half a
+  // sub-tile for c >> 1
+  constexpr int ES = FMT == FMT_FP16 ? 2 : 1;
+  const int ka = k_tile_offset(0, da, D, ES), kb = k_tile_offset(0, db, D, ES);
+  __syncthreads();
+  for (int hb = h0; hb < h1; hb += hpi) {
+    const int h = hb + warp / wph;
+    const bool act = h < h1;
+    char* page = pool.pages + (blk * pool.Hkv + (act ? h : 0)) * pool.page_bytes;
+    float* scales = reinterpret_cast<float*>(page + 2 * pool.code_bytes);
+    float amax = 0.f, s = 0.f, inv = 0.f;
+    // With several units per warp the first round only finds the block's absmax.
+    const int rounds = kBlock && upw > 1 ? 2 * upw : upw;
+    for (int k = 0; k < rounds; ++k) {
+      const bool last = k >= rounds - upw;
+      const int u = warp % wph * upw + k % upw;
+      const int sub = u / UPT, j = rg + RG * (u % UPT);
+      const int tok = 16 * sub + 2 * j;  // chunk c: token tok + (c & 1) + 8 (c >> 1)
+      uint32_t raw[4][4];
+      const __half* src = static_cast<const __half*>(p.x[kv]) + (t0 + tok) * p.stride[kv] + h * D;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const __half* at = src + ((c & 1) + 8 * (c >> 1)) * p.stride[kv];
+        const uint2 a = act ? *reinterpret_cast<const uint2*>(at + da) : make_uint2(0, 0);
+        const uint2 b = act ? *reinterpret_cast<const uint2*>(at + db) : make_uint2(0, 0);
+        raw[c][0] = a.x;
+        raw[c][1] = a.y;
+        raw[c][2] = b.x;
+        raw[c][3] = b.y;
+      }
+      float x[4][8];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        widen8(make_uint4(raw[c][0], raw[c][1], raw[c][2], raw[c][3]), p.bf16, x[c]);
+      if (norm)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) norm8<D>(x[c], w, p.eps);
+      if (turn) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2* t = cs + (tok + (c & 1) + 8 * (c >> 1)) * rp;
+          if (split) {
+            const float4 c0 = *reinterpret_cast<const float4*>(t + 4 * ci);
+            const float4 c1 = *reinterpret_cast<const float4*>(t + 4 * ci + 2);
+            const float cv[4] = {c0.x, c0.z, c1.x, c1.z}, sv[4] = {c0.y, c0.w, c1.y, c1.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = x[c][i], d = x[c][4 + i];
+              x[c][i] = fmaf(a, cv[i], -d * sv[i]);
+              x[c][4 + i] = fmaf(a, sv[i], d * cv[i]);
+            }
+          } else if (inter || (FMT == FMT_INT8_GROUP && pool.ng > 1)) {
+            rotate8<D>(x[c], ci, r, inter, t);
+          }
+        }
+      }
+      if constexpr (kBlock) {
+        if (k < upw) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[c][i]));
+        }
+        if (k == upw - 1) {  // every unit of the block seen: its warps agree on the scale
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          if (wph > 1) {
+            if (lane == 0) sh.red[warp] = amax;
+            __syncthreads();
+            for (int i = 0; i < wph; ++i) amax = fmaxf(amax, sh.red[warp / wph * wph + i]);
+            __syncthreads();
+          }
+          s = __fdiv_rn(amax, kTop);
+          inv = quant_inverse(s);
+          if (act && warp % wph == 0 && lane == 0) scales[kv] = s;
+        }
+      }
+      if (!last || !act) continue;
+      char* tile = page + (kv == 0 ? 0 : pool.code_bytes) + sub * pool.sub_bytes;
+      if constexpr (FMT == FMT_FP16) {
+        uint32_t o[4][4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 v = narrow8(x[c]);
+          o[c][0] = v.x;
+          o[c][1] = v.y;
+          o[c][2] = v.z;
+          o[c][3] = v.w;
+        }
+        if (kv == 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            char* at = tile + (2 * j + (c & 1)) * 64 + (c >> 1) * (16 * D);
+            *reinterpret_cast<uint2*>(at + ka) = make_uint2(o[c][0], o[c][1]);
+            *reinterpret_cast<uint2*>(at + kb) = make_uint2(o[c][2], o[c][3]);
+          }
+        } else {
+          char* at = tile + v_tile_offset(2 * j, da, D, 2);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t sel = i & 1 ? 0x7632u : 0x5410u;
+            *reinterpret_cast<uint2*>(at + 64 * i) =
+                make_uint2(prmt(o[0][i >> 1], o[1][i >> 1], sel), prmt(o[2][i >> 1], o[3][i >> 1], sel));
+          }
+        }
+      } else {
+        uint32_t k4[4][2];  // per token: channels da .. da+3 and db .. db+3
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (FMT == FMT_INT8_GROUP) {
+            float a = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[c][i]));
+            for (int o = pool.group >> 4; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            s = __fdiv_rn(a, kTop);
+            inv = quant_inverse(s);
+            if (8 * ci % pool.group == 0)
+              scales[(kv * bs + tok + (c & 1) + 8 * (c >> 1)) * pool.ng + 8 * ci / pool.group] = s;
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float y[4] = {x[c][4 * q], x[c][4 * q + 1], x[c][4 * q + 2], x[c][4 * q + 3]};
+            if constexpr (FMT == FMT_INT8_CHANNEL) {
+              const float* chs = pool.chan_scales + ((int64_t)kv * pool.Hkv + h) * D + (q ? db : da);
+              uint32_t v = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v |= (uint32_t)quant_i8(y[i], chs[i]) << (8 * i);
+              k4[c][q] = v;
+            } else {
+              k4[c][q] = quant_word_fast<FMT>(y, s, inv);
+            }
+          }
+        }
+        if (kv == 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            char* at = tile + (2 * j + (c & 1)) * 64 + (c >> 1) * (8 * D);
+            *reinterpret_cast<uint32_t*>(at + ka) = k4[c][0];
+            *reinterpret_cast<uint32_t*>(at + kb) = k4[c][1];
+          }
+        } else {  // transpose 4 tokens x 4 channels, twice
+          char* at = tile + v_tile_offset(2 * j, da, D, 1);
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t a = prmt(k4[0][q], k4[1][q], 0x5140u), b = prmt(k4[2][q], k4[3][q], 0x5140u);
+            const uint32_t c = prmt(k4[0][q], k4[1][q], 0x7362u), d = prmt(k4[2][q], k4[3][q], 0x7362u);
+            *reinterpret_cast<uint32_t*>(at + 64 * (4 * q)) = prmt(a, b, 0x5410u);
+            *reinterpret_cast<uint32_t*>(at + 64 * (4 * q + 1)) = prmt(a, b, 0x7632u);
+            *reinterpret_cast<uint32_t*>(at + 64 * (4 * q + 2)) = prmt(c, d, 0x5410u);
+            *reinterpret_cast<uint32_t*>(at + 64 * (4 * q + 3)) = prmt(c, d, 0x7632u);
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// Resident CTAs to compile for: whole blocks need some 80 registers, a run held
+// in registers 8 more per chunk.
+constexpr int ingest_ctas(int cpt) { return cpt <= 2 ? 6 : cpt == 4 ? 5 : 3; }
+
 template <int FMT, int D, int CPT>
-__global__ void __launch_bounds__(kIngestThreads) kvq_ingest_kernel(const __grid_constant__ IngestParams p) {
+__global__ void __launch_bounds__(kIngestThreads, ingest_ctas(CPT)) kvq_ingest_kernel(const __grid_constant__ IngestParams p) {
   extern __shared__ __align__(16) char smem[];
   // The decode-step form launches as a programmatic dependent: wait for what
   // ran before, then let the decode launch (see kvq_append_kernel).
@@ -318,10 +540,19 @@ __global__ void __launch_bounds__(kIngestThreads) kvq_ingest_kernel(const __grid
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x >= p.kv_ctas) {
     const int64_t b = blockIdx.x - p.kv_ctas;
-    const int64_t t0 = b / p.q_parts * p.q_tpc;
-    rope_tokens<D, kIngestThreads>(p.q, p.Hq, RopeRows{}, 0, p.q_inv, p.bf16, p.positions, t0,
-                                   static_cast<int>(min((int64_t)p.q_tpc, p.T - t0)),
-                                   static_cast<int>(b % p.q_parts), p.q_parts, p.eps, p.plan, smem);
+    constexpr int rows = kIngestThreads / (D / 8);
+    const int h = static_cast<int>(b % p.q_parts) * rows + threadIdx.x / (D / 8);
+    auto turn = [&](auto bf, auto in) {
+      rope_tokens<D, decltype(bf)::value, decltype(in)::value>(
+          p.q, p.Hq, RopeRows{}, 0, p.positions, b / p.q_parts, 1, h, p.eps, p.plan,
+          reinterpret_cast<float*>(smem));
+    };
+    using Y = std::true_type;
+    using N = std::false_type;
+    if (p.plan.layout == KVQ_ROPE_INTERLEAVED)
+      p.bf16 ? turn(Y{}, Y{}) : turn(N{}, Y{});
+    else
+      p.bf16 ? turn(Y{}, N{}) : turn(N{}, N{});
     return;
   }
   __shared__ IngestShared sh;
@@ -368,6 +599,14 @@ __global__ void __launch_bounds__(kIngestThreads) kvq_ingest_kernel(const __grid
     int e = i + 1;
     while (e < win && e < i + pool.bs && !(sh.cut[e >> 5] >> (e & 31) & 1)) ++e;
     const int blk = sh.blk[i + 1];
+    if constexpr (whole_blocks<FMT>()) {
+      if (blk >= 0 && e - i == pool.bs && pool.bs >= 16 &&
+          __syncthreads_and(tid >= pool.bs || sh.off[i + min(tid, pool.bs - 1)] == tid)) {
+        ingest_whole<FMT, D>(p, sh, cs, c0 + i, blk, h0, h1, kv);
+        i = e;
+        continue;
+      }
+    }
     if (blk >= 0)
       ingest_run<FMT, D, CPT>(p, sh, tile, cs, c0 + i, e - i, i, blk, h0, h1, kv);
     i = e;
@@ -378,7 +617,7 @@ __global__ void __launch_bounds__(kIngestThreads) kvq_ingest_kernel(const __grid
 // query CTAs' own, if that is more).
 inline int ingest_smem(const PoolView& pool, int rotary_dim) {
   const int kv = pool.code_bytes + pool.bs * rotary_dim / 2 * 8;
-  const int q = rope_smem(rotary_dim, pool.D);
+  const int q = rope_smem(rotary_dim);
   return kv > q ? kv : q;
 }
 

@@ -72,7 +72,9 @@ struct RopeArgs {
   float eps = 0.f;
   const kvq_rope_plan* plan = nullptr;
 };
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+// `beside`: launch while the kernel before it on the stream still runs (which
+// must let its dependents launch and touch nothing that this call touches).
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st, bool beside = false);
 
 // Dequantized fp16 K and V of n slots, [n][Hkv][D] each.
 cudaError_t launch_read_values(const PoolView& pool, const int64_t* slots, int64_t n, __half* k,

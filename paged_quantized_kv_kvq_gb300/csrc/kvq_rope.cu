@@ -11,58 +11,71 @@ namespace kvq {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 320;  // at most; 48 registers let four such CTAs share an SM
 
 struct RopeParams {
   RopeRows rows[2];
   int heads[2];
-  bool bf16;
   const int64_t* positions;
   int64_t T;
   int tpc;    // tokens per CTA
   int parts;  // CTAs a token's rows are spread over
-  uint32_t inv;
   float eps;
   kvq_rope_plan plan;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kRopeThreads) kvq_rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ __align__(16) char smem[rope_smem(D, D)];
+template <int D, bool BF16, bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, 4) kvq_rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ __align__(16) float smem[rope_smem(D) / 4];
   const int64_t t0 = (blockIdx.x / p.parts) * (int64_t)p.tpc;
-  rope_tokens<D, kRopeThreads>(p.rows[0], p.heads[0], p.rows[1], p.heads[1], p.inv, p.bf16,
-                               p.positions, t0, static_cast<int>(min((int64_t)p.tpc, p.T - t0)),
-                               blockIdx.x % p.parts, p.parts, p.eps, p.plan, smem);
+  const int part = blockIdx.x % p.parts, rpc = blockDim.x / (D / 8);  // rows of the CTA
+  rope_tokens<D, BF16, INTER>(p.rows[0], p.heads[0], p.rows[1], p.heads[1], p.positions, t0,
+                              static_cast<int>(min((int64_t)p.tpc, p.T - t0)),
+                              part * rpc + threadIdx.x / (D / 8), p.eps, p.plan, smem);
+}
+
+template <int D>
+cudaError_t run_rope(const cudaLaunchConfig_t& cfg, const RopeParams& p, bool bf16) {
+  if (p.plan.layout == KVQ_ROPE_INTERLEAVED)
+    return bf16 ? cudaLaunchKernelEx(&cfg, kvq_rope_kernel<D, true, true>, p)
+                : cudaLaunchKernelEx(&cfg, kvq_rope_kernel<D, false, true>, p);
+  return bf16 ? cudaLaunchKernelEx(&cfg, kvq_rope_kernel<D, true, false>, p)
+              : cudaLaunchKernelEx(&cfg, kvq_rope_kernel<D, false, false>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st, bool beside) {
   RopeParams p{};
   for (int i = 0; i < 2; ++i) {
     p.rows[i] = RopeRows{a.x[i], a.x_stride[i], a.out[i], a.out_stride[i], a.weight[i]};
     p.heads[i] = a.heads[i];
   }
-  p.bf16 = a.bf16;
   p.positions = a.positions;
   p.T = a.T;
   p.eps = a.eps;
   if (a.plan != nullptr) p.plan = *a.plan;
-  // Few tokens: spread a token's rows over CTAs so that every thread has one
-  // chunk; many: several tokens per CTA share its set-up.
-  const int H = a.heads[0] + a.heads[1];
-  p.inv = rope_inverse(H);
-  const int rpp = kRopeThreads / (a.D / 8);
-  const int passes = (H + rpp - 1) / rpp;
-  p.parts = a.T >= 512 ? 1 : passes;
-  p.tpc = a.T >= 4096 ? kRopeTokens : 1;
+  // A thread takes one head row of up to kRopeTokens tokens; a token's rows are
+  // spread evenly over CTAs of at most 10 warps.  A warp holds 2 rows of 128
+  // channels or 4 of 64.  One token per CTA while that fills the SMs.
+  const int H = a.heads[0] + a.heads[1], rpw = 256 / a.D;
+  const int warps = (H + rpw - 1) / rpw;
+  p.parts = (warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32);
+  // (at least a thread per pair of channels, for the angles)
+  const int threads = std::max(KVQ_ROPE_MAX_PAIRS, 32 * ((warps + p.parts - 1) / p.parts));
+  p.tpc = a.T * p.parts >= 4096 ? kRopeTokens : 1;
   const int64_t grid = (a.T + p.tpc - 1) / p.tpc * p.parts;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (a.D == 64)
-    kvq_rope_kernel<64><<<static_cast<unsigned>(grid), kRopeThreads, 0, st>>>(p);
-  else
-    kvq_rope_kernel<128><<<static_cast<unsigned>(grid), kRopeThreads, 0, st>>>(p);
-  return phase_mark(st, cudaGetLastError());
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return phase_mark(st, a.D == 64 ? run_rope<64>(cfg, p, a.bf16) : run_rope<128>(cfg, p, a.bf16));
 }
 
 }  // namespace kvq

@@ -21,6 +21,7 @@
 #include <cuda_fp16.h>
 
 #include "kvq.h"
+#include "kvq_f32x2.cuh"
 
 namespace kvq {
 
@@ -31,6 +32,19 @@ __device__ __forceinline__ float2 rope_cs(uint64_t turn, int64_t pos, float magn
   float s, c;
   __sincosf(a, &s, &c);  // a = 2 pi * fraction of a turn
   return make_float2(c * magnitude, s * magnitude);
+}
+
+// Cosines and sines of tokens 0 .. n-1 (their positions at `pos`): cs[t][pair].
+// A thread keeps its pair.
+template <int THREADS>
+__device__ __forceinline__ void rope_table(const kvq_rope_plan& plan, const int64_t* pos, int n,
+                                           float2* cs) {
+  static_assert(THREADS % KVQ_ROPE_MAX_PAIRS == 0, "a thread per pair");
+  const int rp = plan.rotary_dim >> 1, q = threadIdx.x % KVQ_ROPE_MAX_PAIRS;
+  if (q >= rp) return;
+  const uint64_t turn = plan.turns[q];
+  for (int t = threadIdx.x / KVQ_ROPE_MAX_PAIRS; t < n; t += THREADS / KVQ_ROPE_MAX_PAIRS)
+    cs[t * rp + q] = rope_cs(turn, pos[t], plan.magnitude);
 }
 
 // 8 values of a 16-byte chunk, widened exactly.
@@ -63,14 +77,22 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
 // calls it (lanes without a row carry zeros).
 template <int D>
 __device__ __forceinline__ void norm8(float (&x)[8], const float (&w)[8], float eps) {
-  float s = 0.f;
+  uint64_t v[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
+  for (int i = 0; i < 4; ++i) v[i] = f2_pack(x[2 * i], x[2 * i + 1]);
+  uint64_t q = f2_mul(v[0], v[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) q = f2_madd(v[i], v[i], q);
+  float s, s1;
+  f2_unpack(q, s, s1);
+  s += s1;
 #pragma unroll
   for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   const float r = rsqrtf(fmaf(s, 1.f / D, eps));
+  const uint64_t rr = f2_pack(r, r);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= r * w[i];
+  for (int i = 0; i < 4; ++i)
+    f2_unpack(f2_mul(v[i], f2_mul(f2_pack(w[2 * i], w[2 * i + 1]), rr)), x[2 * i], x[2 * i + 1]);
 }
 
 // Rotation of chunk `ci` (channels 8ci .. 8ci+7) of a head whose token's cos
@@ -122,132 +144,149 @@ struct RopeRows {
   const float* weight;  // null: no norm
 };
 
-constexpr int kRopeTokens = 4;
+constexpr int kRopeTokens = 4;  // tokens per CTA at most
 
-// Shared memory of rope_tokens: cosines and sines of its tokens, both sets' weights.
-__host__ __device__ constexpr int rope_smem(int rotary_dim, int D) {
-  return kRopeTokens * rotary_dim / 2 * 8 + 2 * D * 4;
+// Shared memory of rope_tokens: cosines, sines and negated sines of its tokens.
+__host__ __device__ constexpr int rope_smem(int rotary_dim) {
+  return kRopeTokens * 3 * (rotary_dim / 2) * 4;
 }
 
-// ceil(2^32 / h), h > 1: the high word of row * that is row / h for row * h < 2^32
-// (here row < kRopeTokens * h + 2 * 32 and h <= 2^14).
-inline uint32_t rope_inverse(int h) {
-  return h > 1 ? static_cast<uint32_t>((0x100000000ull + h - 1) / h) : 0;
-}
-
-// Tokens t0 .. t0+nt-1 (nt <= kRopeTokens) of sets A (hA heads) and B (hB
-// heads), every parts-th stretch of their rows; `inv` = rope_inverse(hA + hB).
+// Head row `h` of tokens t0 .. t0+nt-1 (nt <= kRopeTokens): set A's hA heads
+// followed by set B's hB.  Every thread of the CTA calls it; LPH = D/8
+// consecutive threads share a row (h >= hA + hB: none); at least 64 threads.
 //
-// A pass of the CTA takes one row per D/8 lanes.  In the half layout a lane
-// holds channels 4c .. 4c+3 and, where they are rotated, their partners r/2
-// further on, so that a rotation stays within a lane (two 8-byte accesses, each
-// still whole sectors over the row); otherwise channels 8c .. 8c+7 (one 16-byte
-// access).  Either way its pairs are 4c .. 4c+3.
-// The kernel that uses this is bound by its instructions as much as by HBM: a
-// row's lane costs about 90 of them for its 32 bytes, so the row index is split
-// by a multiplication, and the weights come from shared memory.
-template <int D, int THREADS>
+// In the half layout a lane holds channels 4c .. 4c+3 and, where they are
+// rotated, their partners r/2 further on, so that a rotation stays within a lane
+// (two 8-byte accesses, each still whole sectors over the row); otherwise
+// channels 8c .. 8c+7 (one 16-byte access).  Either way its pairs are
+// 4c .. 4c+3.  The row's pointers and weights are set up once for all nt tokens,
+// whose loads are issued together, and the arithmetic is packed two by two:
+// after HBM it is the instructions that bound this (16384 tokens x 40 heads with
+// norms: 161 per 16 bytes of input and 65 us with one row at a time).
+template <int D, bool BF16, bool INTER>
 __device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const RopeRows& B, int hB,
-                                            uint32_t inv, bool bf16, const int64_t* positions,
-                                            int64_t t0, int nt, int part, int parts, float eps,
-                                            const kvq_rope_plan& plan, char* smem) {
-  constexpr int LPH = D / 8, RPP = THREADS / LPH;  // lanes per head, rows per pass
+                                            const int64_t* positions, int64_t t0, int nt, int h,
+                                            float eps, const kvq_rope_plan& plan, float* smem) {
+  constexpr int LPH = D / 8;
   const int r = plan.rotary_dim, rp = r >> 1;
-  float2* cs = reinterpret_cast<float2*>(smem);
-  float* wsm = reinterpret_cast<float*>(cs + kRopeTokens * rp);
-  for (int i = threadIdx.x; i < nt * rp; i += THREADS)
-    cs[i] = rope_cs(plan.turns[i % rp], positions[t0 + i / rp], plan.magnitude);
-  for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
-    const float* w = i < D ? A.weight : B.weight;
-    wsm[i] = w != nullptr ? w[i % D] : 1.f;
-  }
-  const int ci = threadIdx.x % LPH, row0 = threadIdx.x / LPH;
-  const bool inter = plan.layout == KVQ_ROPE_INTERLEAVED, rot = 8 * ci < r;
-  const bool norm = A.weight != nullptr || B.weight != nullptr;
-  const int da = !inter && rot ? 4 * ci : 8 * ci, db = !inter && rot ? 4 * ci + rp : 8 * ci + 4;
-  const __half* xA = static_cast<const __half*>(A.x) + t0 * A.x_stride;
-  const __half* xB = static_cast<const __half*>(B.x) + t0 * B.x_stride - hA * D;
-  __half* oA = A.out + t0 * A.out_stride;
-  __half* oB = B.out + t0 * B.out_stride - hA * D;
-  __syncthreads();
-  const int H = hA + hB, rows = nt * H;
-  constexpr int U = 2;  // rows in flight per thread
-  for (int base = part * RPP; base < rows; base += parts * RPP * U) {
-    uint2 raw[U][2];
-    int tok[U], head[U];
+  const int ci = threadIdx.x % LPH;
+  const bool rot = 8 * ci < r;
+  const int da = !INTER && rot ? 4 * ci : 8 * ci, db = !INTER && rot ? 4 * ci + rp : 8 * ci + 4;
+  const bool act = h < hA + hB, b = act && h >= hA;
+  const RopeRows& R = b ? B : A;
+  const int64_t at = act ? (b ? h - hA : h) * D : 0;
+  const __half* x = static_cast<const __half*>(R.x) + t0 * R.x_stride + at;
+  const int64_t xs = R.x_stride, os = R.out_stride;
+  uint32_t raw[kRopeTokens][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = base + u * parts * RPP + row0;
-      tok[u] = H > 1 ? static_cast<int>(__umulhi(row, inv)) : row;
-      head[u] = row - tok[u] * H;
-      raw[u][0] = raw[u][1] = make_uint2(0, 0);
-      if (row < rows) {
-        const bool b = head[u] >= hA;
-        const __half* x = (b ? xB : xA) + tok[u] * (b ? B.x_stride : A.x_stride) + head[u] * D;
-        if (inter) {
-          const uint4 v = *reinterpret_cast<const uint4*>(x + da);
-          raw[u][0] = make_uint2(v.x, v.y);
-          raw[u][1] = make_uint2(v.z, v.w);
-        } else {
-          raw[u][0] = *reinterpret_cast<const uint2*>(x + da);
-          raw[u][1] = *reinterpret_cast<const uint2*>(x + db);
-        }
+  for (int t = 0; t < kRopeTokens; ++t) {
+    raw[t][0] = raw[t][1] = raw[t][2] = raw[t][3] = 0;
+    if (act && t < nt) {
+      if constexpr (INTER) {
+        const uint4 v = *reinterpret_cast<const uint4*>(x + t * xs + da);
+        raw[t][0] = v.x;
+        raw[t][1] = v.y;
+        raw[t][2] = v.z;
+        raw[t][3] = v.w;
       } else {
-        tok[u] = -1;
+        const uint2 v = *reinterpret_cast<const uint2*>(x + t * xs + da);
+        const uint2 u = *reinterpret_cast<const uint2*>(x + t * xs + db);
+        raw[t][0] = v.x;
+        raw[t][1] = v.y;
+        raw[t][2] = u.x;
+        raw[t][3] = u.y;
       }
     }
+  }
+  const bool norm = R.weight != nullptr;
+  const bool warp_norm = __any_sync(0xffffffffu, norm);
+  uint64_t w[4];
+  if (warp_norm) {
+    const float4 a = norm ? *reinterpret_cast<const float4*>(R.weight + da) : make_float4(1, 1, 1, 1);
+    const float4 c = norm ? *reinterpret_cast<const float4*>(R.weight + db) : make_float4(1, 1, 1, 1);
+    w[0] = f2_pack(a.x, a.y);
+    w[1] = f2_pack(a.z, a.w);
+    w[2] = f2_pack(c.x, c.y);
+    w[3] = f2_pack(c.z, c.w);
+  }
+  float* cs = smem;  // [nt][3][rp]: cos, sin, -sin
+  const int q = threadIdx.x % KVQ_ROPE_MAX_PAIRS;  // (a division by rp would cost more)
+  if (q < rp)
+    for (int t = threadIdx.x / KVQ_ROPE_MAX_PAIRS; t < nt; t += blockDim.x / KVQ_ROPE_MAX_PAIRS) {
+      const float2 v = rope_cs(plan.turns[q], positions[t0 + t], plan.magnitude);
+      cs[3 * t * rp + q] = v.x;
+      cs[(3 * t + 1) * rp + q] = v.y;
+      cs[(3 * t + 2) * rp + q] = -v.y;
+    }
+  __syncthreads();
+  const float* my = cs + 4 * ci;
+  __half* out = R.out + t0 * os + at;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const bool b = head[u] >= hA;
-      float x[8];
-      widen8(make_uint4(raw[u][0].x, raw[u][0].y, raw[u][1].x, raw[u][1].y), bf16, x);
-      if (norm) {
-        float s = 0.f;
+  for (int t = 0; t < kRopeTokens; ++t) {
+    if (t >= nt) break;
+    uint64_t v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(x[i], x[i], s);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        const float f = (b ? B.weight : A.weight) != nullptr ? rsqrtf(fmaf(s, 1.f / D, eps)) : 1.f;
-        const float4 wa = *reinterpret_cast<const float4*>(wsm + (b ? D : 0) + da);
-        const float4 wb = *reinterpret_cast<const float4*>(wsm + (b ? D : 0) + db);
-        x[0] *= f * wa.x;
-        x[1] *= f * wa.y;
-        x[2] *= f * wa.z;
-        x[3] *= f * wa.w;
-        x[4] *= f * wb.x;
-        x[5] *= f * wb.y;
-        x[6] *= f * wb.z;
-        x[7] *= f * wb.w;
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (BF16) {
+        v[i] = f2_pack(__uint_as_float(raw[t][i] << 16), __uint_as_float(raw[t][i] & 0xFFFF0000u));
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[t][i]));
+        v[i] = f2_pack(f.x, f.y);
       }
-      if (rot) {
-        const float4* t = reinterpret_cast<const float4*>(cs + max(tok[u], 0) * rp + 4 * ci);
-        const float4 c0 = t[0], c1 = t[1];
-        const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
-        if (inter) {
+    }
+    if (warp_norm) {
+      uint64_t q = f2_mul(v[0], v[0]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[2 * i], d = x[2 * i + 1];
-            x[2 * i] = fmaf(a, c[i], -d * s[i]);
-            x[2 * i + 1] = fmaf(a, s[i], d * c[i]);
-          }
-        } else {
+      for (int i = 1; i < 4; ++i) q = f2_madd(v[i], v[i], q);
+      float s, s1;
+      f2_unpack(q, s, s1);
+      s += s1;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = x[i], d = x[4 + i];
-            x[i] = fmaf(a, c[i], -d * s[i]);
-            x[4 + i] = fmaf(a, s[i], d * c[i]);
-          }
+      for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const float f = norm ? rsqrtf(fmaf(s, 1.f / D, eps)) : 1.f;
+      const uint64_t ff = f2_pack(f, f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f2_mul(v[i], f2_mul(w[i], ff));
+    }
+    if (rot) {
+      const float* c = my + 3 * t * rp;
+      const float4 cc = *reinterpret_cast<const float4*>(c);
+      const float4 ss = *reinterpret_cast<const float4*>(c + rp);
+      if constexpr (INTER) {
+        const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float a, d;
+          f2_unpack(v[i], a, d);
+          v[i] = f2_pack(fmaf(a, cv[i], -d * sv[i]), fmaf(a, sv[i], d * cv[i]));
+        }
+      } else {
+        const float4 nn = *reinterpret_cast<const float4*>(c + 2 * rp);
+        const uint64_t c2[2] = {f2_pack(cc.x, cc.y), f2_pack(cc.z, cc.w)};
+        const uint64_t s2[2] = {f2_pack(ss.x, ss.y), f2_pack(ss.z, ss.w)};
+        const uint64_t n2[2] = {f2_pack(nn.x, nn.y), f2_pack(nn.z, nn.w)};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t a = v[i], d = v[2 + i];
+          v[i] = f2_madd(d, n2[i], f2_mul(a, c2[i]));
+          v[2 + i] = f2_madd(a, s2[i], f2_mul(d, c2[i]));
         }
       }
-      if (tok[u] >= 0) {
-        __half* out = (b ? oB : oA) + tok[u] * (b ? B.out_stride : A.out_stride) + head[u] * D;
-        const uint4 o = narrow8(x);
-        if (inter) {
-          *reinterpret_cast<uint4*>(out + da) = o;
-        } else {
-          *reinterpret_cast<uint2*>(out + da) = make_uint2(o.x, o.y);
-          *reinterpret_cast<uint2*>(out + db) = make_uint2(o.z, o.w);
-        }
+    }
+    if (act) {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, d;
+        f2_unpack(v[i], a, d);
+        const __half2 hh = __floats2half2_rn(a, d);
+        o[i] = *reinterpret_cast<const uint32_t*>(&hh);
+      }
+      if constexpr (INTER) {
+        *reinterpret_cast<uint4*>(out + t * os + da) = make_uint4(o[0], o[1], o[2], o[3]);
+      } else {
+        *reinterpret_cast<uint2*>(out + t * os + da) = make_uint2(o[0], o[1]);
+        *reinterpret_cast<uint2*>(out + t * os + db) = make_uint2(o[2], o[3]);
       }
     }
   }

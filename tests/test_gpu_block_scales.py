@@ -105,6 +105,48 @@ def test_append_of_many_tokens(fmt, bs, T):
     pool2.close()
 
 
+@pytest.mark.parametrize("fmt,group", [(FORMATS[0], 0), (FORMATS[1], 0), (kvq.KVQ_INT8_PER_GROUP, 32)])
+def test_codes_at_the_borders(fmt, group):
+    """Whole blocks of values that sit on and next to the codes' borders, zero blocks,
+    subnormal and huge scales, infinities and NaN: the bits of the definition (for
+    the per-group format, of the append that was there)."""
+    rng = np.random.default_rng(12)
+    nb, hkv, d, bs = 80, 1, 128, 16
+    T = nb * bs
+    x = (rng.integers(-127, 128, (T, hkv, d)) + rng.choice([0, 0.5, -0.5, 0.4999, 0.5001], (T, hkv, d))).astype(np.float32)
+    scale = 2.0 ** rng.integers(-20, 8, (nb, 1, 1, 1))  # absmax 127 * 2^n: exact ties
+    scale[::3] *= rng.random((len(scale[::3]), 1, 1, 1)) + 0.5
+    x = (np.clip(x, -127, 127).reshape(nb, bs, hkv, d) * scale)
+    x[:, 0, :, ::32] = 127 * scale[:, 0]
+    x[5] = 0
+    x[6] = 6e-8 * rng.integers(-3, 4, x[6].shape)
+    x[7] *= 0
+    x[7, 3, 0, 9] = 65504
+    x = x.reshape(T, hkv, d).astype(np.float16)
+    x[:, 0, 1] = np.minimum(x[:, 0, 1], 60000)
+    slots = np.arange(T, dtype=np.int64)
+    pool = kvq.KVPool(nb, bs, hkv, d, fmt, group, device=DEV)
+    assert pool.rope_append(None, None, _t(x), _t(-x), None, _t(slots)) is None
+    codes, scales = pool.read_slots(_t(slots))
+    if group:
+        other = kvq.KVPool(nb, bs, hkv, d, fmt, group, device=DEV)
+        other.append(_t(x), _t(-x), _t(slots))
+        c2, s2 = other.read_slots(_t(slots))
+        assert torch.equal(codes, c2) and torch.equal(scales, s2)
+        x[100:130, 0, 5] = np.nan
+        x[200, 0, 7] = np.inf
+        pool.rope_append(None, None, _t(x), _t(-x), None, _t(slots))
+        other.append(_t(x), _t(-x), _t(slots))
+        for a, b in zip(pool.read_slots(_t(slots)), other.read_slots(_t(slots))):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        other.close()
+    else:
+        ref = BlockCache(fmt, nb, bs, hkv, d)
+        ref.append(x, -x, slots)
+        _check(pool, ref, slots)
+    pool.close()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_out_of_range_slots_are_flagged_and_skipped(fmt):
     rng = np.random.default_rng(3)
