@@ -97,6 +97,8 @@ def header_functions() -> list[str]:
 def lib() -> ctypes.CDLL:
     """The loaded libkvq.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -162,12 +164,28 @@ def _check(st: int, where: str) -> None:
         raise KVQError(st, where)
 
 
-def _stream(stream):
-    import torch
+_torch = None
 
+
+def _th():
+    """torch, imported at the first call that has tensors (the library itself does
+    without it)."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        torch = _th()
+        try:  # the handle itself: building a Stream object costs more than a launch
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            stream = torch.cuda.current_stream()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -179,7 +197,7 @@ def _ptr(t, dtype=None, name="tensor"):
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 # ------------------------------------------------------------------ C ABI
@@ -214,24 +232,21 @@ def kvq_free_pool(pool) -> None:
 
 
 def kvq_set_channel_scales(pool, k_scale, v_scale, stream=None) -> None:
-    import torch
-
+    torch = _th()
     _check(lib().kvq_set_channel_scales(pool, _ptr(k_scale, torch.float32, "k_scale"),
                                         _ptr(v_scale, torch.float32, "v_scale"), _stream(stream)),
            "kvq_set_channel_scales")
 
 
 def kvq_calibrate_channel_scales(pool, k, v, stream=None) -> None:
-    import torch
-
+    torch = _th()
     _check(lib().kvq_calibrate_channel_scales(pool, _ptr(k, torch.float16, "k"),
                                               _ptr(v, torch.float16, "v"), k.shape[0],
                                               _stream(stream)), "kvq_calibrate_channel_scales")
 
 
 def kvq_append(pool, k, v, slot_mapping, stream=None) -> None:
-    import torch
-
+    torch = _th()
     if k.shape != v.shape or k.shape[0] != slot_mapping.numel():
         raise ValueError("k, v must be [T, kv_heads, head_dim] and slot_mapping [T]")
     _check(lib().kvq_append(pool, _ptr(k, torch.float16, "k"), _ptr(v, torch.float16, "v"),
@@ -246,15 +261,15 @@ def _rows_view(t, dtype, name):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    stride = t.stride()
+    if len(stride) != 3 or stride[2] != 1 or stride[1] != t.shape[2]:
         raise ValueError("%s must be [rows, heads, head_dim] with contiguous heads" % name)
-    return ctypes.c_void_p(t.data_ptr()), int(t.stride(0))
+    return t.data_ptr(), stride[0]
 
 
 def kvq_append_strided(pool, k, v, slot_mapping, stream=None) -> None:
     """kvq_append for head slices of wider token rows (per-head mixed precision)."""
-    import torch
-
+    torch = _th()
     kp, ks = _rows_view(k, torch.float16, "k")
     vp, vs = _rows_view(v, torch.float16, "v")
     if ks != vs or k.shape != v.shape or k.shape[0] != slot_mapping.numel():
@@ -273,41 +288,39 @@ def kvq_rope_init(rotary_dim, interleaved=False, scaling=KVQ_ROPE_NONE, base=100
     return plan
 
 
-def _x_rows(t, ref, name):
-    """_rows_view of fp16 or bf16 rows that agree with `ref` in type and tokens."""
-    if t.dtype != ref.dtype or t.shape[0] != ref.shape[0] or t.shape[-1] != ref.shape[-1]:
+def _x_rows(t, dtype, T, D, name):
+    """_rows_view of rows that agree with the others in type, tokens and head_dim,
+    and their heads."""
+    shape = t.shape
+    if t.dtype != dtype or len(shape) != 3 or shape[0] != T or shape[2] != D:
         raise ValueError("%s must have the type, tokens and head_dim of the other rows" % name)
-    return _rows_view(t, ref.dtype, name)
+    ptr, stride = _rows_view(t, dtype, name)
+    return ptr, stride, shape[1]
 
 
-def _x_type(t, name):
-    import torch
-
-    if t.dtype == torch.float16:
+def _x_type(dtype, name):
+    torch = _th()
+    if dtype is torch.float16:
         return KVQ_X_FP16
-    if t.dtype == torch.bfloat16:
+    if dtype is torch.bfloat16:
         return KVQ_X_BF16
-    raise ValueError("%s must be float16 or bfloat16, got %s" % (name, t.dtype))
+    raise ValueError("%s must be float16 or bfloat16, got %s" % (name, dtype))
 
 
 def _weight(w, head_dim, name):
-    import torch
-
     if w is None:
         return None
     if w.numel() != head_dim:
         raise ValueError("%s must be [head_dim]" % name)
-    return _ptr(w, torch.float32, name)
+    return _ptr(w, _th().float32, name)
 
 
 def _positions(plan, positions, T):
-    import torch
-
     if plan is None:
         return None, None
     if positions is None or positions.numel() != T:
         raise ValueError("positions must be [T]")
-    return ctypes.byref(plan), _ptr(positions, torch.int64, "positions")
+    return ctypes.byref(plan), _ptr(positions, _th().int64, "positions")
 
 
 def kvq_rope(plan, q, k, positions, q_out=None, k_out=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -316,26 +329,28 @@ def kvq_rope(plan, q, k, positions, q_out=None, k_out=None, q_weight=None, k_wei
     given) of query rows q [T, Hq, D] and key rows k [T, Hk, D], fp16 or bf16,
     into fp16 rows q_out and k_out (kvq_rope in include/kvq.h).  q or k may be
     None; fp16 rows without an out are turned in place."""
-    import torch
-
+    half = _th().float16
     ref = q if q is not None else k
     if ref is None:
         raise ValueError("q or k must be given")
-    x_type = _x_type(ref, "q" if q is not None else "k")
+    dtype = ref.dtype
+    x_type = _x_type(dtype, "q" if q is not None else "k")
     T, _, D = ref.shape
-    args = []
-    for x, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+
+    def side(x, out, name):
         if x is None:
-            args.append((None, 0, 0, None, 0))
-            continue
-        xp, xs = _x_rows(x, ref, name)
-        out = x if out is None else out
-        op, os_ = _rows_view(out, torch.float16, name + "_out")
-        if out.shape != x.shape:
+            return None, 0, 0, None, 0
+        ptr, stride, heads = _x_rows(x, dtype, T, D, name)
+        if out is None:
+            out = x
+        optr, ostride, oheads = _x_rows(out, half, T, D, name + "_out")
+        if oheads != heads:
             raise ValueError("%s_out must have the shape of %s" % (name, name))
-        args.append((xp, xs, x.shape[1], op, os_))
+        return ptr, stride, heads, optr, ostride
+
+    qp, qs, hq, qo, qos = side(q, q_out, "q")
+    kp, ks, hk, ko, kos = side(k, k_out, "k")
     pl, pos = _positions(plan, positions, T)
-    (qp, qs, hq, qo, qos), (kp, ks, hk, ko, kos) = args
     _check(lib().kvq_rope(pl, x_type, qp, qs, hq, kp, ks, hk, D, pos, T,
                           _weight(q_weight, D, "q_weight"), _weight(k_weight, D, "k_weight"),
                           float(eps), qo, qos, ko, kos, _stream(stream)), "kvq_rope")
@@ -346,22 +361,20 @@ def kvq_rope_append(pool, plan, q, k, v, positions, slot_mapping, q_out=None, q_
     """kvq_rope of q (into fp16 q_out; in place if None) and k, and the append of
     the rotated k and of v to the pool, in one kernel (kvq_rope_append in
     include/kvq.h).  q may be None."""
-    import torch
-
-    x_type = _x_type(k, "k")
+    torch = _th()
+    dtype = k.dtype
+    x_type = _x_type(dtype, "k")
     T, _, D = k.shape
     if v.shape != k.shape or slot_mapping.numel() != T:
         raise ValueError("k, v must be [T, kv_heads, head_dim] and slot_mapping [T]")
-    kp, ks = _rows_view(k, k.dtype, "k")
-    vp, vs = _x_rows(v, k, "v")
+    kp, ks = _rows_view(k, dtype, "k")
+    vp, vs, _ = _x_rows(v, dtype, T, D, "v")
     qp, qs, hq, qo, qos = None, 0, 0, None, 0
     if q is not None:
-        qp, qs = _x_rows(q, k, "q")
-        q_out = q if q_out is None else q_out
-        qo, qos = _rows_view(q_out, torch.float16, "q_out")
-        if q_out.shape != q.shape:
+        qp, qs, hq = _x_rows(q, dtype, T, D, "q")
+        qo, qos, oheads = _x_rows(q if q_out is None else q_out, torch.float16, T, D, "q_out")
+        if oheads != hq:
             raise ValueError("q_out must have the shape of q")
-        hq = q.shape[1]
     pl, pos = _positions(plan, positions, T)
     _check(lib().kvq_rope_append(pool, pl, x_type, qp, qs, hq, kp, ks, vp, vs, pos,
                                  _ptr(slot_mapping, torch.int64, "slot_mapping"), T,
@@ -372,8 +385,7 @@ def kvq_rope_append(pool, plan, q, k, v, positions, slot_mapping, q_out=None, q_
 def kvq_paged_decode_strided(pool, q, block_table, context_lens, max_context_len, sm_scale, out,
                              workspace=None, stream=None) -> None:
     """kvq_paged_decode for head slices of wider q / out rows (per-head mixed precision)."""
-    import torch
-
+    torch = _th()
     qp, qs = _rows_view(q, torch.float16, "q")
     op, os_ = _rows_view(out, torch.float32, "out")
     S, Hq, _ = q.shape
@@ -387,8 +399,7 @@ def kvq_paged_decode_strided(pool, q, block_table, context_lens, max_context_len
 
 def kvq_copy_blocks(pool, src_blocks, dst_blocks, stream=None) -> None:
     """Block dst_blocks[i] becomes a copy of block src_blocks[i] (copy-on-write)."""
-    import torch
-
+    torch = _th()
     if src_blocks.numel() != dst_blocks.numel():
         raise ValueError("src_blocks and dst_blocks must have the same length")
     _check(lib().kvq_copy_blocks(pool, _ptr(src_blocks, torch.int32, "src_blocks"),
@@ -403,8 +414,7 @@ def kvq_decode_workspace_bytes(pool, num_seqs, num_q_heads, max_context_len, spl
 
 def kvq_paged_decode(pool, q, block_table, context_lens, max_context_len, sm_scale, out,
                      workspace=None, split_blocks=0, stream=None) -> None:
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_paged_decode_ex(
@@ -419,8 +429,7 @@ def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm
                          workspace=None, split_blocks=0, stream=None) -> None:
     """kvq_paged_decode that also writes each row's log-sum-exp, lse [S, Hq] fp32
     (kvq_paged_decode_lse in include/kvq.h)."""
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     if lse.shape != (S, Hq):
         raise ValueError("lse must be [num_seqs, num_q_heads]")
@@ -438,8 +447,7 @@ def kvq_attention_weights(pool, q, block_table, context_lens, max_context_len, s
     """Attention weights of the cached tokens, summed over each kv head's Q heads and
     added to decay * prev: scores [S, Hkv, >= max_context_len] fp32
     (kvq_attention_weights in include/kvq.h).  prev may be scores itself."""
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     if scores.dim() != 3 or scores.shape[0] != S or lse.shape != (S, Hq):
         raise ValueError("scores must be [num_seqs, kv_heads, tokens] and lse [num_seqs, num_q_heads]")
@@ -460,8 +468,7 @@ def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, b
     (kvq_evict_blocks in include/kvq.h): scores [S, Hkv, >= max_context_len], kept
     int32 [S, budget_blocks], scores_out [S, Hkv, >= budget_blocks * block_size].
     table_out and lens_out may be block_table and context_lens themselves."""
-    import torch
-
+    torch = _th()
     S = context_lens.numel()
     if scores.dim() != 3 or scores.shape[0] != S or block_table.shape[0] != S:
         raise ValueError("scores must be [num_seqs, kv_heads, tokens] and block_table [num_seqs, blocks]")
@@ -485,8 +492,7 @@ def kvq_decode_step(pool, k_new, v_new, q, block_table, context_lens, max_contex
                     out, workspace=None, stream=None) -> None:
     """Append each sequence's new token at position context_lens[s]-1, then
     decode (kvq_decode_step in include/kvq.h)."""
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     if k_new.shape != v_new.shape or k_new.shape[0] != S:
         raise ValueError("k_new, v_new must be [num_seqs, kv_heads, head_dim]")
@@ -508,8 +514,7 @@ def kvq_cascade_decode(pool, q, block_table, context_lens, max_context_len, pref
                        sm_scale, out, workspace, stream=None) -> None:
     """Decode whose first prefix_blocks blocks (shared by every sequence) are
     attended once for all sequences (kvq_cascade_decode in include/kvq.h)."""
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_cascade_decode(
@@ -523,8 +528,7 @@ def kvq_cascade_decode(pool, q, block_table, context_lens, max_context_len, pref
 def kvq_cascade_decode_step(pool, k_new, v_new, q, block_table, context_lens, max_context_len,
                             prefix_blocks, sm_scale, out, workspace, stream=None) -> None:
     """kvq_decode_step with the shared-prefix cascade decode."""
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     if k_new.shape != v_new.shape or k_new.shape[0] != S:
         raise ValueError("k_new, v_new must be [num_seqs, kv_heads, head_dim]")
@@ -542,8 +546,7 @@ def kvq_prefill(pool, q, q_start, max_q_len, block_table, context_lens, max_cont
                 out, stream=None) -> None:
     """Causal attention of each sequence's new query tokens over its cache
     (kvq_prefill in include/kvq.h).  q: [Tq, Hq, D] fp16, q_start: [S+1] int32."""
-    import torch
-
+    torch = _th()
     Tq, Hq, _ = q.shape
     S = q_start.numel() - 1
     _check(lib().kvq_prefill(
@@ -562,8 +565,7 @@ def kvq_prefill_ex(pool, q, q_start, max_q_len, block_table, context_lens, max_c
     """kvq_prefill in two passes through a caller workspace (kvq_prefill_ex in
     include/kvq.h); workspace: uint8 device tensor of at least
     kvq_prefill_workspace_bytes(...) bytes, or None when that is 0."""
-    import torch
-
+    torch = _th()
     Tq, Hq, _ = q.shape
     S = q_start.numel() - 1
     ws = None if workspace is None else _ptr(workspace, torch.uint8, "workspace")
@@ -579,8 +581,7 @@ def kvq_selftest_decode_timeout(pool, q, block_table, context_lens, max_context_
                                 workspace, wait_tries=20, stream=None) -> None:
     """Decode with one page copy withheld so that a bounded wait runs out
     (kvq_selftest_decode_timeout in include/kvq.h)."""
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_selftest_decode_timeout(
@@ -599,8 +600,7 @@ def kvq_paged_decode_noalloc(pool, q, block_table, context_lens, max_context_len
     """kvq_paged_decode without a workspace argument, for callers that cannot
     allocate device memory: the split scratch is a fixed 16 MiB array inside
     the library (see kvq_paged_decode_noalloc in include/kvq.h)."""
-    import torch
-
+    torch = _th()
     S, Hq, _ = q.shape
     _check(lib().kvq_paged_decode_noalloc(
         pool, _ptr(q, torch.float16, "q"), S, Hq, _ptr(block_table, torch.int32, "block_table"),
@@ -610,8 +610,7 @@ def kvq_paged_decode_noalloc(pool, q, block_table, context_lens, max_context_len
 
 
 def kvq_read_slots(pool, slots, codes_out, scales_out=None, stream=None) -> None:
-    import torch
-
+    torch = _th()
     _check(lib().kvq_read_slots(pool, _ptr(slots, torch.int64, "slots"), slots.numel(),
                                 _ptr(codes_out, None, "codes_out"),
                                 _ptr(scales_out, torch.float32, "scales_out")
@@ -622,8 +621,7 @@ def kvq_read_slots(pool, slots, codes_out, scales_out=None, stream=None) -> None
 def kvq_read_values(pool, slots, k_out, v_out, stream=None) -> None:
     """Cached K and V of the slots as fp16 values, [n, kv_heads, head_dim] each
     (kvq_read_values in include/kvq.h)."""
-    import torch
-
+    torch = _th()
     if k_out.shape != v_out.shape or k_out.shape[0] != slots.numel():
         raise ValueError("k_out, v_out must be [n, kv_heads, head_dim]")
     _check(lib().kvq_read_values(pool, _ptr(slots, torch.int64, "slots"), slots.numel(),
@@ -656,8 +654,7 @@ class KVPool:
 
     def __init__(self, num_blocks, block_size, kv_heads, head_dim, dtype, group=0, device="cuda",
                  fill_byte: int | None = None):
-        import torch
-
+        torch = _th()
         self.num_blocks, self.block_size, self.kv_heads, self.head_dim = (
             num_blocks, block_size, kv_heads, head_dim)
         self.dtype, self.group = dtype, (group if dtype in GROUP_FORMATS else 0)
@@ -688,8 +685,7 @@ class KVPool:
     def rope_append(self, plan, q, k, v, positions, slot_mapping, q_out=None, q_weight=None,
                     k_weight=None, eps=1e-6, stream=None):
         """Rotated (and normed) fp16 queries; keys and values go to the pool."""
-        import torch
-
+        torch = _th()
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
         kvq_rope_append(self.handle, plan, q, k, v, positions, slot_mapping, q_out, q_weight,
@@ -698,8 +694,7 @@ class KVPool:
 
     def decode(self, q, block_table, context_lens, max_context_len, sm_scale=None, out=None,
                split_blocks=0, stream=None):
-        import torch
-
+        torch = _th()
         S, Hq, D = q.shape
         if sm_scale is None:
             sm_scale = D ** -0.5
@@ -713,8 +708,7 @@ class KVPool:
 
     def decode_step(self, k_new, v_new, q, block_table, context_lens, max_context_len,
                     sm_scale=None, out=None, stream=None):
-        import torch
-
+        torch = _th()
         S, Hq, D = q.shape
         if sm_scale is None:
             sm_scale = D ** -0.5
@@ -728,8 +722,7 @@ class KVPool:
 
     def decode_lse(self, q, block_table, context_lens, max_context_len, sm_scale=None, stream=None):
         """decode's output and each row's log-sum-exp [S, Hq]."""
-        import torch
-
+        torch = _th()
         S, Hq, D = q.shape
         out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
         lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
@@ -751,8 +744,7 @@ class KVPool:
     def evict_blocks(self, scores, block_table, context_lens, max_context_len, budget_blocks,
                      sink_blocks=0, recent_blocks=1, stream=None):
         """(table, lens, kept, scores) after the eviction, in new tensors."""
-        import torch
-
+        torch = _th()
         self._check_heads(scores)
         S = context_lens.numel()
         table, lens = torch.empty_like(block_table), torch.empty_like(context_lens)
@@ -769,8 +761,7 @@ class KVPool:
 
     def cascade_decode(self, q, block_table, context_lens, max_context_len, prefix_blocks,
                        sm_scale=None, out=None, stream=None):
-        import torch
-
+        torch = _th()
         S, Hq, D = q.shape
         if sm_scale is None:
             sm_scale = D ** -0.5
@@ -783,8 +774,7 @@ class KVPool:
         return out
 
     def read_slots(self, slots, stream=None):
-        import torch
-
+        torch = _th()
         n = slots.numel()
         cdt = torch.float16 if self.dtype == KVQ_FP16 else (
             torch.uint8 if self.dtype in (KVQ_FP8_E4M3_PER_TOKEN, KVQ_FP8_E5M2,
@@ -802,8 +792,7 @@ class KVPool:
         return codes, scales
 
     def read_values(self, slots, stream=None):
-        import torch
-
+        torch = _th()
         k = torch.empty((slots.numel(), self.kv_heads, self.head_dim), dtype=torch.float16,
                         device=slots.device)
         v = torch.empty_like(k)

@@ -9,12 +9,15 @@
 // no running maximum, no split to join, no workspace.
 //
 // Bound: HBM -- the K half of the pages once (half of a decode's bytes) and
-// 8 bytes of scores per (token, kv head).  A warp takes one stretch of tokens
-// of one (sequence, kv head) and loads all of its K words before the first
-// product, straight into the registers that are its tensor-core fragments
-// (pages are stored in that order); nothing passes through shared memory.  The
-// Q heads sit on the n dimension of mma.m16n8k16 as in the decode; groups of
-// more than 8 heads read the stretch again per 8, from L1.
+// 8 bytes of scores per (token, kv head).  A warp walks a stretch of tokens of one
+// (sequence, kv head), 4 KB of K words a step, straight into the registers that
+// are its tensor-core fragments (pages are stored in that order); nothing passes
+// through shared memory.  The next step's words are loaded before this step's
+// products, so that 16 warps keep 64 KB an SM in flight throughout; one step per
+// warp, without that overlap, left the loads of 10 warps waiting behind three
+// round trips (lengths, table, pages): 110 us for 8 x 32768 tokens of INT8 blocks.
+// The Q heads sit on the n dimension of mma.m16n8k16 as in the decode; groups of
+// more than 8 heads take their products 8 at a time.
 #pragma once
 #include "kvq_decode_impl.cuh"
 #include "kvq_internal.h"
@@ -23,11 +26,17 @@ namespace kvq {
 
 constexpr int kWeightsWarps = 4;
 
-// 16-token sub-tiles per warp: 64 tokens, 32 for fp16 codes (their words would
-// take 128 registers).
-template <int FMT>
+// 16-token sub-tiles per step: 4 KB of codes (INT4: 2 KB).
+template <int FMT, int D>
 constexpr int weights_tiles() {
-  return FMT == FMT_FP16 ? 2 : 4;
+  return 256 / D / (FMT == FMT_FP16 ? 2 : 1);
+}
+// Resident CTAs to compile for: two steps' words and a head tile's fragments fit
+// 128 registers; per-channel scales keep a second set of fragments, INT4 twice the
+// sub-tiles' sums, narrow groups a scale each per token.
+template <int FMT, int NG>
+constexpr int weights_ctas() {
+  return NG > 2 ? 2 : FMT == FMT_INT8_CHANNEL || FMT == FMT_INT4_GROUP || NG > 1 ? 3 : 4;
 }
 
 struct WeightsParams {
@@ -37,158 +46,178 @@ struct WeightsParams {
   float* scores;
   int64_t stride;
   float decay;
+  int per;     // tokens per warp (a multiple of a step's)
   int nchunk;  // CTAs per (sequence, kv head)
 };
 
 template <int FMT, int D, int NG>
-__global__ void __launch_bounds__(kWeightsWarps * 32) kvq_weights_kernel(const __grid_constant__ WeightsParams p) {
+__global__ void __launch_bounds__(kWeightsWarps * 32, weights_ctas<FMT, NG>())
+    kvq_weights_kernel(const __grid_constant__ WeightsParams p) {
   using T = FmtTraits<FMT>;
   constexpr int KS = D / 16, KPG = KS / NG, SUB = KPG >= 2 ? 2 : 1;
   constexpr int NU32 = lane_words<FMT, D>(), NC = NU32 / 4;  // 32-bit words, 16-byte chunks per lane
-  constexpr int TL = weights_tiles<FMT>();
+  constexpr int TL = weights_tiles<FMT, D>();
   constexpr int NS = T::group_scales ? NG : 1;
+  const float kInf = __int_as_float(0x7f800000u);
   const PoolView& pool = p.d.pool;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, j = lane & 3;
   const int sh = blockIdx.x / p.nchunk, s = sh / pool.Hkv, h = sh - s * pool.Hkv;
-  const int t0 = ((blockIdx.x - sh * p.nchunk) * kWeightsWarps + warp) * 16 * TL;
+  const int t0 = ((blockIdx.x - sh * p.nchunk) * kWeightsWarps + warp) * p.per;
   int L = p.d.lens[s];
   if (L > p.d.max_ctx) {
     if (t0 == 0 && h == 0 && lane == 0) set_error(pool.err, ERR_RANGE);
     L = p.d.max_ctx;
   }
   if (t0 >= L) return;
-  const int bs = pool.bs;
-  const int* trow = p.d.table + (int64_t)s * p.d.max_blocks;
+  const int bs = pool.bs, bl = 31 - __clz(bs), end = min(L, t0 + p.per);
+  const int64_t row = ((int64_t)s * pool.Hkv + h) * p.stride;
 
-  // page of the 8 tokens from t, and their offset in it; null when the block
-  // lies outside the pool (its tokens are skipped) or t behind the sequence
-  const char* page[2 * TL];
-  int off[2 * TL];
-#pragma unroll
-  for (int i = 0; i < 2 * TL; ++i) {
-    const int t = t0 + 8 * i;
-    page[i] = nullptr;
-    off[i] = t & (bs - 1);
-    if (t < L) {
-      const int phys = trow[t / bs];
-      if (phys >= 0 && (int64_t)phys < pool.num_blocks)
-        page[i] = pool.pages + ((int64_t)phys * pool.Hkv + h) * pool.page_bytes;
-      else if (lane == 0)
-        set_error(pool.err, ERR_RANGE);
+  // Block-table entries of the stretch, one per lane, 32 at a time; an entry
+  // outside the pool is flagged once and skipped.
+  const int* trow = p.d.table + (int64_t)s * p.d.max_blocks;
+  const int n0 = t0 >> bl, n1 = (end - 1) >> bl;
+  int held = n0, entry = 0;
+  auto hold = [&](int n) {  // entries n .. n+31
+    held = n;
+    entry = n + lane <= n1 ? trow[n + lane] : 0;
+    if (entry < 0 || (int64_t)entry >= pool.num_blocks) {
+      entry = -1;
+      if (h == 0) set_error(pool.err, ERR_RANGE);
     }
-  }
-  uint32_t kw[TL][NU32];
-  auto load_k = [&]() {
+  };
+  hold(n0);
+
+  // One step's loads.  ok: bit 2x + b, half b (tokens 8b .. 8b+7) of sub-tile x is there.
+  struct Step {
+    uint32_t kw[TL][NU32];
+    float ks[TL][2][NS];
+    float before[TL];
+    uint32_t ok;
+  };
+  auto fetch = [&](int t, Step& S) {
+    if (((t + 16 * TL - 1) >> bl) - held >= 32) hold(t >> bl);
+    S.ok = 0;
 #pragma unroll
-    for (int x = 0; x < TL; ++x)
+    for (int x = 0; x < TL; ++x) {
+      const char* page[2];
+      int off[2], phys[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int tt = t + 16 * x + 8 * b;
+        phys[b] = __shfl_sync(0xffffffffu, entry, (tt >> bl) - held);
+        off[b] = tt & (bs - 1);
+        page[b] = nullptr;
+        if (tt < end && phys[b] >= 0) {
+          page[b] = pool.pages + ((int64_t)phys[b] * pool.Hkv + h) * pool.page_bytes;
+          S.ok |= 1u << (2 * x + b);
+        }
+      }
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         // chunks of the first half hold tokens 0..7, of the second 8..15
         // (INT4 words hold both; 8-token pages hold a half each)
-        const bool b = FMT != FMT_INT4_GROUP && c >= NC / 2;
-        const char* pg = page[2 * x + b];
+        constexpr bool kBoth = FMT == FMT_INT4_GROUP;
+        const int b = !kBoth && c >= NC / 2 ? 1 : 0;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (pg != nullptr) {
+        if (page[b] != nullptr) {
           const int chunk = bs == 8 && b ? c - NC / 2 : c;
-          v = __ldg(reinterpret_cast<const uint4*>(pg + (off[2 * x + b] >> 4) * pool.sub_bytes +
+          v = __ldg(reinterpret_cast<const uint4*>(page[b] + (off[b] >> 4) * pool.sub_bytes +
                                                    chunk * 512 + lane * 16));
         }
-        kw[x][4 * c] = v.x;
-        kw[x][4 * c + 1] = v.y;
-        kw[x][4 * c + 2] = v.z;
-        kw[x][4 * c + 3] = v.w;
+        S.kw[x][4 * c] = v.x;
+        S.kw[x][4 * c + 1] = v.y;
+        S.kw[x][4 * c + 2] = v.z;
+        S.kw[x][4 * c + 3] = v.w;
       }
-  };
-  load_k();
-  float ks[TL][2][NS];
-  if constexpr (T::row_scales) {
+      if constexpr (T::row_scales) {
 #pragma unroll
-    for (int i = 0; i < 2 * TL; ++i)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int gi = 0; gi < NS; ++gi) {
-        float v = 0.f;
-        if (page[i] != nullptr) {
-          const float* sc = reinterpret_cast<const float*>(page[i] + 2 * pool.code_bytes);
-          if constexpr (T::block_scales) {
-            v = sc[0];
-          } else if constexpr (T::group_scales) {
-            v = sc[(off[i] + g) * NS + gi];
-          } else {
-            const int64_t blk = (page[i] - pool.pages) / ((int64_t)pool.Hkv * pool.page_bytes);
-            v = pool.tok_scales[blk * 2 * bs + off[i] + g];
+          for (int gi = 0; gi < NS; ++gi) {
+            float v = 0.f;
+            if (page[b] != nullptr) {
+              const float* sc = reinterpret_cast<const float*>(page[b] + 2 * pool.code_bytes);
+              if constexpr (T::block_scales) {
+                v = sc[0];
+              } else if constexpr (T::group_scales) {
+                v = sc[(off[b] + g) * NS + gi];
+              } else {
+                v = pool.tok_scales[(int64_t)phys[b] * 2 * bs + off[b] + g];
+              }
+            }
+            S.ks[x][b][gi] = v;
           }
-        }
-        ks[i >> 1][i & 1][gi] = v;
       }
-  }
-  // the accumulated weights so far, of the token this lane writes
-  const int64_t row = ((int64_t)s * pool.Hkv + h) * p.stride;
-  float before[TL];
-#pragma unroll
-  for (int x = 0; x < TL; ++x) {
-    const int t = t0 + 16 * x + 8 * (j & 1) + g;
-    before[x] = p.prev != nullptr && j < 2 && t < L ? p.prev[row + t] : 0.f;
-  }
+      // the accumulated weight so far of the token this lane writes
+      const int tw = t + 16 * x + 8 * (j & 1) + g;
+      S.before[x] = p.prev != nullptr && j < 2 && tw < end ? p.prev[row + tw] : 0.f;
+    }
+  };
 
-  float w[TL][2];
-#pragma unroll
-  for (int x = 0; x < TL; ++x) w[x][0] = w[x][1] = 0.f;
-  for (int ht = 0; ht < p.d.n_ht; ++ht) {
-    if (ht > 0) load_k();
-    uint32_t qb[KS][2];
-    uint32_t ql[T::channel ? KS : 1][2];
-    float csc;
+  uint32_t qb[KS][2];
+  uint32_t ql[T::channel ? KS : 1][2];
+  float csc, lse2[2];
+  auto load_heads = [&](int ht) {
     load_q<FMT, D>(p.d, s, h, ht, lane, qb, ql, csc);
     // heads 2j, 2j+1 of the tile; one that is not there, or attends nothing, weighs 0
-    float lse2[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       const int hq = 8 * ht + 2 * j + c;
-      const float v = hq < p.d.G ? p.lse[(int64_t)s * p.d.Hq + h * p.d.G + hq] : __int_as_float(0xff800000u);
-      lse2[c] = v == __int_as_float(0xff800000u) ? __int_as_float(0x7f800000u) : v * 1.4426950408889634f;
+      const float v = hq < p.d.G ? p.lse[(int64_t)s * p.d.Hq + h * p.d.G + hq] : -kInf;
+      lse2[c] = v == -kInf ? kInf : v * 1.4426950408889634f;
+    }
+  };
+
+  Step cur, nxt;
+  fetch(t0, cur);
+  if (p.d.n_ht == 1) load_heads(0);
+  for (int t = t0; t < end; t += 16 * TL) {
+    if (t + 16 * TL < end) fetch(t + 16 * TL, nxt);
+    float w[TL][2];
+#pragma unroll
+    for (int x = 0; x < TL; ++x) w[x][0] = w[x][1] = 0.f;
+    for (int ht = 0; ht < p.d.n_ht; ++ht) {
+      if (p.d.n_ht > 1) load_heads(ht);
+#pragma unroll
+      for (int x = 0; x < TL; ++x) {
+        float acc[NG * SUB][4];
+#pragma unroll
+        for (int a = 0; a < NG * SUB; ++a) acc[a][0] = acc[a][1] = acc[a][2] = acc[a][3] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+          const int ai = (kk / KPG) * SUB + (SUB == 2 ? (kk & 1) : 0);
+          uint32_t a0, a1, a2, a3;
+          k_frag<FMT, D>(cur.kw[x], kk, a0, a1, a2, a3);
+          mma_16816(acc[ai], a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
+          if constexpr (T::channel) mma_16816(acc[ai], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // tokens g and g + 8
+          float z0 = -lse2[0], z1 = -lse2[1];
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) {
+            const float a = SUB == 2 ? acc[gi * SUB][2 * r] + acc[gi * SUB + 1][2 * r] : acc[gi][2 * r];
+            const float b = SUB == 2 ? acc[gi * SUB][2 * r + 1] + acc[gi * SUB + 1][2 * r + 1] : acc[gi][2 * r + 1];
+            const float sc = T::row_scales ? csc * cur.ks[x][r][T::group_scales ? gi : 0] : csc;
+            z0 = fmaf(a, sc, z0);
+            z1 = fmaf(b, sc, z1);
+          }
+          w[x][r] += (lse2[0] == kInf ? 0.f : fast_exp2(z0)) + (lse2[1] == kInf ? 0.f : fast_exp2(z1));
+        }
+      }
     }
 #pragma unroll
     for (int x = 0; x < TL; ++x) {
-      float acc[NG * SUB][4];
-#pragma unroll
-      for (int a = 0; a < NG * SUB; ++a) acc[a][0] = acc[a][1] = acc[a][2] = acc[a][3] = 0.f;
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        const int ai = (kk / KPG) * SUB + (SUB == 2 ? (kk & 1) : 0);
-        uint32_t a0, a1, a2, a3;
-        k_frag<FMT, D>(kw[x], kk, a0, a1, a2, a3);
-        mma_16816(acc[ai], a0, a1, a2, a3, qb[kk][0], qb[kk][1]);
-        if constexpr (T::channel) mma_16816(acc[ai], a0, a1, a2, a3, ql[kk][0], ql[kk][1]);
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {  // tokens g and g + 8
-        float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-        for (int gi = 0; gi < NG; ++gi) {
-          const float a = SUB == 2 ? acc[gi * SUB][2 * r] + acc[gi * SUB + 1][2 * r] : acc[gi][2 * r];
-          const float b = SUB == 2 ? acc[gi * SUB][2 * r + 1] + acc[gi * SUB + 1][2 * r + 1] : acc[gi][2 * r + 1];
-          const float sc = T::row_scales ? csc * ks[x][r][T::group_scales ? gi : 0] : csc;
-          z0 = fmaf(a, sc, z0);
-          z1 = fmaf(b, sc, z1);
-        }
-        w[x][r] += fast_exp2(z0 - lse2[0]) + fast_exp2(z1 - lse2[1]);
-      }
+      // the sum over the lanes' heads; lane j = 0 takes token g, j = 1 token g + 8
+      const float give = j & 1 ? w[x][0] : w[x][1];
+      float mine = (j & 1 ? w[x][1] : w[x][0]) + __shfl_xor_sync(0xffffffffu, give, 1);
+      mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+      const int tw = t + 16 * x + 8 * (j & 1) + g;
+      if (j < 2 && tw < end && (cur.ok >> (2 * x + j) & 1))
+        p.scores[row + tw] = fmaf(p.decay, cur.before[x], mine);
     }
-  }
-#pragma unroll
-  for (int x = 0; x < TL; ++x) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      w[x][r] += __shfl_xor_sync(0xffffffffu, w[x][r], 1);
-      w[x][r] += __shfl_xor_sync(0xffffffffu, w[x][r], 2);
-    }
-    // lanes j = 0 write token g, lanes j = 1 token g + 8
-    const int t = t0 + 16 * x + 8 * (j & 1) + g;
-    if (j < 2 && t < L && page[2 * x + 1] != nullptr && j == 1)
-      p.scores[row + t] = fmaf(p.decay, before[x], w[x][1]);
-    else if (j == 0 && t < L && page[2 * x] != nullptr)
-      p.scores[row + t] = fmaf(p.decay, before[x], w[x][0]);
+    cur = nxt;
   }
 }
 
@@ -200,8 +229,14 @@ struct WeightsLaunch {
 template <int FMT, int D, int NG>
 cudaError_t run_weights(const WeightsLaunch& l) {
   WeightsParams p = l.p;
-  constexpr int per = kWeightsWarps * 16 * weights_tiles<FMT>();
-  p.nchunk = (p.d.max_ctx + per - 1) / per;
+  // Tokens per warp: whole steps, as many as leave every SM four times the warps
+  // it holds (a warp's first loads wait; the ragged ends of sequences idle), 512
+  // at most.
+  constexpr int step = 16 * weights_tiles<FMT, D>();
+  const int64_t tokens = (int64_t)p.d.max_ctx * p.d.S * p.d.pool.Hkv;
+  const int64_t want = tokens / (152 * 16 * 4) / step * step;
+  p.per = static_cast<int>(want < step ? step : want > 512 ? 512 : want);
+  p.nchunk = static_cast<int>((p.d.max_ctx + (int64_t)kWeightsWarps * p.per - 1) / (kWeightsWarps * p.per));
   const int64_t grid = (int64_t)p.nchunk * p.d.S * p.d.pool.Hkv;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   kvq_weights_kernel<FMT, D, NG><<<static_cast<unsigned>(grid), kWeightsWarps * 32, 0, l.st>>>(p);
