@@ -482,6 +482,7 @@ kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int nu
   a.max_blocks = max_blocks_per_seq;
   a.max_ctx = max_context_len;
   a.sm_scale = sm_scale;
+  a.sms = device_sms();
   const cudaError_t e = kvq::launch_weights(a, stream);
   return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
 }

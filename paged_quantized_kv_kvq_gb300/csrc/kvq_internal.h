@@ -94,6 +94,7 @@ struct WeightsArgs {
   float decay;
   int S, Hq, max_blocks, max_ctx;
   float sm_scale;
+  int sms;  // SMs of the device
 };
 cudaError_t launch_weights(const WeightsArgs& a, cudaStream_t st);
 

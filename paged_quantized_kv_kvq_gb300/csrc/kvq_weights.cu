@@ -7,6 +7,7 @@ namespace kvq {
 cudaError_t launch_weights(const WeightsArgs& a, cudaStream_t st) {
   WeightsLaunch l;
   l.st = st;
+  l.sms = a.sms;
   WeightsParams& p = l.p;
   p = WeightsParams{};
   p.d.pool = a.pool;
@@ -21,6 +22,7 @@ cudaError_t launch_weights(const WeightsArgs& a, cudaStream_t st) {
   p.d.max_blocks = a.max_blocks;
   p.d.max_ctx = a.max_ctx;
   p.d.sm_scale_log2 = a.sm_scale * 1.4426950408889634f;
+  p.d.wait_tries = kWaitTries;
   p.lse = a.lse;
   p.prev = a.prev;
   p.scores = a.scores;
