@@ -225,8 +225,8 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   p.bf16 = a.bf16;
   if (a.plan != nullptr) p.plan = *a.plan;
   while ((1 << p.bs_log2) < a.pool.bs) ++p.bs_log2;
-  // Few tokens (a decode step): one per CTA and one head per CTA, for the
-  // latency of a run.  Many: a block's worth of tokens per CTA, and heads for
+  // Few tokens (a decode step, a short prompt): one per CTA, and one head per CTA
+  // (four above 128 tokens) for the latency of a run.  Many: a block's worth of tokens per CTA, and heads for
   // kIngestRounds rounds of its warps, which share its angles.  Formats with one scale per token need every head of
   // a token in one CTA.
   // A long call's query rows go to a kernel of their own, launched beside this
@@ -235,8 +235,10 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   // 154 us in one kernel).
   const bool many = a.T >= 1024;
   const bool tok = a.pool.fmt == FMT_INT8_TOKEN || a.pool.fmt == FMT_FP8_TOKEN;
-  p.tpc = many && a.slots != nullptr ? a.pool.bs : 1;
-  p.hpc = tok ? a.pool.Hkv : many ? kIngestRounds * std::max(1, kIngestWarps * 1024 / (std::max(a.pool.bs, 16) * a.pool.D)) : 1;
+  // (A long call may also be a step of many sequences, each token a run of its own,
+  // which a CTA takes one after the other: 8 tokens per CTA below 16384.)
+  p.tpc = !many || a.slots == nullptr ? 1 : a.T < 16384 ? std::min(a.pool.bs, 8) : a.pool.bs;
+  p.hpc = tok ? a.pool.Hkv : a.T > 128 && !many ? 4 : many ? kIngestRounds * std::max(1, kIngestWarps * 1024 / (std::max(a.pool.bs, 16) * a.pool.D)) : 1;
   p.hsplit = (a.pool.Hkv + p.hpc - 1) / p.hpc;
   p.kv_ctas = (a.T + p.tpc - 1) / p.tpc * p.hsplit * 2;
   int64_t q_ctas = 0;

@@ -63,6 +63,9 @@ struct IngestShared {
   uint32_t has[2];             // offsets the run writes
   float red[kIngestWarps];
   uint32_t tok[kMaxBlock];     // per-token absmax, as bits
+  int grown;                   // heads of a pass whose block scale grew
+  int grown_head[16];
+  float grown_from[16], grown_to[16];
 };
 
 // Slot of token t, or -1 (nothing to store).
@@ -109,6 +112,167 @@ __device__ __forceinline__ float code_value(uint8_t c) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
   else
     return static_cast<float>(static_cast<int>(c) - 128);
+}
+
+// Four codes (channel or token neighbours) of one scale, as a 32-bit word.
+// (Not inlined: it would be there some thirty times, and is reached for one word
+// in thousands where quant4_i8 serves.)
+template <int FMT>
+__device__ __noinline__ uint32_t quant_word(float x0, float x1, float x2, float x3, float s) {
+  return quant_byte<FMT>(x0, s) | (uint32_t)quant_byte<FMT>(x1, s) << 8 |
+         (uint32_t)quant_byte<FMT>(x2, s) << 16 | (uint32_t)quant_byte<FMT>(x3, s) << 24;
+}
+
+// The same with the scale's reciprocal where the format is INT8 (see quant4_i8).
+template <int FMT>
+__device__ __forceinline__ uint32_t quant_word_fast(const float (&x)[4], float s, float inv) {
+  if constexpr (FMT == FMT_INT8_BLOCK || FMT == FMT_INT8_GROUP) {
+    bool ok = inv > 0.f;
+    const uint32_t w = quant4_i8(x, inv, ok);
+    if (ok) return w;
+  }
+  return quant_word<FMT>(x[0], x[1], x[2], x[3], s);
+}
+
+// Four codes at scale s_old, rounded again at s (whose quant_inverse is inv).
+template <int FMT>
+__device__ __forceinline__ uint32_t rescale_word(uint32_t v, float s_old, float s, float inv) {
+  float x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = code_value<FMT>(v >> (8 * e) & 0xFF) * s_old;
+  return quant_word_fast<FMT>(x, s, inv);
+}
+
+// A run of one token, K or V of every head: a row of lanes per head, a decode
+// step's form.  Nothing is staged; with one scale per block the codes that the
+// block keeps are touched only where its scale grows.
+template <int FMT, int D>
+__device__ __forceinline__ void ingest_token(const IngestParams& p, IngestShared& sh, float2* cs,
+                                             int64_t t, int off, int64_t blk, int kv, uint4 first) {
+  constexpr int LPH = D / 8, RPP = kIngestThreads / LPH;
+  constexpr bool kBlock = fmt_block(FMT);
+  constexpr bool kToken = FMT == FMT_INT8_TOKEN || FMT == FMT_FP8_TOKEN;
+  constexpr float kTop = fmt_e4m3(FMT) ? 448.f : FMT == FMT_INT4_GROUP ? 7.f : 127.f;
+  const PoolView& pool = p.pool;
+  const int tid = threadIdx.x, ci = tid % LPH, r0 = tid / LPH, d0 = 8 * ci;
+  const int bs = pool.bs, tt = off & 15, r = p.plan.rotary_dim;
+  const bool turn = kv == 0 && r > 0, norm = kv == 0 && p.k_weight != nullptr;
+  if (turn) rope_table<kIngestThreads>(p.plan, p.positions + t, 1, cs);
+  if (tid == 0) {
+    sh.tok[0] = 0;
+    sh.grown = 0;
+  }
+  float w[8];
+  if (norm)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = p.k_weight[d0 + i];
+  __syncthreads();
+  float x[8];
+  auto load = [&](int hb) {
+    const int h = hb + r0;
+    uint4 raw = first;
+    if (hb > 0)
+      raw = h < pool.Hkv ? *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.x[kv]) +
+                                                           t * p.stride[kv] + h * D + d0)
+                         : make_uint4(0, 0, 0, 0);
+    widen8(raw, p.bf16, x);
+    if (norm) norm8<D>(x, w, p.eps);
+    if (turn) rotate8<D>(x, ci, r, p.plan.layout == KVQ_ROPE_INTERLEAVED, cs);
+  };
+  auto absmax = [&](int lanes) {  // over the chunk and its neighbours
+    float a = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
+    for (int o = lanes >> 1; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+  };
+  float s_tok = 0.f;
+  if constexpr (kToken) {  // the scale of a token spans every head
+    for (int hb = 0; hb < pool.Hkv; hb += RPP) {
+      load(hb);
+      const float a = absmax(32);
+      if ((tid & 31) == 0) atomicMax(&sh.tok[0], __float_as_uint(a));
+    }
+    __syncthreads();
+    s_tok = __fdiv_rn(__uint_as_float(sh.tok[0]), kTop);
+    if (tid == 0) pool.tok_scales[(blk * 2 + kv) * bs + off] = s_tok;
+  }
+  for (int hb = 0; hb < pool.Hkv; hb += RPP) {
+    if (!kToken || pool.Hkv > RPP) load(hb);
+    const int h = hb + r0;
+    const bool act = h < pool.Hkv;
+    char* page = pool.pages + (blk * pool.Hkv + (act ? h : 0)) * pool.page_bytes;
+    char* codes = page + (kv == 0 ? 0 : pool.code_bytes);
+    float* scales = reinterpret_cast<float*>(page + 2 * pool.code_bytes);
+    float s = s_tok;
+    if constexpr (kBlock) {
+      const float a = absmax(LPH);
+      const float s_old = off == 0 || !act ? 0.f : scales[kv];
+      s = fmaxf(s_old, __fdiv_rn(a, kTop));
+      if (act && ci == 0 && off != 0 && s > s_old) {
+        const int i = atomicAdd(&sh.grown, 1);
+        sh.grown_head[i] = h;
+        sh.grown_from[i] = s_old;
+        sh.grown_to[i] = s;
+      }
+      __syncthreads();  // (every lane has read the old scales)
+      const int grown = sh.grown;
+      for (int i = 0; i < grown; ++i) {
+        uint4* tile = reinterpret_cast<uint4*>(pool.pages + (blk * pool.Hkv + sh.grown_head[i]) * pool.page_bytes +
+                                               (kv == 0 ? 0 : pool.code_bytes));
+        const float from = sh.grown_from[i], to = sh.grown_to[i], inv = quant_inverse(to);
+        for (int u = tid; u < pool.code_bytes / 16; u += kIngestThreads) {
+          uint4 v = tile[u];
+          v.x = rescale_word<FMT>(v.x, from, to, inv);
+          v.y = rescale_word<FMT>(v.y, from, to, inv);
+          v.z = rescale_word<FMT>(v.z, from, to, inv);
+          v.w = rescale_word<FMT>(v.w, from, to, inv);
+          tile[u] = v;
+        }
+      }
+      __syncthreads();  // the rescaled codes are there, and the list has been read
+      if (tid == 0) sh.grown = 0;
+      if (act && ci == 0) scales[kv] = s;
+      if (hb + RPP < pool.Hkv) __syncthreads();
+    }
+    char* tile = codes + (off >> 4) * pool.sub_bytes;
+    if constexpr (FMT == FMT_INT8_GROUP || FMT == FMT_INT4_GROUP) {
+      s = __fdiv_rn(absmax(pool.group >> 3), kTop);
+      if (act && d0 % pool.group == 0) scales[(kv * bs + off) * pool.ng + d0 / pool.group] = s;
+    }
+    if (!act) continue;
+    if constexpr (FMT == FMT_FP16) {
+      const uint4 o = narrow8(x);
+      if (kv == 0) {
+        *reinterpret_cast<uint2*>(tile + k_tile_offset(tt, d0, D, 2)) = make_uint2(o.x, o.y);
+        *reinterpret_cast<uint2*>(tile + k_tile_offset(tt, d0 + 4, D, 2)) = make_uint2(o.z, o.w);
+      } else {
+        const uint16_t* half = reinterpret_cast<const uint16_t*>(&o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint16_t*>(tile + v_code_offset(tt, d0 + i, D, 2, bs)) = half[i];
+      }
+    } else if constexpr (FMT == FMT_INT4_GROUP) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        int sh4;
+        const int o = kv == 0 ? k_nibble(tt, d0 + i, sh4) : v_nibble(tt, d0 + i, sh4);
+        store_nibbles(tile + o, 0xFu << sh4, quant_i4(x[i], s) << sh4);
+      }
+    } else {
+      uint8_t q[8];
+      if constexpr (FMT == FMT_INT8_CHANNEL) {
+        const float* chs = pool.chan_scales + ((int64_t)kv * pool.Hkv + h) * D + d0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = quant_byte<FMT>(x[i], chs[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = quant_byte<FMT>(x[i], s);
+      }
+      store_codes8(codes, kv, off, d0, D, bs, pool.sub_bytes, q);
+    }
+  }
+  __syncthreads();
 }
 
 // One run: tokens t0 .. t0+n-1 of the call (window indices w0 ..), block blk.
@@ -211,18 +375,12 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
 #pragma unroll
       for (int i = 1; i < kIngestWarps; ++i) a = fmaxf(a, sh.red[i]);
       s_block = fmaxf(s_old, __fdiv_rn(a, kTop));
+      const float inv_block = quant_inverse(s_block);
       // the codes the block keeps
       const uint32_t zero = fmt_e4m3(FMT) ? 0u : 0x80808080u;
       for (int i = tid; i < pool.code_bytes / 4; i += kIngestThreads) {
         uint32_t v = fresh ? zero : reinterpret_cast<const uint32_t*>(codes)[i];
-        if (!fresh && s_block > s_old) {
-          uint32_t out = 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            out |= (uint32_t)quant_byte<FMT>(code_value<FMT>(v >> (8 * e) & 0xFF) * s_old, s_block)
-                   << (8 * e);
-          v = out;
-        }
+        if (!fresh && s_block > s_old) v = rescale_word<FMT>(v, s_old, s_block, inv_block);
         reinterpret_cast<uint32_t*>(tile)[i] = v;
       }
       if (tid == 0) scales[kv] = s_block;
@@ -304,26 +462,6 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
     if constexpr (!kBlock) __syncthreads();
   }
   if constexpr (kBlock) __syncthreads();
-}
-
-// Four codes (channel or token neighbours) of one scale, as a 32-bit word.
-// (Not inlined: it would be there some thirty times, and is reached for one word
-// in thousands where quant4_i8 serves.)
-template <int FMT>
-__device__ __noinline__ uint32_t quant_word(float x0, float x1, float x2, float x3, float s) {
-  return quant_byte<FMT>(x0, s) | (uint32_t)quant_byte<FMT>(x1, s) << 8 |
-         (uint32_t)quant_byte<FMT>(x2, s) << 16 | (uint32_t)quant_byte<FMT>(x3, s) << 24;
-}
-
-// The same with the scale's reciprocal where the format is INT8 (see quant4_i8).
-template <int FMT>
-__device__ __forceinline__ uint32_t quant_word_fast(const float (&x)[4], float s, float inv) {
-  if constexpr (FMT == FMT_INT8_BLOCK || FMT == FMT_INT8_GROUP) {
-    bool ok = inv > 0.f;
-    const uint32_t w = quant4_i8(x, inv, ok);
-    if (ok) return w;
-  }
-  return quant_word<FMT>(x[0], x[1], x[2], x[3], s);
 }
 
 // A whole block of tokens (t0 .. t0+bs-1 in the order of their slots).  A lane
@@ -564,6 +702,13 @@ __global__ void __launch_bounds__(kIngestThreads, ingest_ctas(CPT)) kvq_ingest_k
   // Window of tokens c0 .. c0+tpc+bs-1: the runs that begin among the first tpc
   // and, for the last of them, as far as a run can go.
   const int tid = threadIdx.x, lane = tid & 31;
+  // one token per CTA: its row's first chunks come while its slot is looked up
+  auto first_rows = [&](int64_t t) {
+    return tid / (D / 8) < pool.Hkv ? *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.x[kv]) +
+                                                                      t * p.stride[kv] + tid * 8)
+                                    : make_uint4(0, 0, 0, 0);
+  };
+  const uint4 row0 = p.tpc == 1 && h0 == 0 ? first_rows(c0) : make_uint4(0, 0, 0, 0);
   const int win = static_cast<int>(min((int64_t)p.tpc + pool.bs, p.T - c0));
   for (int i = tid; i <= win; i += kIngestThreads) {
     const int64_t t = c0 + i - 1;
@@ -599,6 +744,12 @@ __global__ void __launch_bounds__(kIngestThreads, ingest_ctas(CPT)) kvq_ingest_k
     int e = i + 1;
     while (e < win && e < i + pool.bs && !(sh.cut[e >> 5] >> (e & 31) & 1)) ++e;
     const int blk = sh.blk[i + 1];
+    if (e - i == 1) {  // one token: the CTA of the first heads takes all of them
+      if (blk >= 0 && h0 == 0)
+        ingest_token<FMT, D>(p, sh, cs, c0 + i, sh.off[i], blk, kv, p.tpc == 1 ? row0 : first_rows(c0 + i));
+      i = e;
+      continue;
+    }
     if constexpr (whole_blocks<FMT>()) {
       if (blk >= 0 && e - i == pool.bs && pool.bs >= 16 &&
           __syncthreads_and(tid >= pool.bs || sh.off[i + min(tid, pool.bs - 1)] == tid)) {

@@ -73,7 +73,8 @@ struct RopeArgs {
   const kvq_rope_plan* plan = nullptr;
 };
 // `beside`: launch while the kernel before it on the stream still runs (which
-// must let its dependents launch and touch nothing that this call touches).
+// must let its dependents launch and touch nothing that this call touches); the
+// call's kernel ends after that one.
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st, bool beside = false);
 
 // Dequantized fp16 K and V of n slots, [n][Hkv][D] each.

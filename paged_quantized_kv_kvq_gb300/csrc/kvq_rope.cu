@@ -21,6 +21,7 @@ struct RopeParams {
   int tpc;    // tokens per CTA
   int parts;  // CTAs a token's rows are spread over
   float eps;
+  bool beside;  // launched while the kernel before it runs
   kvq_rope_plan plan;
 };
 
@@ -32,6 +33,10 @@ __global__ void __launch_bounds__(kRopeThreads, 4) kvq_rope_kernel(const __grid_
   rope_tokens<D, BF16, INTER>(p.rows[0], p.heads[0], p.rows[1], p.heads[1], p.positions, t0,
                               static_cast<int>(min((int64_t)p.tpc, p.T - t0)),
                               part * rpc + threadIdx.x / (D / 8), p.eps, p.plan, smem);
+  // A kernel after this one may itself be a programmatic dependent and wait for
+  // this grid alone: so this grid ends no earlier than the one it runs beside.  One
+  // CTA waits for that; all of the other grid's are resident by now.
+  if (p.beside && blockIdx.x == gridDim.x - 1) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D>
@@ -54,6 +59,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st, bool beside) {
   p.positions = a.positions;
   p.T = a.T;
   p.eps = a.eps;
+  p.beside = beside;
   if (a.plan != nullptr) p.plan = *a.plan;
   // A thread takes one head row of up to kRopeTokens tokens; a token's rows are
   // spread evenly over CTAs of at most 10 warps.  A warp holds 2 rows of 128

@@ -37,7 +37,7 @@ def _check(pool, ref, slots):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("bs,hkv,d", [(16, 2, 128), (8, 3, 64), (32, 1, 64), (64, 2, 128), (8, 1, 128),
-                                      (16, 5, 64), (32, 2, 128), (64, 1, 64)])
+                                      (16, 5, 64), (32, 2, 128), (64, 1, 64), (16, 11, 128), (32, 33, 64)])
 def test_append_is_bit_exact(fmt, bs, hkv, d):
     """Prompts (whole, ragged, starting inside a block), single tokens that grow or
     keep a scale, padding, a block begun anew."""
@@ -288,6 +288,34 @@ def test_cascade_prefill_and_copies(fmt, bs):
     kvq.kvq_prefill_ex(pool.handle, _t(qq), _t(start), max(n), _t(table), _t(lens), int(lens.max()), d ** -0.5, got, ws)
     np.testing.assert_allclose(got.cpu().numpy(), want, rtol=0, atol=TOL)
     assert pool.error() == kvq.KVQ_OK
+    pool.close()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("d,hkv", [(128, 3), (64, 18)])
+def test_a_step_of_many_sequences(fmt, d, hkv):
+    """1300 sequences, a token each, into blocks that hold tokens already: the form
+    that takes several runs per CTA."""
+    rng = np.random.default_rng(17)
+    bs, S = 16, 1300
+    pool = kvq.KVPool(S, bs, hkv, d, fmt, device=DEV)
+    ref = BlockCache(fmt, S, bs, hkv, d)
+    perm = rng.permutation(S)
+    have = rng.integers(0, bs, S)
+    for t in range(bs):
+        at = perm[have > t] * bs + t
+        if t < 3 and len(at):  # (three tokens are enough of a past)
+            k, v = _rows(rng, len(at), hkv, d), _rows(rng, len(at), hkv, d)
+            pool.append(_t(k), _t(v), _t(at))
+            ref.append(k, v, at)
+    at = perm * bs + np.minimum(have, 3)
+    at[::41] = -1
+    k, v = _rows(rng, S, hkv, d), _rows(rng, S, hkv, d)
+    pool.append(_t(k), _t(v), _t(at))
+    ref.append(k, v, at)
+    assert pool.error() == kvq.KVQ_OK
+    whole = np.concatenate([perm[i] * bs + np.arange(min(have[i], 3) + 1) for i in range(0, S, 7) if at[i] >= 0])
+    _check(pool, ref, whole)
     pool.close()
 
 

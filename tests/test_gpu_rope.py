@@ -167,7 +167,10 @@ def _plain_pool(fmt, group, nb, bs, hkv, d, chan):
     (32, 3, 1, 64, [50, 1, 64, 33], [0, 9, 0, 0], torch.float16),
     (64, 4, 4, 128, [70, 200], [0, 0], torch.bfloat16),
     (16, 8, 2, 64, [700, 500, 17, 1], [0, 0, 3, 2], torch.bfloat16),         # many tokens, runs cut anywhere
-    (8, 2, 3, 128, [11, 1], [0, 4], torch.float16), (8, 2, 1, 64, [1200], [0], torch.float16)])
+    (8, 2, 3, 128, [11, 1], [0, 4], torch.float16), (8, 2, 1, 64, [1200], [0], torch.float16),
+    (16, 20, 20, 128, [1, 1, 2, 1], [3, 0, 14, 20], torch.bfloat16),         # more heads than a CTA's rows
+    (32, 40, 40, 64, [1] * 150, [s % 37 for s in range(150)], torch.float16),
+    (16, 4, 2, 128, [1] * 1100 + [40, 16], [5] * 1100 + [0, 16], torch.float16)])  # a long call of single tokens
 def test_rope_append(fmt, group, bs, hq, hkv, d, lens, starts, dtype):
     if bs == 8 and fmt == kvq.KVQ_INT4_PER_GROUP:
         pytest.skip("INT4 takes blocks of 16 tokens or more")
