@@ -34,9 +34,19 @@ bool plan_decode(const PoolView& pool, int S, int Hq, int max_ctx, int split_blo
   auto smem_of = [&](int ns) {
     return round_up(W * ns * stage_bytes + W * ns * (8 + 4 * sps) + W * 4 + (S + 1) * 4, 128);
   };
-  const int budget = std::min(80 * 1024, 228 * 1024 / kDecodeCtasPerSm - 1024);
-  int nstage = kDecodeStages;
-  while (nstage > min_stage && smem_of(nstage) > budget) --nstage;
+  auto stages_in = [&](int budget) {
+    int ns = kDecodeStages;
+    while (ns > min_stage && smem_of(ns) > budget) --ns;
+    return ns;
+  };
+  int nstage = stages_in(std::min(80 * 1024, 228 * 1024 / kDecodeCtasPerSm - 1024));
+  // Pools with one scale per block: pages of 32 tokens leave a warp of three CTAs
+  // two stages; two CTAs with three hold as many bytes in flight and let the kernel
+  // have the registers that three make it spill (8 x ~16K tokens, e4m3, blocks of
+  // 32: 70.5 us with three, 64.6 with two; blocks of 16, four stages, 64 x 2048:
+  // 60.8 with three, 64.6 with two).
+  plan->two_ctas = fmt_block(pool.fmt) && nstage < 3;
+  if (plan->two_ctas) nstage = stages_in(228 * 1024 / 2 - 1024);
   const int smem = smem_of(nstage);
   if (smem > 227 * 1024) return false;
   const int G = Hq / pool.Hkv;
@@ -117,6 +127,7 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
   l.smem = plan.smem_bytes;
   l.st = st;
   l.dependent = dependent;
+  l.two_ctas = plan.two_ctas;
   if (fmt_block(a.pool.fmt)) return launch_decode_block(l);
   if (a.pool.bs == 8)
     return a.pool.fmt == FMT_INT8_GROUP ? launch_decode_bs8_group(l) : launch_decode_bs8_misc(l);

@@ -5,11 +5,19 @@
 
 namespace kvq {
 
+namespace {
+
+template <int FMT>
+cudaError_t run_block(const DecodeLaunch& l) {
+  if (l.p.pool.bs == 8) return run_decode_d<FMT, true>(l);
+  if (!l.two_ctas) return run_decode_d<FMT>(l);
+  return l.p.pool.D == 64 ? run_decode<FMT, 64, 1, false, 2>(l) : run_decode<FMT, 128, 1, false, 2>(l);
+}
+
+}  // namespace
+
 cudaError_t launch_decode_block(const DecodeLaunch& l) {
-  const bool fp8 = l.p.pool.fmt == FMT_FP8_BLOCK;
-  if (l.p.pool.bs == 8)
-    return fp8 ? run_decode_d<FMT_FP8_BLOCK, true>(l) : run_decode_d<FMT_INT8_BLOCK, true>(l);
-  return fp8 ? run_decode_d<FMT_FP8_BLOCK>(l) : run_decode_d<FMT_INT8_BLOCK>(l);
+  return l.p.pool.fmt == FMT_FP8_BLOCK ? run_block<FMT_FP8_BLOCK>(l) : run_block<FMT_INT8_BLOCK>(l);
 }
 
 }  // namespace kvq

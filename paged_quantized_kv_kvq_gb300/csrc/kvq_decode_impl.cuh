@@ -504,7 +504,36 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
       }
     }
   }
-  {
+  if constexpr (tile_scale<FMT, BS8>()) {
+    // tile by tile: half the V words are live at a time, which pays for the product's
+    // own registers
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      uint32_t vw[NU32];
+      load_lane_words<FMT, D>(r.vtile[t], lane, vw);
+      const int rows = r.rows[t];
+      if (T::maybe_nan && rows < 16) {
+        // zero the codes of tokens past the context (2j, 2j+1, 2j+8, 2j+9) so that
+        // 0 * NaN cannot reach the sum
+        const int t0 = 2 * j;
+        const uint32_t msk = (t0 < rows ? 0xFFu : 0u) | (t0 + 1 < rows ? 0xFF00u : 0u) |
+                             (t0 + 8 < rows ? 0xFF0000u : 0u) | (t0 + 9 < rows ? 0xFF000000u : 0u);
+#pragma unroll
+        for (int w = 0; w < NU32; ++w) vw[w] &= msk;
+      }
+      const float s = r.vs[t][0][0];
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        uint32_t a0, a1, a2, a3;
+        v_frag<FMT>(vw, mt, a0, a1, a2, a3);
+        float c[4];
+        mma_16816_from0(c, a0, a1, a2, a3, bh0[t][0], bh1[t][0]);
+        mma_16816(c, a0, a1, a2, a3, bl0[t][0], bl1[t][0]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][e] = fmaf(c[e], s, o[mt][e]);
+      }
+    }
+  } else {
     uint32_t vwp[2][NU32];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -579,12 +608,11 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
         else
           v_frag<FMT>(vwp[t], mt, a0, a1, a2, a3);
         if constexpr (T::block_scales) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_16816(c, a0, a1, a2, a3, bh0[t][gi], bh1[t][gi]);
+          float c[4];
+          mma_16816_from0(c, a0, a1, a2, a3, bh0[t][gi], bh1[t][gi]);
           mma_16816(c, a0, a1, a2, a3, bl0[t][gi], bl1[t][gi]);
-          const float s = tile_scale<FMT, BS8>() ? r.vs[t][0][0] : 1.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][e] = fmaf(c[e], s, o[mt][e]);
+          for (int e = 0; e < 4; ++e) o[mt][e] += c[e];
         } else {
           mma_16816(o[mt], a0, a1, a2, a3, bh0[t][gi], bh1[t][gi]);
           mma_16816(o[mt], a0, a1, a2, a3, bl0[t][gi], bl1[t][gi]);
@@ -646,8 +674,8 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, int 
   }
 }
 
-template <int FMT, int D, int NG, bool BS8>
-__global__ void __launch_bounds__(kDecodeThreads, kDecodeCtasPerSm)
+template <int FMT, int D, int NG, bool BS8, int CTAS>
+__global__ void __launch_bounds__(kDecodeThreads, CTAS)
     kvq_decode_kernel(const DecodeParams p) {
   using T = FmtTraits<FMT>;
   constexpr int KS = D / 16;
@@ -1308,11 +1336,13 @@ struct DecodeLaunch {
   int smem;
   cudaStream_t st;
   bool dependent;  // launch as a programmatic dependent of the previous kernel
+  bool two_ctas = false;  // planned for two CTAs per SM (per-block formats)
 };
 
-template <int FMT, int D, int NG, bool BS8 = false>
+// CTAS: resident CTAs per SM the kernel is compiled for.
+template <int FMT, int D, int NG, bool BS8 = false, int CTAS = kDecodeCtasPerSm>
 cudaError_t run_decode(const DecodeLaunch& l) {
-  cudaError_t e = allow_big_smem<kvq_decode_kernel<FMT, D, NG, BS8>>();
+  cudaError_t e = allow_big_smem<kvq_decode_kernel<FMT, D, NG, BS8, CTAS>>();
   if (e != cudaSuccess) return e;
   {
     cudaLaunchConfig_t dc = {};
@@ -1325,7 +1355,7 @@ cudaError_t run_decode(const DecodeLaunch& l) {
     da[0].val.programmaticStreamSerializationAllowed = 1;
     dc.attrs = da;
     dc.numAttrs = l.dependent ? 1 : 0;
-    e = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode_kernel<FMT, D, NG, BS8>, l.p));
+    e = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode_kernel<FMT, D, NG, BS8, CTAS>, l.p));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};

@@ -126,6 +126,7 @@ struct DecodePlan {
   int smem_bytes = 0;   // dynamic shared memory per CTA
   int merge_grid = 0;   // CTAs of the merge kernel
   int merge_chunk = 8;  // pieces the merge loads per round trip
+  bool two_ctas = false;  // two resident CTAs per SM instead of three
   size_t ps_bytes = 0;  // page prefix at the start of the workspace
   size_t ws_bytes = 0;  // page prefix + split partials
 };

@@ -401,7 +401,9 @@ cudaError_t run_weights(const WeightsLaunch& l) {
   const int span = pool.bs < 32 ? 32 : pool.bs;
   const int stage = p.slot_bytes * span / pool.bs + static_cast<int>(sizeof(StageInfo)) + 8;
   const int fixed = kWeightsWarps * (512 + 4) + (p.d.S + 1) * 4;
-  const int room = (228 * 1024 / kWeightsCtas - 1024 - fixed) / kWeightsWarps / stage;
+  auto stages_of = [&](int ctas) { return (228 * 1024 / ctas - 1024 - fixed) / kWeightsWarps / stage; };
+  int room = stages_of(kWeightsCtas);
+  if (room < 3) room = stages_of(2);  // (large pages: fewer warps with deeper streams)
   p.nstage = room < 2 ? 2 : room < kWeightsStages ? room : kWeightsStages;
   const int smem = kWeightsWarps * p.nstage * stage + fixed;
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
