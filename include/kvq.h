@@ -160,8 +160,8 @@ kvq_status kvq_calibrate_channel_scales(kvq_pool* pool, const kvq_half* k, const
  * Two tokens with the same slot in one call race (result unspecified).
  * Formats with one scale per block quantize a block's tokens together, so the
  * tokens of one call that fall into one block must stand next to each other in
- * slot_mapping (as every mapping made sequence by sequence has them; otherwise
- * that block's contents are unspecified).  The block's scale becomes
+ * slot_mapping, with no padding between them (as every mapping made sequence by
+ * sequence has them; otherwise that block's contents are unspecified).  The block's scale becomes
  * s = max(s_old, absmax of the call's tokens in it / 127 (448)); a token at
  * offset 0 starts the block anew, with no s_old and nothing kept of what it
  * held.  Where s grew, the block's other codes are rounded again at the new
@@ -259,7 +259,9 @@ kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
  *                 above; v is neither normed nor rotated
  *   slot_mapping : as for kvq_append, with its rule for per-block formats; the
  *                 query row of a token that is not stored is computed all the same
- * The other arguments are those of kvq_rope; num_q_heads may be 0. */
+ * The other arguments are those of kvq_rope; num_q_heads may be 0.  (Calls of
+ * 1024 tokens or more run their query rows as a kernel of its own beside the
+ * other.) */
 kvq_status kvq_rope_append(kvq_pool* pool, const kvq_rope_plan* plan, kvq_x_type x_type,
                            const void* q, int64_t q_row_stride, int num_q_heads, const void* k,
                            int64_t k_row_stride, const void* v, int64_t v_row_stride,
@@ -530,7 +532,8 @@ kvq_status kvq_paged_decode_lse(const kvq_pool* pool, const kvq_half* q, int num
  *            max_context_len; values at t >= context_lens[s] are left as they were
  * The other arguments are those of kvq_paged_decode.  A token new in this step
  * has no history: its prev must hold 0.  Device errors as for kvq_paged_decode; a
- * skipped block's scores are left as they were. */
+ * skipped block's scores are left as they were.  UNSUPPORTED when the lengths of
+ * num_seqs sequences leave no room in shared memory (beyond about 20000). */
 kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int num_seqs,
                                  int num_q_heads, const int32_t* block_table,
                                  int max_blocks_per_seq, const int32_t* context_lens,

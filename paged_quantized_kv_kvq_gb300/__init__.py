@@ -298,11 +298,14 @@ def kvq_rope_init(rotary_dim, interleaved=False, scaling=KVQ_ROPE_NONE, base=100
 def _x_rows(t, dtype, T, D, name):
     """_rows_view of rows that agree with the others in type, tokens and head_dim,
     and their heads."""
-    shape = t.shape
+    shape, stride = t.shape, t.stride()
     if t.dtype != dtype or len(shape) != 3 or shape[0] != T or shape[2] != D:
-        raise ValueError("%s must have the type, tokens and head_dim of the other rows" % name)
-    ptr, stride = _rows_view(t, dtype, name)
-    return ptr, stride, shape[1]
+        raise ValueError("%s must be [%d, heads, %d] of %s like the other rows" % (name, T, D, dtype))
+    if stride[2] != 1 or stride[1] != D:
+        raise ValueError("%s must be [rows, heads, head_dim] with contiguous heads" % name)
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.data_ptr(), stride[0], shape[1]
 
 
 def _x_type(dtype, name):

@@ -205,6 +205,13 @@ def test_decode(fmt, bs, hq, hkv, d, lens):
         out = pool.decode(_t(q), _t(table), _t(lens), int(max(lens.max(), 1)), split_blocks=split)
         assert pool.error() == kvq.KVQ_OK
         _near(out.cpu().numpy(), want)
+    wide_q = torch.zeros((len(lens), hq + 3, d), dtype=torch.float16, device=DEV)
+    wide_q[:, 2:2 + hq] = _t(q)
+    wide = torch.full((len(lens), hq + 1, d), 9.0, device=DEV)
+    ws = torch.empty(kvq.kvq_decode_workspace_bytes(pool.handle, len(lens), hq, int(lens.max())), dtype=torch.uint8, device=DEV)
+    kvq.kvq_paged_decode_strided(pool.handle, wide_q[:, 2:2 + hq], _t(table), _t(lens), int(lens.max()), d ** -0.5, wide[:, 1:], ws)
+    _near(wide[:, 1:].cpu().numpy(), want)
+    assert (wide[:, 0] == 9).all()
     out = torch.empty((len(lens), hq, d), device=DEV)
     kvq.kvq_paged_decode_noalloc(pool.handle, _t(q), _t(table), _t(lens), int(lens.max()), d ** -0.5, out)
     _near(out.cpu().numpy(), want)

@@ -257,6 +257,65 @@ def test_without_rotation_it_is_the_append(fmt, group):
         b.close()
 
 
+@pytest.mark.parametrize("fmt,group", [(kvq.KVQ_INT8_PER_BLOCK, 0), (kvq.KVQ_INT8_PER_GROUP, 128)])
+@pytest.mark.parametrize("graph", [False, True])
+def test_long_append_and_the_step_behind_it(fmt, group, graph):
+    """A prompt long enough for two kernels, and right behind it on the stream a step
+    whose append launches as a programmatic dependent: eagerly and replayed, the
+    same as with a synchronisation between the two."""
+    rng = np.random.default_rng(21)
+    bs, hq, hkv, d, S = 16, 8, 2, 128, 3
+    lens = [900, 700, 555]
+    slots, nb = _slots(rng, lens, bs, [0] * S)
+    T = sum(lens)
+    qkv = _rows(rng, T, hq + 2 * hkv, d)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    pos = _t(np.concatenate([np.arange(n) for n in lens]))
+    per = [(n + bs - 1) // bs for n in lens]
+    table = np.zeros((S, max(per) + 1), np.int32)
+    at = 0
+    spare = nb
+    for s, n in enumerate(lens):
+        table[s, :per[s]] = slots[at:at + n:bs] // bs
+        table[s, per[s]] = spare  # (the step may need a new block)
+        spare += 1
+        at += n
+    L = _t(np.array(lens, np.int32) + 1)
+    plan = kvq.kvq_rope_init(d)
+    kn, vn, qn = (_rows(rng, S, h, d) for h in (hkv, hkv, hq))
+    results = []
+    for apart in (True, False):
+        pool = kvq.KVPool(spare, bs, hkv, d, fmt, group, device=DEV)
+        qo, out = torch.empty((T, hq, d), dtype=torch.float16, device=DEV), torch.zeros((S, hq, d), device=DEV)
+        ws = torch.empty(kvq.kvq_decode_workspace_bytes(pool.handle, S, hq, 901), dtype=torch.uint8, device=DEV)
+        sl, tb = _t(slots), _t(table)
+
+        def call():
+            kvq.kvq_rope_append(pool.handle, plan, q, k, v, pos, sl, qo)
+            if apart:
+                torch.cuda.synchronize()
+            kvq.kvq_decode_step(pool.handle, kn, vn, qn, tb, L, 901, d ** -0.5, out, ws)
+
+        call()
+        torch.cuda.synchronize()
+        if graph and not apart:
+            g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+            with torch.cuda.graph(g, stream=side):
+                call()
+            for _ in range(5):
+                out.zero_()
+                g.replay()
+                torch.cuda.synchronize()
+        for _ in range(0 if graph else 5):
+            call()
+        torch.cuda.synchronize()
+        assert pool.error() == kvq.KVQ_OK
+        results.append((qo.clone(), out.clone()) + tuple(pool.read_slots(sl)))
+        pool.close()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
 def test_padding_and_bad_slots():
     """A padded token's queries are computed; a slot outside the pool is flagged."""
     rng = np.random.default_rng(8)
