@@ -530,12 +530,20 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const __half* at = src + ((c & 1) + 8 * (c >> 1)) * p.stride[kv];
-        const uint2 a = act ? *reinterpret_cast<const uint2*>(at + da) : make_uint2(0, 0);
-        const uint2 b = act ? *reinterpret_cast<const uint2*>(at + db) : make_uint2(0, 0);
-        raw[c][0] = a.x;
-        raw[c][1] = a.y;
-        raw[c][2] = b.x;
-        raw[c][3] = b.y;
+        if (!turn) {  // (channels da .. db+3 adjoin)
+          const uint4 a = act ? *reinterpret_cast<const uint4*>(at + da) : make_uint4(0, 0, 0, 0);
+          raw[c][0] = a.x;
+          raw[c][1] = a.y;
+          raw[c][2] = a.z;
+          raw[c][3] = a.w;
+        } else {
+          const uint2 a = act ? *reinterpret_cast<const uint2*>(at + da) : make_uint2(0, 0);
+          const uint2 b = act ? *reinterpret_cast<const uint2*>(at + db) : make_uint2(0, 0);
+          raw[c][0] = a.x;
+          raw[c][1] = a.y;
+          raw[c][2] = b.x;
+          raw[c][3] = b.y;
+        }
       }
       float x[4][8];
 #pragma unroll

@@ -68,10 +68,11 @@ __device__ __forceinline__ float absmax4_nan(float a, float b, float c, float d)
 
 // Codes of x[0..3] (biased, packed in a word, x[0] lowest) at a scale s whose
 // quant_inverse is inv > 0: the bits of quant_i8, unless `ok` is cleared.
-// x * inv is within 2^-22 of x / s relative, 2^-15 for |x / s| <= 127.5, so the
-// two round to the same integer unless x * inv lies that close to a half, i.e.
-// unless its distance from the integer exceeds 0.4999; then, and for NaN, ok is
-// cleared and the caller takes quant_i8.  (Adding 1.5 * 2^23 rounds half to even
+// x * inv and the rounded x / s are within 2^-21 of each other relative (2^-22 from
+// the reciprocal, a rounding each), 6.1e-5 for |x / s| <= 127.5, so the two round to
+// the same integer unless x * inv lies that close to a half, i.e. unless its
+// distance from the integer exceeds 0.49993; then, and for NaN, ok is cleared and
+// the caller takes quant_i8.  (Adding 1.5 * 2^23 rounds half to even
 // and leaves the integer in the low bits.  Five instructions a value; an IEEE
 // division alone is twice that.)
 __device__ __forceinline__ uint32_t quant4_i8(const float (&x)[4], float inv, bool& ok) {
@@ -86,7 +87,7 @@ __device__ __forceinline__ uint32_t quant4_i8(const float (&x)[4], float inv, bo
     f2_unpack(b, m[2 * i], m[2 * i + 1]);
     f2_unpack(d, t[2 * i], t[2 * i + 1]);
   }
-  ok = ok && absmax4_nan(t[0], t[1], t[2], t[3]) < 0.4999f;
+  ok = ok && absmax4_nan(t[0], t[1], t[2], t[3]) < 0.49993f;
   return prmt(prmt(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040u),
               prmt(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040u), 0x5410u) ^
          0x80808080u;
