@@ -157,11 +157,13 @@ kvq_status kvq_calibrate_channel_scales(kvq_pool* pool, const kvq_half* k, const
  * itself saturating at 57344 for KVQ_FP8_E5M2,
  * e4m3 round-to-nearest-even saturating for FP8; an all-zero group stores s=0
  * and zero codes.  Per-channel uses the pool's static scales.  FP16 stores x.
- * Two tokens with the same slot in one call race (result unspecified).
+ * Two tokens with the same slot in one call race (result unspecified; with
+ * per-block formats that of the whole block).
  * Formats with one scale per block quantize a block's tokens together, so the
  * tokens of one call that fall into one block must stand next to each other in
  * slot_mapping, with no padding between them (as every mapping made sequence by
- * sequence has them; otherwise that block's contents are unspecified).  The block's scale becomes
+ * sequence has them; otherwise that block's contents are unspecified).  The
+ * block's scale becomes
  * s = max(s_old, absmax of the call's tokens in it / 127 (448)); a token at
  * offset 0 starts the block anew, with no s_old and nothing kept of what it
  * held.  Where s grew, the block's other codes are rounded again at the new
@@ -207,7 +209,7 @@ typedef struct {
     double factor;    /* >= 1; KVQ_ROPE_NONE ignores it             */
     double orig_len;  /* >= 1; KVQ_ROPE_PARTS and KVQ_ROPE_BANDS only */
     double low, high; /* 0 < low < high; the same two               */
-    double magnitude; /* factor on cosine and sine; 0 takes 1, or for
+    double magnitude; /* factor on cosine and sine, <= 3e38; 0 takes 1, or for
                          KVQ_ROPE_PARTS 0.1 ln(factor) + 1          */
 } kvq_rope_config;
 
@@ -257,7 +259,8 @@ kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
  * k_out would first have rounded them to fp16) and reach memory only as codes.
  *   k, v        : [T][kv_heads][head_dim] of the pool, fp16 or bf16, strided as
  *                 above; v is neither normed nor rotated
- *   slot_mapping : as for kvq_append, with its rule for per-block formats; the
+ *   slot_mapping : as for kvq_append, with its rule for per-block formats (a slot
+ *                 given twice leaves its block unspecified in every format); the
  *                 query row of a token that is not stored is computed all the same
  * The other arguments are those of kvq_rope; num_q_heads may be 0.  (Calls of
  * 1024 tokens or more run their query rows as a kernel of its own beside the
@@ -527,13 +530,15 @@ kvq_status kvq_paged_decode_lse(const kvq_pool* pool, const kvq_half* q, int num
  *                     of exp(q . k^_t * sm_scale - lse),   t < context_lens[s]
  *   lse    : fp32 [num_seqs][num_q_heads] of the same q over the same tokens
  *            (kvq_paged_decode_lse); a row whose lse is -inf weighs nothing
+ *   decay  : finite
  *   prev   : fp32 like scores, or NULL (zeros); may be scores itself
  *   scores : fp32 [num_seqs][kv_heads][score_stride], score_stride >=
  *            max_context_len; values at t >= context_lens[s] are left as they were
  * The other arguments are those of kvq_paged_decode.  A token new in this step
  * has no history: its prev must hold 0.  Device errors as for kvq_paged_decode; a
  * skipped block's scores are left as they were.  UNSUPPORTED when the lengths of
- * num_seqs sequences leave no room in shared memory (beyond about 20000). */
+ * num_seqs sequences leave no room in shared memory (beyond about 20000), or
+ * max_context_len is within 64 of 2^31. */
 kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int num_seqs,
                                  int num_q_heads, const int32_t* block_table,
                                  int max_blocks_per_seq, const int32_t* context_lens,

@@ -254,11 +254,17 @@ def kvq_append(pool, k, v, slot_mapping, stream=None) -> None:
                             _stream(stream)), "kvq_append")
 
 
-def _here(t):
+def _here(*tensors):
     """Refuse tensors of a GPU that is not the current one: the kernels are launched
-    on the current GPU's stream."""
-    if t.is_cuda and t.get_device() != _th()._C._cuda_getDevice():
-        raise ValueError("tensors must be on the current CUDA device")
+    on the current GPU's stream.  (Host tensors, device -1, are _ptr's to refuse.)"""
+    dev = None
+    for t in tensors:
+        if t is None or not t.is_cuda:
+            continue
+        if dev is None:
+            dev = _th()._C._cuda_getDevice()
+        if t.get_device() != dev:
+            raise ValueError("tensors must be on the current CUDA device")
 
 
 def _rows_view(t, dtype, name):
@@ -345,7 +351,7 @@ def kvq_rope(plan, q, k, positions, q_out=None, k_out=None, q_weight=None, k_wei
         raise ValueError("q or k must be given")
     dtype = ref.dtype
     x_type = _x_type(dtype, "q" if q is not None else "k")
-    _here(ref)
+    _here(q, k, positions, q_out, k_out, q_weight, k_weight)
     T, _, D = ref.shape
 
     def side(x, out, name):
@@ -375,7 +381,7 @@ def kvq_rope_append(pool, plan, q, k, v, positions, slot_mapping, q_out=None, q_
     torch = _th()
     dtype = k.dtype
     x_type = _x_type(dtype, "k")
-    _here(k)
+    _here(q, k, v, positions, slot_mapping, q_out, q_weight, k_weight)
     T, _, D = k.shape
     if v.shape != k.shape or slot_mapping.numel() != T:
         raise ValueError("k, v must be [T, kv_heads, head_dim] and slot_mapping [T]")
@@ -445,7 +451,7 @@ def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm
     S, Hq, _ = q.shape
     if lse.shape != (S, Hq):
         raise ValueError("lse must be [num_seqs, num_q_heads]")
-    _here(q)
+    _here(q, block_table, context_lens, out, lse, workspace)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_paged_decode_lse(
         pool, _ptr(q, torch.float16, "q"), S, Hq, _ptr(block_table, torch.int32, "block_table"),
@@ -466,7 +472,7 @@ def kvq_attention_weights(pool, q, block_table, context_lens, max_context_len, s
         raise ValueError("scores must be [num_seqs, kv_heads, tokens] and lse [num_seqs, num_q_heads]")
     if prev is not None and prev.shape != scores.shape:
         raise ValueError("prev must have the shape of scores")
-    _here(q)
+    _here(q, block_table, context_lens, lse, scores, prev)
     _check(lib().kvq_attention_weights(
         pool, _ptr(q, torch.float16, "q"), S, Hq, _ptr(block_table, torch.int32, "block_table"),
         block_table.shape[1], _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
@@ -492,7 +498,7 @@ def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, b
         raise ValueError("kept must be [num_seqs, budget_blocks]")
     if scores_out is not None and (scores_out.dim() != 3 or scores_out.shape[:2] != scores.shape[:2]):
         raise ValueError("scores_out must be [num_seqs, kv_heads, tokens]")
-    _here(scores)
+    _here(scores, block_table, context_lens, table_out, lens_out, kept, scores_out)
     _check(lib().kvq_evict_blocks(
         pool, _ptr(scores, torch.float32, "scores"), scores.shape[2], S,
         _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
@@ -639,7 +645,7 @@ def kvq_read_values(pool, slots, k_out, v_out, stream=None) -> None:
     torch = _th()
     if k_out.shape != v_out.shape or k_out.shape[0] != slots.numel():
         raise ValueError("k_out, v_out must be [n, kv_heads, head_dim]")
-    _here(k_out)
+    _here(slots, k_out, v_out)
     _check(lib().kvq_read_values(pool, _ptr(slots, torch.int64, "slots"), slots.numel(),
                                  _ptr(k_out, torch.float16, "k_out"),
                                  _ptr(v_out, torch.float16, "v_out"), _stream(stream)),

@@ -1,5 +1,6 @@
 // kvq_api.cu -- the C ABI (include/kvq.h): pool creation and byte accounting,
 // host-side argument checks, and dispatch to the kernels.
+#include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <new>
@@ -295,7 +296,8 @@ kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
   a.D = head_dim;
   a.eps = eps;
   a.plan = plan;
-  return from_cuda(kvq::launch_rope(a, stream));
+  const cudaError_t e = kvq::launch_rope(a, stream);
+  return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
 }
 
 kvq_status kvq_rope_append(kvq_pool* pool, const kvq_rope_plan* plan, kvq_x_type x_type,
@@ -461,12 +463,13 @@ kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int nu
     return KVQ_ERR_INVALID_ARG;
   if (num_q_heads % pool->view.Hkv != 0) return KVQ_ERR_INVALID_ARG;
   if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * pool->view.bs) return KVQ_ERR_INVALID_ARG;
-  if (!(sm_scale == sm_scale) || !(decay == decay)) return KVQ_ERR_INVALID_ARG;
+  if (!(sm_scale == sm_scale) || !std::isfinite(decay)) return KVQ_ERR_INVALID_ARG;
   if (num_seqs == 0 || max_context_len == 0) return KVQ_OK;
   if (q == nullptr || block_table == nullptr || context_lens == nullptr || lse == nullptr ||
       scores == nullptr)
     return KVQ_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(q) & 15) return KVQ_ERR_INVALID_ARG;
+  if (max_context_len > 0x7fffffff - 64) return KVQ_ERR_UNSUPPORTED;  // (rounded up to pages in 32 bits)
   kvq::WeightsArgs a;
   a.pool = pool->view;
   a.q = reinterpret_cast<const __half*>(q);

@@ -15,7 +15,10 @@
 // `budget` of them lie above (or ties are all that is left): some 15 counts for
 // weights as attention gives them, 32 at most.  A short row costs one launch and
 // a chain of such steps; the reading loads eight heads of two tokens at once, so
-// that a long row is not a chain of round trips.
+// that a long row is not a chain of round trips.  Measured: 16 rows of up to 1000
+// tokens 7.1 us, 8 rows of 32768 tokens x 8 heads 14.2 us (12.8 with clusters of 16
+// CTAs, which not every part of the chip can place; 256 threads 6.4 and 18.4, 1024
+// threads 7.9 and 13.9).
 //
 // Sums.  Two blocks next to the border may differ in the last bits, and which
 // of them stays must not depend on the order of a sum: each block's is carried

@@ -15,9 +15,9 @@ namespace {
 // L2 once and from L1 for its other slots.  The bound for few slots is one chain
 // of loads.  Where the 16 slots are a sub-tile in its order (long calls), a thread
 // takes 8 channels of the four tokens that share V words instead and every word
-// is read once; the bound then is HBM (codes in, twice as many bytes out).
+// is read once; the bound then is the instructions that widen and round (16384
+// slots x 8 heads of INT8: 25 us, of which HBM would take 15).
 constexpr int kValueSlots = 16;
-
 
 // Channels 8ci .. 8ci+7 of tokens 2j, 2j+1, 2j+8, 2j+9 of the sub-tile at offset
 // `off` of block blk (one-byte codes); token t's values go to out + t rows.
@@ -226,9 +226,9 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   if (a.plan != nullptr) p.plan = *a.plan;
   while ((1 << p.bs_log2) < a.pool.bs) ++p.bs_log2;
   // Few tokens (a decode step, a short prompt): one per CTA, and one head per CTA
-  // (four above 128 tokens) for the latency of a run.  Many: a block's worth of tokens per CTA, and heads for
-  // kIngestRounds rounds of its warps, which share its angles.  Formats with one scale per token need every head of
-  // a token in one CTA.
+  // (four above 128 tokens) for the latency of a run.  Many: a block's worth of
+  // tokens per CTA, and heads for kIngestRounds rounds of its warps, which share its
+  // angles.  Formats with one scale per token need every head of a token in one CTA.
   // A long call's query rows go to a kernel of their own, launched beside this
   // one: this one's 128 registers leave an SM 16 warps, too few loads in flight
   // for the rows that are most of the bytes (16384 tokens, 32 Q and 8 kv heads:
@@ -238,7 +238,8 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   // (A long call may also be a step of many sequences, each token a run of its own,
   // which a CTA takes one after the other: 8 tokens per CTA below 16384.)
   p.tpc = !many || a.slots == nullptr ? 1 : a.T < 16384 ? std::min(a.pool.bs, 8) : a.pool.bs;
-  p.hpc = tok ? a.pool.Hkv : a.T > 128 && !many ? 4 : many ? kIngestRounds * std::max(1, kIngestWarps * 1024 / (std::max(a.pool.bs, 16) * a.pool.D)) : 1;
+  const int round_heads = std::max(1, kIngestWarps * 1024 / (std::max(a.pool.bs, 16) * a.pool.D));
+  p.hpc = tok ? a.pool.Hkv : many ? kIngestRounds * round_heads : a.T > 128 ? 4 : 1;
   p.hsplit = (a.pool.Hkv + p.hpc - 1) / p.hpc;
   p.kv_ctas = (a.T + p.tpc - 1) / p.tpc * p.hsplit * 2;
   int64_t q_ctas = 0;

@@ -10,8 +10,10 @@
 //    atomics and no second kernel, whatever number of tokens the call brings;
 //  * a 16-token sub-tile that the run covers is assembled in shared memory and
 //    leaves as 16-byte stores, although its bytes interleave tokens.
-// Bounds: HBM for prompts (fp16 rows in, codes out), latency for a decode step
-// (one token per run: slot -> rows -> absmax -> codes).
+// Bounds: the instructions that norm, rotate and quantize for prompts (16384
+// tokens x 8 heads into INT8 blocks: 46 us, 26 million warp instructions, where HBM
+// would take 15), latency for a decode step (one token per run: slot -> rows ->
+// absmax -> codes; 8.5 us for 64 tokens with their 32 query heads).
 //
 // One scale per (block, head): s = max(s_old, absmax / top) in fp32, where top
 // is 127 or 448 and s_old the block's scale, unless the run writes offset 0,

@@ -94,7 +94,7 @@ extern "C" kvq_status kvq_rope_init(const kvq_rope_config* c, kvq_rope_plan* out
   if (c->layout != KVQ_ROPE_HALF && c->layout != KVQ_ROPE_INTERLEAVED) return KVQ_ERR_INVALID_ARG;
   const double s = c->factor, n = c->orig_len, pi = 3.14159265358979323846;
   if (!(c->base > 1.0) || !std::isfinite(c->base) || !(c->magnitude >= 0.0) ||
-      !std::isfinite(c->magnitude))
+      !(c->magnitude <= 3e38))  // (kept as fp32)
     return KVQ_ERR_INVALID_ARG;
   if (c->scaling < KVQ_ROPE_NONE || c->scaling > KVQ_ROPE_BANDS) return KVQ_ERR_INVALID_ARG;
   if (c->scaling != KVQ_ROPE_NONE && (!(s >= 1.0) || !std::isfinite(s))) return KVQ_ERR_INVALID_ARG;

@@ -162,7 +162,8 @@ __host__ __device__ constexpr int rope_smem(int rotary_dim) {
 // 4c .. 4c+3.  The row's pointers and weights are set up once for all nt tokens,
 // whose loads are issued together, and the arithmetic is packed two by two:
 // after HBM it is the instructions that bound this (16384 tokens x 40 heads with
-// norms: 161 per 16 bytes of input and 65 us with one row at a time).
+// norms: 55.5 us, 0.89 of the copy rate with the issue slots 72% busy; one row at a
+// time 161 instructions per 16 bytes of input and 65 us).
 template <int D, bool BF16, bool INTER>
 __device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const RopeRows& B, int hB,
                                             const int64_t* positions, int64_t t0, int nt, int h,

@@ -19,9 +19,9 @@
 // a warp, not once a stretch.  Pages come by bulk copies into stages of the warp's
 // own, some 200 KB in flight an SM, and are read back as the tensor-core fragments
 // they are stored as, two sub-tiles side by side.
-// Measured: 8 x 32768 tokens of INT8 blocks in 64 us (287 MB, 0.66 of the copy
+// Measured: 8 x 32768 tokens of INT8 blocks in 65 us (285 MB, 0.66 of the copy
 // rate; its page stream without the arithmetic takes 62), 64 x ~1050 tokens of INT8
-// groups in 21.9 us.  Stretches of 256 tokens per warp took 67 and 24 us with the
+// groups in 22 us.  Stretches of 256 tokens per warp took 67 and 24 us with the
 // next 4 KB held in registers, 67 and 27 with stages; pages aligned to 64 or 128
 // bytes, waits that suspend, or the heads of a block side by side changed nothing
 // or lost; a fourth CTA per SM spills, and two wait for their arithmetic.

@@ -52,6 +52,16 @@ def test_weights_refusals(L, kw):
     assert _weights(L, FakePool(), **kw) == kvq.KVQ_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("decay", [float("inf"), float("-inf")])
+def test_weights_need_a_finite_decay(L, decay):
+    assert _weights(L, FakePool(), decay=decay) == kvq.KVQ_ERR_INVALID_ARG
+
+
+def test_weights_of_the_longest_contexts(L):
+    n = 2 ** 31 - 1
+    assert _weights(L, FakePool(bs=64), mb=n // 64 + 1, mc=n, stride=n) == kvq.KVQ_ERR_UNSUPPORTED
+
+
 def test_weights_nothing_to_do(L):
     assert _weights(L, FakePool(), S=0) == kvq.KVQ_OK
     assert _weights(L, FakePool(), mc=0, stride=0) == kvq.KVQ_OK

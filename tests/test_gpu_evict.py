@@ -340,3 +340,36 @@ def test_serving_loop(fmt, group):
             table, lens, scores, tally = nt.cpu().numpy(), nl.cpu().numpy(), ns[:, :, :W].contiguous(), new
     assert lens.max() <= budget * bs + 4
     pool.close()
+
+
+@pytest.mark.parametrize("fmt,group", [(kvq.KVQ_INT8_PER_BLOCK, 0), (kvq.KVQ_INT8_PER_GROUP, 128)])
+def test_blocks_beyond_four_gigabytes(fmt, group):
+    """Pages whose offsets need more than 32 bits, through every call on them."""
+    rng = np.random.default_rng(6)
+    nb, bs, hkv, hq, d = 140000, 16, 8, 16, 128  # 4.6 GB
+    lens = np.array([700, 1, 90], np.int32)
+    small = np.zeros((3, 44), np.int32)
+    small[0], small[1, 0], small[2, :6] = np.arange(44), 44, 45 + np.arange(6)
+    far = nb - 1 - 37 * rng.permutation(51)
+    table = far[small].astype(np.int32)
+    ref = BlockCache(fmt, 51, bs, hkv, d) if fmt in kvq.BLOCK_FORMATS else oracle.OracleCache(fmt, 51, bs, hkv, d, group)
+    pool = kvq.KVPool(nb, bs, hkv, d, fmt, group, device=DEV)
+    near, there = (np.concatenate([tokens(t, lens, s, bs) for s in range(3)]) for t in (small, table))
+    k, v = (rng.standard_normal((len(near), hkv, d)).astype(np.float16) for _ in range(2))
+    kvq.kvq_rope_append(pool.handle, None, None, _t(k), _t(v), None, _t(there))
+    ref.append(k, v, near)
+    values = (lambda at: ref.values(at)) if fmt in kvq.BLOCK_FORMATS else \
+        (lambda at: np.stack([ref.dequantized(kv)[at] for kv in (0, 1)], 1))
+    got = torch.stack(pool.read_values(_t(there)), 1).cpu().numpy()
+    np.testing.assert_array_equal(got, values(near).astype(np.float32).astype(np.float16))
+    q = rng.standard_normal((3, hq, d)).astype(np.float16)
+    out, lse, w = attention(lambda s: values(tokens(small, lens, s, bs)), q, lens)
+    o, e = pool.decode_lse(_t(q), _t(table), _t(lens), 700)
+    np.testing.assert_allclose(o.cpu().numpy(), out, rtol=0, atol=TOL)
+    np.testing.assert_allclose(e.cpu().numpy(), lse, rtol=2.0 ** -19, atol=2.0 ** -16)
+    scores = torch.zeros((3, hkv, 704), device=DEV)
+    pool.accumulate_weights(_t(q), _t(table), _t(lens), 700, e, scores)
+    for s in range(3):
+        np.testing.assert_allclose(scores[s, :, :lens[s]].cpu().numpy(), w[s].sum(1), rtol=2.0 ** -14, atol=1e-9)
+    assert pool.error() == kvq.KVQ_OK
+    pool.close()

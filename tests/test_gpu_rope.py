@@ -331,3 +331,43 @@ def test_padding_and_bad_slots():
         pool.rope_append(plan, x[:, :1], x[:, 1:2], x[:, 2:], _t(pos), _t(np.array([32, -1, 1 << 50])))
         assert pool.error() == kvq.KVQ_ERR_OUT_OF_RANGE and torch.equal(before, pool.buffer[256:])
         pool.close()
+
+
+def test_tensors_of_another_device_are_refused():
+    """Every tensor of a call is looked at, not the first alone."""
+
+    class Elsewhere:
+        is_cuda = True
+
+        @staticmethod
+        def get_device():
+            return torch.cuda.current_device() + 1
+
+    here = torch.zeros(1, device=DEV)
+    kvq._here(here, None, torch.zeros(1))
+    with pytest.raises(ValueError):
+        kvq._here(here, None, Elsewhere())
+
+
+@pytest.mark.parametrize("fmt,group", [(kvq.KVQ_INT8_PER_BLOCK, 0), (kvq.KVQ_FP8_E4M3_PER_BLOCK, 0),
+                                       (kvq.KVQ_INT8_PER_GROUP, 64), (kvq.KVQ_INT4_PER_GROUP, 32)])
+@pytest.mark.parametrize("T", [200, 3000])
+def test_a_slot_given_twice_spoils_its_own_block_only(fmt, group, T):
+    rng = np.random.default_rng(T)
+    nb, bs = T // 16 + 8, 16
+    pools = [kvq.KVPool(nb, bs, 3, 64, fmt, group, device=DEV, fill_byte=0) for _ in range(2)]
+    x = _rows(rng, T, 6, 64)
+    slots = np.arange(T) + bs
+    twice = slots.copy()
+    twice[64:64 + 40] = slots[64]        # more tokens of one block than it holds
+    twice[130:134] = slots[129]          # a few in the middle of a run
+    for pool, at in zip(pools, (slots, twice)):
+        pool.rope_append(None, None, x[:, :3], x[:, 3:], None, _t(at))
+        assert pool.error() == kvq.KVQ_OK
+    spoilt = np.unique(np.concatenate([slots[64:104], slots[129:134]]) // bs)
+    rest = slots[~np.isin(slots // bs, spoilt)]
+    rest = np.concatenate([np.arange(bs), rest, np.arange((T // bs + 3) * bs, nb * bs)])
+    for a, b in zip(*(pool.read_values(_t(rest)) for pool in pools)):
+        assert torch.equal(a, b)
+    for pool in pools:
+        pool.close()

@@ -64,6 +64,18 @@ def test_init_refusals(kw, status):
     assert e.value.status == status
 
 
+def test_magnitude_must_fit_fp32():
+    with pytest.raises(kvq.KVQError) as e:
+        kvq.kvq_rope_init(64, magnitude=1e39)
+    assert e.value.status == kvq.KVQ_ERR_INVALID_ARG
+    assert kvq.kvq_rope_init(64, magnitude=1e38).magnitude == ctypes.c_float(1e38).value
+
+
+def test_too_many_rows(L):
+    """Rows that would need more than 2^31 - 1 CTAs."""
+    assert _rope(L, hq=8192, qs=8192 * 128, qos=8192 * 128, T=(1 << 31) - 1) == kvq.KVQ_ERR_UNSUPPORTED
+
+
 def test_null_plan_arguments(L):
     plan = kvq.RopePlan()
     assert L.kvq_rope_init(None, ctypes.byref(plan)) == kvq.KVQ_ERR_INVALID_ARG
