@@ -8,7 +8,7 @@ namespace kvq {
 
 namespace {
 
-// K and V of 16 slots of one kv head per CTA, as fp16: code times scale in
+// K and V of 16 slots (long calls: 32 or 64) of one kv head per CTA, as fp16: code times scale in
 // fp32, rounded once.  A thread takes 8 channels of one slot: its K codes are
 // two neighbouring words of the page, its V codes lie in eight words 64 bytes
 // apart, each shared with three other tokens, so a sub-tile's sectors come from
@@ -16,7 +16,8 @@ namespace {
 // of loads.  Where the 16 slots are a sub-tile in its order (long calls), a thread
 // takes 8 channels of the four tokens that share V words instead and every word
 // is read once; the bound then is the instructions that widen and round (16384
-// slots x 8 heads of INT8: 25 us, of which HBM would take 15).
+// slots x 8 heads of INT8: 18 us, of which HBM would take 15;
+// with the threads of a 128-thread half that a sub-tile leaves idle 25).
 constexpr int kValueSlots = 16;
 
 // Channels 8ci .. 8ci+7 of tokens 2j, 2j+1, 2j+8, 2j+9 of the sub-tile at offset
@@ -25,6 +26,7 @@ template <int FMT>
 __device__ __forceinline__ void read_tile(const PoolView& pool, int64_t blk, int off, int kv, int h,
                                           int ci, int j, __half* out) {
   const int D = pool.D, d0 = 8 * ci;
+  const int64_t row = (int64_t)pool.Hkv * D;
   const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
   const char* tile = page + (kv == 0 ? 0 : pool.code_bytes) + (off >> 4) * pool.sub_bytes;
   const float* sc = reinterpret_cast<const float*>(page + 2 * pool.code_bytes);
@@ -79,33 +81,36 @@ __device__ __forceinline__ void read_tile(const PoolView& pool, int64_t blk, int
       x[e] = (odd ? __high2float(pr) : __low2float(pr)) * (FMT == FMT_INT8_CHANNEL ? chs[e] : s[c]);
     }
     const int t = 2 * j + (c & 1) + 8 * (c >> 1);
-    *reinterpret_cast<uint4*>(out + (int64_t)t * pool.Hkv * D) = narrow8(x);
+    *reinterpret_cast<uint4*>(out + t * row) = narrow8(x);
   }
 }
 
 template <int FMT>
-__global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int bs_log2,
+__global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int bs_log2, int tpt_log2,
                                                               const int64_t* slots, int64_t n,
                                                               __half* k, __half* v) {
-  const int D = pool.D, lph = D / 8;
+  // (powers of two throughout: a division costs as much as the rest of a row)
+  const int D = pool.D, lph_log2 = D == 64 ? 3 : 4, lph = 1 << lph_log2, tpt = 1 << tpt_log2;
   const int kv = threadIdx.x >> 7;  // 128 threads each for K and V
   const int h = blockIdx.y;
-  if (FMT != FMT_FP16 && FMT != FMT_INT4_GROUP && pool.bs >= 16 && (int64_t)(blockIdx.x + 1) * kValueSlots <= n) {
-    const int64_t i0 = (int64_t)blockIdx.x * kValueSlots, first = slots[i0];
+  const int unit = threadIdx.x & 127 & (tpt - 1);  // of the tpt threads (whole warps) of its 16 slots
+  const int64_t i0 = (((int64_t)blockIdx.x << (7 - tpt_log2)) + ((threadIdx.x & 127) >> tpt_log2)) * kValueSlots;
+  if (FMT != FMT_FP16 && FMT != FMT_INT4_GROUP && pool.bs >= 16 && i0 + kValueSlots <= n) {
+    const int64_t first = slots[i0];
     const int lane = threadIdx.x & 15;
-    if (__syncthreads_and(slots[i0 + lane] == first + lane) && first >= 0 && (first & 15) == 0 &&
+    if (__all_sync(0xffffffffu, slots[i0 + lane] == first + lane) && first >= 0 && (first & 15) == 0 &&
         first < pool.num_blocks * pool.bs) {
-      const int unit = threadIdx.x & 127, ci = unit % lph, j = unit / lph;
+      const int ci = unit & (lph - 1), j = unit >> lph_log2;
       if (j < 4)
         read_tile<FMT>(pool, first >> bs_log2, static_cast<int>(first & (pool.bs - 1)), kv, h, ci, j,
                        (kv == 0 ? k : v) + (i0 * pool.Hkv + h) * D + 8 * ci);
       return;
     }
   }
-  for (int u = threadIdx.x & 127; u < kValueSlots * lph; u += 128) {
-    const int64_t i = (int64_t)blockIdx.x * kValueSlots + u / lph;
+  for (int u = unit; u < kValueSlots * lph; u += tpt) {
+    const int64_t i = i0 + (u >> lph_log2);
     if (i >= n) return;
-    const int ci = u % lph, d0 = 8 * ci;
+    const int ci = u & (lph - 1), d0 = 8 * ci;
     const int64_t slot = slots[i];
     if (slot < 0) continue;
     if (slot >= pool.num_blocks * pool.bs) {
@@ -177,12 +182,15 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
 
 cudaError_t launch_read_values(const PoolView& pool, const int64_t* slots, int64_t n, __half* k,
                                __half* v, cudaStream_t st) {
-  const int64_t gx = (n + kValueSlots - 1) / kValueSlots;
+  // Threads of 16 slots: all 128 for a short call's latency, the 4 per 8 channels that
+  // a sub-tile takes for a long one.
+  const int tpt_log2 = n < 2048 ? 7 : pool.D == 64 ? 5 : 6;
+  const int64_t spc = kValueSlots << (7 - tpt_log2), gx = (n + spc - 1) / spc;
   if (gx > 0x7fffffffLL || pool.Hkv > 65535) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(gx), pool.Hkv);
   int log2 = 0;
   while ((1 << log2) < pool.bs) ++log2;
-  auto run = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(pool, log2, slots, n, k, v); };
+  auto run = [&](auto kernel) { kernel<<<grid, 256, 0, st>>>(pool, log2, tpt_log2, slots, n, k, v); };
   switch (pool.fmt) {
     case FMT_FP16: run(kvq_read_values_kernel<FMT_FP16>); break;
     case FMT_INT8_TOKEN: run(kvq_read_values_kernel<FMT_INT8_TOKEN>); break;

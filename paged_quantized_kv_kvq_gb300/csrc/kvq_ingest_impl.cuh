@@ -63,7 +63,7 @@ struct IngestShared {
   uint8_t off[2 * kMaxBlock];  // its offset in the block
   uint32_t cut[4];             // bit i: token i begins a new block
   uint32_t has[2];             // offsets the run writes
-  float red[kIngestWarps];
+  float red[2 * kIngestWarps];
   uint32_t tok[kMaxBlock];     // per-token absmax, as bits
   int grown;                   // heads of a pass whose block scale grew
   int grown_head[16];
@@ -490,10 +490,12 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ci = lane % LPH, rg = lane / LPH;
   const int bs = pool.bs;
-  const int units = (bs >> 4) * UPT;                  // of one head
-  const int wph = min(units, kIngestWarps);           // warps per head
-  const int upw = units / wph;                        // units per warp: 1, or 2 (64 tokens x 128)
-  const int hpi = kIngestWarps / wph;                 // heads at a time
+  // (powers of two: units of a head, warps per head, units per warp -- 1, or 2 for 64
+  // tokens x 128 -- and heads at a time)
+  const int units = (bs >> 4) * UPT;
+  const int wl = units >= 4 ? 2 : units - 1, wph = 1 << wl;
+  const int ul = units >> (wl + 1), upw = 1 << ul;
+  const int hpi = kIngestWarps >> wl;
   const int r = p.plan.rotary_dim, rp = r >> 1;
   const bool turn = kv == 0 && r > 0, norm = kv == 0 && p.k_weight != nullptr;
   const bool inter = p.plan.layout == KVQ_ROPE_INTERLEAVED;
@@ -501,6 +503,37 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
   // unless scale groups are narrower than the head, whose lanes must adjoin.
   const bool split = turn && !inter && (FMT != FMT_INT8_GROUP || pool.ng == 1) && 8 * ci < r;
   const int da = split ? 4 * ci : 8 * ci, db = split ? 4 * ci + rp : 8 * ci + 4;
+  // Rounds: a head's (or several heads') units, one per warp.  With several units per
+  // warp the first rounds of a head only find the block's absmax.
+  const int rl = kBlock && ul > 0 ? ul + 1 : ul, rounds = 1 << rl;
+  const int total = ((h1 - h0 + hpi - 1) >> (2 - wl)) << rl;
+  const int wu = (warp & (wph - 1)) << ul, wh = h0 + (warp >> wl);
+  uint32_t next[4][4];  // rows of the round to come
+  auto load = [&](int it) {
+    const int u = wu + (it & (upw - 1)), h = wh + ((it >> rl) << (2 - wl));
+    const int tok = 16 * (u / UPT) + 2 * (rg + RG * (u % UPT));  // chunk c: token tok + (c & 1) + 8 (c >> 1)
+    const __half* src = static_cast<const __half*>(p.x[kv]) + (t0 + tok) * p.stride[kv] + h * D;
+    const bool act = h < h1;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const __half* at = src + ((c & 1) + 8 * (c >> 1)) * p.stride[kv];
+      if (!turn) {  // (channels da .. db+3 adjoin)
+        const uint4 a = act ? *reinterpret_cast<const uint4*>(at + da) : make_uint4(0, 0, 0, 0);
+        next[c][0] = a.x;
+        next[c][1] = a.y;
+        next[c][2] = a.z;
+        next[c][3] = a.w;
+      } else {
+        const uint2 a = act ? *reinterpret_cast<const uint2*>(at + da) : make_uint2(0, 0);
+        const uint2 b = act ? *reinterpret_cast<const uint2*>(at + db) : make_uint2(0, 0);
+        next[c][0] = a.x;
+        next[c][1] = a.y;
+        next[c][2] = b.x;
+        next[c][3] = b.y;
+      }
+    }
+  };
+  load(0);
   if (turn) rope_table<kIngestThreads>(p.plan, p.positions + t0, bs, cs);
   float w[8];
   if (norm)
@@ -514,43 +547,23 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
   constexpr int ES = FMT == FMT_FP16 ? 2 : 1;
   const int ka = k_tile_offset(0, da, D, ES), kb = k_tile_offset(0, db, D, ES);
   __syncthreads();
+  int it = 0;
   for (int hb = h0; hb < h1; hb += hpi) {
-    const int h = hb + warp / wph;
+    const int h = hb + (warp >> wl);
     const bool act = h < h1;
     char* page = pool.pages + (blk * pool.Hkv + (act ? h : 0)) * pool.page_bytes;
     float* scales = reinterpret_cast<float*>(page + 2 * pool.code_bytes);
     float amax = 0.f, s = 0.f, inv = 0.f;
-    // With several units per warp the first round only finds the block's absmax.
-    const int rounds = kBlock && upw > 1 ? 2 * upw : upw;
-    for (int k = 0; k < rounds; ++k) {
+    for (int k = 0; k < rounds; ++k, ++it) {
       const bool last = k >= rounds - upw;
-      const int u = warp % wph * upw + k % upw;
+      const int u = wu + (k & (upw - 1));
       const int sub = u / UPT, j = rg + RG * (u % UPT);
-      const int tok = 16 * sub + 2 * j;  // chunk c: token tok + (c & 1) + 8 (c >> 1)
-      uint32_t raw[4][4];
-      const __half* src = static_cast<const __half*>(p.x[kv]) + (t0 + tok) * p.stride[kv] + h * D;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const __half* at = src + ((c & 1) + 8 * (c >> 1)) * p.stride[kv];
-        if (!turn) {  // (channels da .. db+3 adjoin)
-          const uint4 a = act ? *reinterpret_cast<const uint4*>(at + da) : make_uint4(0, 0, 0, 0);
-          raw[c][0] = a.x;
-          raw[c][1] = a.y;
-          raw[c][2] = a.z;
-          raw[c][3] = a.w;
-        } else {
-          const uint2 a = act ? *reinterpret_cast<const uint2*>(at + da) : make_uint2(0, 0);
-          const uint2 b = act ? *reinterpret_cast<const uint2*>(at + db) : make_uint2(0, 0);
-          raw[c][0] = a.x;
-          raw[c][1] = a.y;
-          raw[c][2] = b.x;
-          raw[c][3] = b.y;
-        }
-      }
+      const int tok = 16 * sub + 2 * j;
       float x[4][8];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        widen8(make_uint4(raw[c][0], raw[c][1], raw[c][2], raw[c][3]), p.bf16, x[c]);
+        widen8(make_uint4(next[c][0], next[c][1], next[c][2], next[c][3]), p.bf16, x[c]);
+      if (it + 1 < total) load(it + 1);
       if (norm)
 #pragma unroll
         for (int c = 0; c < 4; ++c) norm8<D>(x[c], w, p.eps);
@@ -583,11 +596,11 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
         if (k == upw - 1) {  // every unit of the block seen: its warps agree on the scale
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          if (wph > 1) {
-            if (lane == 0) sh.red[warp] = amax;
+          if (wph > 1) {  // (the two halves in turn: one barrier)
+            float* red = sh.red + (hb - h0 & hpi) * (kIngestWarps / hpi);
+            if (lane == 0) red[warp] = amax;
             __syncthreads();
-            for (int i = 0; i < wph; ++i) amax = fmaxf(amax, sh.red[warp / wph * wph + i]);
-            __syncthreads();
+            for (int i = 0; i < wph; ++i) amax = fmaxf(amax, red[(warp & ~(wph - 1)) + i]);
           }
           s = __fdiv_rn(amax, kTop);
           inv = quant_inverse(s);
@@ -675,9 +688,11 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
   __syncthreads();
 }
 
-// Resident CTAs to compile for: whole blocks need some 80 registers, a run held
-// in registers 8 more per chunk.
-constexpr int ingest_ctas(int cpt) { return cpt <= 2 ? 6 : cpt == 4 ? 5 : 3; }
+// Resident CTAs to compile for: whole blocks need some 96 registers with the rows of
+// the next round on their way, a run held in registers 8 more per chunk.  (16384
+// tokens with their queries and the read-back: 96.1 us; with four CTAs 96.6, with six
+// 98.0, with six and no rows ahead 96.9.)
+constexpr int ingest_ctas(int cpt) { return cpt <= 4 ? 5 : 3; }
 
 template <int FMT, int D, int CPT>
 __global__ void __launch_bounds__(kIngestThreads, ingest_ctas(CPT)) kvq_ingest_kernel(const __grid_constant__ IngestParams p) {
@@ -746,13 +761,15 @@ __global__ void __launch_bounds__(kIngestThreads, ingest_ctas(CPT)) kvq_ingest_k
   float2* cs = reinterpret_cast<float2*>(smem + pool.code_bytes);
   const int h1 = min(h0 + p.hpc, pool.Hkv);
   const int nown = min(p.tpc, win);
-  for (int i = 0; i < nown;) {
-    if (!(sh.cut[i >> 5] >> (i & 31) & 1)) {  // belongs to a run of an earlier CTA
-      ++i;
-      continue;
-    }
-    int e = i + 1;
-    while (e < win && e < i + pool.bs && !(sh.cut[e >> 5] >> (e & 31) & 1)) ++e;
+  const uint64_t cuts[2] = {(uint64_t)sh.cut[1] << 32 | sh.cut[0], (uint64_t)sh.cut[3] << 32 | sh.cut[2]};
+  auto next_cut = [&](int i) {  // the first cut at or behind token i of the window
+    const uint64_t a = i < 64 ? cuts[0] >> i : 0, b = i < 64 ? cuts[1] : i < 128 ? cuts[1] >> (i - 64) : 0;
+    return a != 0 ? i + __ffsll(a) - 1 : b != 0 ? max(i, 64) + __ffsll(b) - 1 : 128;
+  };
+  // (what lies before the first cut belongs to a run of an earlier CTA; what a run
+  // has beyond a block's tokens, slots given twice, is dropped)
+  for (int i = next_cut(0); i < nown; i = next_cut(i)) {
+    const int e = min(next_cut(i + 1), i + pool.bs);  // (every place behind the window is a cut)
     const int blk = sh.blk[i + 1];
     if (e - i == 1) {  // one token: the CTA of the first heads takes all of them
       if (blk >= 0 && h0 == 0)

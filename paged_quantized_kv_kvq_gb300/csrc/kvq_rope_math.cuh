@@ -162,18 +162,18 @@ __host__ __device__ constexpr int rope_smem(int rotary_dim) {
 // 4c .. 4c+3.  The row's pointers and weights are set up once for all nt tokens,
 // whose loads are issued together, and the arithmetic is packed two by two:
 // after HBM it is the instructions that bound this (16384 tokens x 40 heads with
-// norms: 55.5 us, 0.89 of the copy rate with the issue slots 72% busy; one row at a
-// time 161 instructions per 16 bytes of input and 65 us).
-template <int D, bool BF16, bool INTER>
-__device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const RopeRows& B, int hB,
-                                            const int64_t* positions, int64_t t0, int nt, int h,
-                                            float eps, const kvq_rope_plan& plan, float* smem) {
+// norms: 52.1 us, 0.95 of the copy rate, at 116 instructions per 16 bytes of input; with
+// checks of rows and tokens 142 and 55.5 us, one row at a time 161 and 65 us).
+template <int D, bool BF16, bool INTER, bool full>
+__device__ __forceinline__ void rope_tokens_of(const RopeRows& A, int hA, const RopeRows& B, int hB,
+                                               const int64_t* positions, int64_t t0, int nt, int h,
+                                               float eps, const kvq_rope_plan& plan, float* smem) {
   constexpr int LPH = D / 8;
   const int r = plan.rotary_dim, rp = r >> 1;
   const int ci = threadIdx.x % LPH;
   const bool rot = 8 * ci < r;
   const int da = !INTER && rot ? 4 * ci : 8 * ci, db = !INTER && rot ? 4 * ci + rp : 8 * ci + 4;
-  const bool act = h < hA + hB, b = act && h >= hA;
+  const bool act = full || h < hA + hB, b = act && h >= hA;
   const RopeRows& R = b ? B : A;
   const int64_t at = act ? (b ? h - hA : h) * D : 0;
   const __half* x = static_cast<const __half*>(R.x) + t0 * R.x_stride + at;
@@ -181,8 +181,8 @@ __device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const Rop
   uint32_t raw[kRopeTokens][4];
 #pragma unroll
   for (int t = 0; t < kRopeTokens; ++t) {
-    raw[t][0] = raw[t][1] = raw[t][2] = raw[t][3] = 0;
-    if (act && t < nt) {
+    if (!full) raw[t][0] = raw[t][1] = raw[t][2] = raw[t][3] = 0;
+    if (full || (act && t < nt)) {
       if constexpr (INTER) {
         const uint4 v = *reinterpret_cast<const uint4*>(x + t * xs + da);
         raw[t][0] = v.x;
@@ -213,7 +213,8 @@ __device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const Rop
   float* cs = smem;  // [nt][3][rp]: cos, sin, -sin
   const int q = threadIdx.x % KVQ_ROPE_MAX_PAIRS;  // (a division by rp would cost more)
   if (q < rp)
-    for (int t = threadIdx.x / KVQ_ROPE_MAX_PAIRS; t < nt; t += blockDim.x / KVQ_ROPE_MAX_PAIRS) {
+    for (int t = threadIdx.x / KVQ_ROPE_MAX_PAIRS; t < (full ? kRopeTokens : nt);
+         t += blockDim.x / KVQ_ROPE_MAX_PAIRS) {
       const float2 v = rope_cs(plan.turns[q], positions[t0 + t], plan.magnitude);
       cs[3 * t * rp + q] = v.x;
       cs[(3 * t + 1) * rp + q] = v.y;
@@ -224,7 +225,7 @@ __device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const Rop
   __half* out = R.out + t0 * os + at;
 #pragma unroll
   for (int t = 0; t < kRopeTokens; ++t) {
-    if (t >= nt) break;
+    if (!full && t >= nt) break;
     uint64_t v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -291,6 +292,18 @@ __device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const Rop
       }
     }
   }
+}
+
+template <int D, bool BF16, bool INTER>
+__device__ __forceinline__ void rope_tokens(const RopeRows& A, int hA, const RopeRows& B, int hB,
+                                            const int64_t* positions, int64_t t0, int nt, int h,
+                                            float eps, const kvq_rope_plan& plan, float* smem) {
+  // a CTA whose tokens and rows are all there goes without the checks
+  const int h_end = h - static_cast<int>(threadIdx.x) / (D / 8) + static_cast<int>(blockDim.x) / (D / 8);
+  if (nt == kRopeTokens && h_end <= hA + hB)
+    rope_tokens_of<D, BF16, INTER, true>(A, hA, B, hB, positions, t0, nt, h, eps, plan, smem);
+  else
+    rope_tokens_of<D, BF16, INTER, false>(A, hA, B, hB, positions, t0, nt, h, eps, plan, smem);
 }
 
 }  // namespace kvq
