@@ -254,17 +254,26 @@ def kvq_append(pool, k, v, slot_mapping, stream=None) -> None:
                             _stream(stream)), "kvq_append")
 
 
-def _here(*tensors):
-    """Refuse tensors of a GPU that is not the current one: the kernels are launched
-    on the current GPU's stream.  (Host tensors, device -1, are _ptr's to refuse.)"""
-    dev = None
-    for t in tensors:
-        if t is None or not t.is_cuda:
-            continue
-        if dev is None:
-            dev = _th()._C._cuda_getDevice()
-        if t.get_device() != dev:
-            raise ValueError("tensors must be on the current CUDA device")
+def _device():
+    """The current GPU, on whose stream the kernels are launched: the one that every
+    tensor of a call must be on.  -2, no tensor's device, without a GPU."""
+    try:
+        return _th()._C._cuda_getDevice()
+    except (AttributeError, AssertionError, RuntimeError):
+        return -2
+
+
+def _at(t, dtype, name, dev):
+    """_ptr of a tensor on GPU dev."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device" % name)
+    if t.dtype != dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _rows_view(t, dtype, name):
@@ -301,16 +310,16 @@ def kvq_rope_init(rotary_dim, interleaved=False, scaling=KVQ_ROPE_NONE, base=100
     return plan
 
 
-def _x_rows(t, dtype, T, D, name):
-    """_rows_view of rows that agree with the others in type, tokens and head_dim,
-    and their heads."""
+def _x_rows(t, dtype, T, D, name, dev):
+    """_rows_view of rows that agree with the others in type, tokens and head_dim, and
+    their heads."""
     shape, stride = t.shape, t.stride()
     if t.dtype != dtype or len(shape) != 3 or shape[0] != T or shape[2] != D:
         raise ValueError("%s must be [%d, heads, %d] of %s like the other rows" % (name, T, D, dtype))
     if stride[2] != 1 or stride[1] != D:
         raise ValueError("%s must be [rows, heads, head_dim] with contiguous heads" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device" % name)
     return t.data_ptr(), stride[0], shape[1]
 
 
@@ -323,20 +332,20 @@ def _x_type(dtype, name):
     raise ValueError("%s must be float16 or bfloat16, got %s" % (name, dtype))
 
 
-def _weight(w, head_dim, name):
+def _weight(w, head_dim, name, dev):
     if w is None:
         return None
     if w.numel() != head_dim:
         raise ValueError("%s must be [head_dim]" % name)
-    return _ptr(w, _th().float32, name)
+    return _at(w, _th().float32, name, dev)
 
 
-def _positions(plan, positions, T):
+def _positions(plan, positions, T, dev):
     if plan is None:
         return None, None
     if positions is None or positions.numel() != T:
         raise ValueError("positions must be [T]")
-    return ctypes.byref(plan), _ptr(positions, _th().int64, "positions")
+    return ctypes.byref(plan), _at(positions, _th().int64, "positions", dev)
 
 
 def kvq_rope(plan, q, k, positions, q_out=None, k_out=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -351,25 +360,25 @@ def kvq_rope(plan, q, k, positions, q_out=None, k_out=None, q_weight=None, k_wei
         raise ValueError("q or k must be given")
     dtype = ref.dtype
     x_type = _x_type(dtype, "q" if q is not None else "k")
-    _here(q, k, positions, q_out, k_out, q_weight, k_weight)
+    dev = _device()
     T, _, D = ref.shape
 
     def side(x, out, name):
         if x is None:
             return None, 0, 0, None, 0
-        ptr, stride, heads = _x_rows(x, dtype, T, D, name)
+        ptr, stride, heads = _x_rows(x, dtype, T, D, name, dev)
         if out is None:
             out = x
-        optr, ostride, oheads = _x_rows(out, half, T, D, name + "_out")
+        optr, ostride, oheads = _x_rows(out, half, T, D, name + "_out", dev)
         if oheads != heads:
             raise ValueError("%s_out must have the shape of %s" % (name, name))
         return ptr, stride, heads, optr, ostride
 
     qp, qs, hq, qo, qos = side(q, q_out, "q")
     kp, ks, hk, ko, kos = side(k, k_out, "k")
-    pl, pos = _positions(plan, positions, T)
+    pl, pos = _positions(plan, positions, T, dev)
     _check(lib().kvq_rope(pl, x_type, qp, qs, hq, kp, ks, hk, D, pos, T,
-                          _weight(q_weight, D, "q_weight"), _weight(k_weight, D, "k_weight"),
+                          _weight(q_weight, D, "q_weight", dev), _weight(k_weight, D, "k_weight", dev),
                           float(eps), qo, qos, ko, kos, _stream(stream)), "kvq_rope")
 
 
@@ -381,22 +390,22 @@ def kvq_rope_append(pool, plan, q, k, v, positions, slot_mapping, q_out=None, q_
     torch = _th()
     dtype = k.dtype
     x_type = _x_type(dtype, "k")
-    _here(q, k, v, positions, slot_mapping, q_out, q_weight, k_weight)
+    dev = _device()
     T, _, D = k.shape
     if v.shape != k.shape or slot_mapping.numel() != T:
         raise ValueError("k, v must be [T, kv_heads, head_dim] and slot_mapping [T]")
-    kp, ks = _rows_view(k, dtype, "k")
-    vp, vs, _ = _x_rows(v, dtype, T, D, "v")
+    kp, ks, _ = _x_rows(k, dtype, T, D, "k", dev)
+    vp, vs, _ = _x_rows(v, dtype, T, D, "v", dev)
     qp, qs, hq, qo, qos = None, 0, 0, None, 0
     if q is not None:
-        qp, qs, hq = _x_rows(q, dtype, T, D, "q")
-        qo, qos, oheads = _x_rows(q if q_out is None else q_out, torch.float16, T, D, "q_out")
+        qp, qs, hq = _x_rows(q, dtype, T, D, "q", dev)
+        qo, qos, oheads = _x_rows(q if q_out is None else q_out, torch.float16, T, D, "q_out", dev)
         if oheads != hq:
             raise ValueError("q_out must have the shape of q")
-    pl, pos = _positions(plan, positions, T)
+    pl, pos = _positions(plan, positions, T, dev)
     _check(lib().kvq_rope_append(pool, pl, x_type, qp, qs, hq, kp, ks, vp, vs, pos,
-                                 _ptr(slot_mapping, torch.int64, "slot_mapping"), T,
-                                 _weight(q_weight, D, "q_weight"), _weight(k_weight, D, "k_weight"),
+                                 _at(slot_mapping, torch.int64, "slot_mapping", dev), T,
+                                 _weight(q_weight, D, "q_weight", dev), _weight(k_weight, D, "k_weight", dev),
                                  float(eps), qo, qos, _stream(stream)), "kvq_rope_append")
 
 
@@ -451,13 +460,13 @@ def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm
     S, Hq, _ = q.shape
     if lse.shape != (S, Hq):
         raise ValueError("lse must be [num_seqs, num_q_heads]")
-    _here(q, block_table, context_lens, out, lse, workspace)
+    dev = _device()
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_paged_decode_lse(
-        pool, _ptr(q, torch.float16, "q"), S, Hq, _ptr(block_table, torch.int32, "block_table"),
-        block_table.shape[1], _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
-        float(sm_scale), _ptr(out, torch.float32, "out"), _ptr(lse, torch.float32, "lse"),
-        _ptr(workspace, None, "workspace") if workspace is not None else None, ws_bytes,
+        pool, _at(q, torch.float16, "q", dev), S, Hq, _at(block_table, torch.int32, "block_table", dev),
+        block_table.shape[1], _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len),
+        float(sm_scale), _at(out, torch.float32, "out", dev), _at(lse, torch.float32, "lse", dev),
+        None if workspace is None else _at(workspace, workspace.dtype, "workspace", dev), ws_bytes,
         int(split_blocks), _stream(stream)), "kvq_paged_decode_lse")
 
 
@@ -472,12 +481,12 @@ def kvq_attention_weights(pool, q, block_table, context_lens, max_context_len, s
         raise ValueError("scores must be [num_seqs, kv_heads, tokens] and lse [num_seqs, num_q_heads]")
     if prev is not None and prev.shape != scores.shape:
         raise ValueError("prev must have the shape of scores")
-    _here(q, block_table, context_lens, lse, scores, prev)
+    dev = _device()
     _check(lib().kvq_attention_weights(
-        pool, _ptr(q, torch.float16, "q"), S, Hq, _ptr(block_table, torch.int32, "block_table"),
-        block_table.shape[1], _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len),
-        float(sm_scale), _ptr(lse, torch.float32, "lse"), float(decay),
-        _ptr(prev, torch.float32, "prev"), _ptr(scores, torch.float32, "scores"), scores.shape[2],
+        pool, _at(q, torch.float16, "q", dev), S, Hq, _at(block_table, torch.int32, "block_table", dev),
+        block_table.shape[1], _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len),
+        float(sm_scale), _at(lse, torch.float32, "lse", dev), float(decay),
+        _at(prev, torch.float32, "prev", dev), _at(scores, torch.float32, "scores", dev), scores.shape[2],
         _stream(stream)), "kvq_attention_weights")
 
 
@@ -498,14 +507,14 @@ def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, b
         raise ValueError("kept must be [num_seqs, budget_blocks]")
     if scores_out is not None and (scores_out.dim() != 3 or scores_out.shape[:2] != scores.shape[:2]):
         raise ValueError("scores_out must be [num_seqs, kv_heads, tokens]")
-    _here(scores, block_table, context_lens, table_out, lens_out, kept, scores_out)
+    dev = _device()
     _check(lib().kvq_evict_blocks(
-        pool, _ptr(scores, torch.float32, "scores"), scores.shape[2], S,
-        _ptr(block_table, torch.int32, "block_table"), block_table.shape[1],
-        _ptr(context_lens, torch.int32, "context_lens"), int(max_context_len), int(budget_blocks),
-        int(sink_blocks), int(recent_blocks), _ptr(table_out, torch.int32, "table_out"),
-        _ptr(lens_out, torch.int32, "lens_out"), _ptr(kept, torch.int32, "kept"),
-        _ptr(scores_out, torch.float32, "scores_out"),
+        pool, _at(scores, torch.float32, "scores", dev), scores.shape[2], S,
+        _at(block_table, torch.int32, "block_table", dev), block_table.shape[1],
+        _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len), int(budget_blocks),
+        int(sink_blocks), int(recent_blocks), _at(table_out, torch.int32, "table_out", dev),
+        _at(lens_out, torch.int32, "lens_out", dev), _at(kept, torch.int32, "kept", dev),
+        _at(scores_out, torch.float32, "scores_out", dev),
         0 if scores_out is None else scores_out.shape[2], _stream(stream)), "kvq_evict_blocks")
 
 
@@ -645,10 +654,10 @@ def kvq_read_values(pool, slots, k_out, v_out, stream=None) -> None:
     torch = _th()
     if k_out.shape != v_out.shape or k_out.shape[0] != slots.numel():
         raise ValueError("k_out, v_out must be [n, kv_heads, head_dim]")
-    _here(slots, k_out, v_out)
-    _check(lib().kvq_read_values(pool, _ptr(slots, torch.int64, "slots"), slots.numel(),
-                                 _ptr(k_out, torch.float16, "k_out"),
-                                 _ptr(v_out, torch.float16, "v_out"), _stream(stream)),
+    dev = _device()
+    _check(lib().kvq_read_values(pool, _at(slots, torch.int64, "slots", dev), slots.numel(),
+                                 _at(k_out, torch.float16, "k_out", dev),
+                                 _at(v_out, torch.float16, "v_out", dev), _stream(stream)),
            "kvq_read_values")
 
 

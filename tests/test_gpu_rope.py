@@ -333,20 +333,31 @@ def test_padding_and_bad_slots():
         pool.close()
 
 
-def test_tensors_of_another_device_are_refused():
+@pytest.mark.parametrize("which", ["q", "k", "positions", "q_out", "k_out", "q_weight", "k_weight"])
+def test_tensors_of_another_device_are_refused(which):
     """Every tensor of a call is looked at, not the first alone."""
 
     class Elsewhere:
+        """A tensor as another GPU would hold it."""
+
+        def __init__(self, t):
+            self.t = t
+
         is_cuda = True
 
-        @staticmethod
-        def get_device():
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+        def get_device(self):
             return torch.cuda.current_device() + 1
 
-    here = torch.zeros(1, device=DEV)
-    kvq._here(here, None, torch.zeros(1))
+    x = torch.zeros((2, 3, 64), dtype=torch.float16, device=DEV)
+    a = dict(q=x, k=x.clone(), positions=torch.zeros(2, dtype=torch.int64, device=DEV), q_out=x.clone(), k_out=x.clone(),
+             q_weight=torch.ones(64, device=DEV), k_weight=torch.ones(64, device=DEV))
+    kvq.kvq_rope(kvq.kvq_rope_init(64), **a)
+    a[which] = Elsewhere(a[which])
     with pytest.raises(ValueError):
-        kvq._here(here, None, Elsewhere())
+        kvq.kvq_rope(kvq.kvq_rope_init(64), **a)
 
 
 @pytest.mark.parametrize("fmt,group", [(kvq.KVQ_INT8_PER_BLOCK, 0), (kvq.KVQ_FP8_E4M3_PER_BLOCK, 0),
