@@ -8,16 +8,16 @@ namespace kvq {
 
 namespace {
 
-// K and V of 16 slots (long calls: 32 or 64) of one kv head per CTA, as fp16: code times scale in
-// fp32, rounded once.  A thread takes 8 channels of one slot: its K codes are
-// two neighbouring words of the page, its V codes lie in eight words 64 bytes
+// K and V of 16 slots (long calls: 32 or 64) of one kv head per CTA, as fp16: code
+// times scale in fp32, rounded once.  A thread takes 8 channels of one slot: its K
+// codes are two neighbouring words of the page, its V codes lie in eight words 64 bytes
 // apart, each shared with three other tokens, so a sub-tile's sectors come from
 // L2 once and from L1 for its other slots.  The bound for few slots is one chain
 // of loads.  Where the 16 slots are a sub-tile in its order (long calls), a thread
 // takes 8 channels of the four tokens that share V words instead and every word
-// is read once; the bound then is the instructions that widen and round (16384
-// slots x 8 heads of INT8: 18 us, of which HBM would take 15;
-// with the threads of a 128-thread half that a sub-tile leaves idle 25).
+// is read once; the bound then is HBM and the instructions that widen and round
+// (16384 slots x 8 heads of INT8: 18 us, of which HBM would take 15; 25 with 128
+// threads to a sub-tile, half of them idle).
 constexpr int kValueSlots = 16;
 
 // Channels 8ci .. 8ci+7 of tokens 2j, 2j+1, 2j+8, 2j+9 of the sub-tile at offset
