@@ -87,6 +87,13 @@ class RopePlan(ctypes.Structure):
                 ("turns", ctypes.c_uint64 * KVQ_ROPE_MAX_PAIRS)]
 
 
+class PoolHandle(ctypes.c_void_p):
+    """A kvq_pool* with the shape it was allocated with: (block_size, kv_heads,
+    head_dim).  The library sees addresses only; tensors are held against this."""
+
+    shape = None
+
+
 def header_functions() -> list[str]:
     """Names of the functions include/kvq.h declares."""
     text = open(HEADER_PATH).read()
@@ -217,13 +224,14 @@ def kvq_pool_bytes(num_blocks, block_size, kv_heads, head_dim, dtype, group=0) -
 
 
 def kvq_alloc_pool(num_blocks, block_size, kv_heads, head_dim, dtype, group=0, device_buf=None):
-    """Returns an opaque handle (ctypes.c_void_p).  device_buf: optional torch
+    """Returns an opaque handle (a ctypes.c_void_p).  device_buf: optional torch
     uint8 CUDA tensor of at least kvq_pool_bytes(..) bytes, owned by the caller."""
-    h = ctypes.c_void_p()
+    h = PoolHandle()
     ptr = _ptr(device_buf, name="device_buf") if device_buf is not None else None
     nbytes = device_buf.numel() * device_buf.element_size() if device_buf is not None else 0
     _check(lib().kvq_alloc_pool(num_blocks, block_size, kv_heads, head_dim, dtype, group, ptr,
                                 nbytes, ctypes.byref(h)), "kvq_alloc_pool")
+    h.shape = (block_size, kv_heads, head_dim)
     return h
 
 
@@ -323,6 +331,44 @@ def _x_rows(t, dtype, T, D, name, dev):
     return t.data_ptr(), stride[0], shape[1]
 
 
+def _pool_shape(pool):
+    """(kv_heads, head_dim) of a handle made by kvq_alloc_pool; None for any other,
+    which has to be the caller's care."""
+    shape = getattr(pool, "shape", None)
+    return None if shape is None else shape[1:]
+
+
+def _check_pool_rows(pool, k, D):
+    """[T, kv_heads, head_dim] rows that the kernels read with the pool's own sizes."""
+    shape = _pool_shape(pool)
+    if shape is not None and (k.shape[1] != shape[0] or D != shape[1]):
+        raise ValueError("k, v must have the pool's %d kv heads of %d channels" % shape)
+
+
+def _check_seqs(pool, q, block_table, context_lens):
+    """S, Hq of q [S, Hq, head_dim], held against the pool, the table and the lengths."""
+    if len(q.shape) != 3:
+        raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
+    S, Hq, D = q.shape
+    shape = _pool_shape(pool)
+    if shape is not None:
+        if D != shape[1]:
+            raise ValueError("q must have the pool's head_dim of %d" % shape[1])
+        if Hq % shape[0] != 0:
+            raise ValueError("q's heads must be a multiple of the pool's %d kv heads" % shape[0])
+    if len(block_table.shape) != 2 or block_table.shape[0] != S:
+        raise ValueError("block_table must be [num_seqs, max_blocks_per_seq]")
+    if context_lens.numel() != S:
+        raise ValueError("context_lens must be [num_seqs]")
+    return S, Hq
+
+
+def _check_score_heads(pool, scores):
+    shape = _pool_shape(pool)
+    if shape is not None and scores.shape[1] != shape[0]:
+        raise ValueError("scores must have the pool's %d kv heads" % shape[0])
+
+
 def _x_type(dtype, name):
     torch = _th()
     if dtype is torch.float16:
@@ -394,6 +440,7 @@ def kvq_rope_append(pool, plan, q, k, v, positions, slot_mapping, q_out=None, q_
     T, _, D = k.shape
     if v.shape != k.shape or slot_mapping.numel() != T:
         raise ValueError("k, v must be [T, kv_heads, head_dim] and slot_mapping [T]")
+    _check_pool_rows(pool, k, D)
     kp, ks, _ = _x_rows(k, dtype, T, D, "k", dev)
     vp, vs, _ = _x_rows(v, dtype, T, D, "v", dev)
     qp, qs, hq, qo, qos = None, 0, 0, None, 0
@@ -457,9 +504,11 @@ def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm
     """kvq_paged_decode that also writes each row's log-sum-exp, lse [S, Hq] fp32
     (kvq_paged_decode_lse in include/kvq.h)."""
     torch = _th()
-    S, Hq, _ = q.shape
+    S, Hq = _check_seqs(pool, q, block_table, context_lens)
     if lse.shape != (S, Hq):
         raise ValueError("lse must be [num_seqs, num_q_heads]")
+    if out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
     dev = _device()
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_paged_decode_lse(
@@ -476,9 +525,10 @@ def kvq_attention_weights(pool, q, block_table, context_lens, max_context_len, s
     added to decay * prev: scores [S, Hkv, >= max_context_len] fp32
     (kvq_attention_weights in include/kvq.h).  prev may be scores itself."""
     torch = _th()
-    S, Hq, _ = q.shape
+    S, Hq = _check_seqs(pool, q, block_table, context_lens)
     if scores.dim() != 3 or scores.shape[0] != S or lse.shape != (S, Hq):
         raise ValueError("scores must be [num_seqs, kv_heads, tokens] and lse [num_seqs, num_q_heads]")
+    _check_score_heads(pool, scores)
     if prev is not None and prev.shape != scores.shape:
         raise ValueError("prev must have the shape of scores")
     dev = _device()
@@ -499,8 +549,9 @@ def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, b
     table_out and lens_out may be block_table and context_lens themselves."""
     torch = _th()
     S = context_lens.numel()
-    if scores.dim() != 3 or scores.shape[0] != S or block_table.shape[0] != S:
+    if scores.dim() != 3 or scores.shape[0] != S or block_table.dim() != 2 or block_table.shape[0] != S:
         raise ValueError("scores must be [num_seqs, kv_heads, tokens] and block_table [num_seqs, blocks]")
+    _check_score_heads(pool, scores)
     if table_out.shape != block_table.shape or lens_out.numel() != S:
         raise ValueError("table_out and lens_out must be shaped like block_table and context_lens")
     if kept is not None and kept.shape != (S, budget_blocks):
@@ -652,7 +703,9 @@ def kvq_read_values(pool, slots, k_out, v_out, stream=None) -> None:
     """Cached K and V of the slots as fp16 values, [n, kv_heads, head_dim] each
     (kvq_read_values in include/kvq.h)."""
     torch = _th()
-    if k_out.shape != v_out.shape or k_out.shape[0] != slots.numel():
+    shape = _pool_shape(pool)
+    if k_out.shape != v_out.shape or k_out.dim() != 3 or k_out.shape[0] != slots.numel() or (
+            shape is not None and k_out.shape[1:] != shape):
         raise ValueError("k_out, v_out must be [n, kv_heads, head_dim]")
     dev = _device()
     _check(lib().kvq_read_values(pool, _at(slots, torch.int64, "slots", dev), slots.numel(),
@@ -766,7 +819,6 @@ class KVPool:
     def accumulate_weights(self, q, block_table, context_lens, max_context_len, lse, scores,
                            decay=1.0, sm_scale=None, stream=None):
         """scores = decay * scores + this step's attention weights, in place."""
-        self._check_heads(scores)
         kvq_attention_weights(self.handle, q, block_table, context_lens, max_context_len,
                               q.shape[2] ** -0.5 if sm_scale is None else sm_scale, lse, scores,
                               scores, decay, stream)
@@ -776,7 +828,6 @@ class KVPool:
                      sink_blocks=0, recent_blocks=1, stream=None):
         """(table, lens, kept, scores) after the eviction, in new tensors."""
         torch = _th()
-        self._check_heads(scores)
         S = context_lens.numel()
         table, lens = torch.empty_like(block_table), torch.empty_like(context_lens)
         kept = torch.empty((S, budget_blocks), dtype=torch.int32, device=scores.device)
@@ -785,10 +836,6 @@ class KVPool:
         kvq_evict_blocks(self.handle, scores, block_table, context_lens, max_context_len,
                          budget_blocks, sink_blocks, recent_blocks, table, lens, kept, out, stream)
         return table, lens, kept, out
-
-    def _check_heads(self, scores):
-        if scores.shape[1] != self.kv_heads:
-            raise ValueError("scores must have the pool's %d kv heads" % self.kv_heads)
 
     def cascade_decode(self, q, block_table, context_lens, max_context_len, prefix_blocks,
                        sm_scale=None, out=None, stream=None):
