@@ -537,8 +537,9 @@ kvq_status kvq_paged_decode_lse(const kvq_pool* pool, const kvq_half* q, int num
  * The other arguments are those of kvq_paged_decode.  A token new in this step
  * has no history: its prev must hold 0.  Device errors as for kvq_paged_decode; a
  * skipped block's scores are left as they were.  UNSUPPORTED when the lengths of
- * num_seqs sequences leave no room in shared memory (beyond about 20000), or
- * max_context_len is within 64 of 2^31. */
+ * num_seqs sequences leave no room in shared memory (beyond about 20000), when
+ * max_context_len is within 64 of 2^31, or when num_seqs * kv_heads *
+ * max_context_len / 32 (64 for blocks of 64) is within 2^17 of 2^31. */
 kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int num_seqs,
                                  int num_q_heads, const int32_t* block_table,
                                  int max_blocks_per_seq, const int32_t* context_lens,

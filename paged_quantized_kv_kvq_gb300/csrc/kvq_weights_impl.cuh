@@ -400,6 +400,7 @@ cudaError_t run_weights(const WeightsLaunch& l) {
   // stages: what kWeightsCtas CTAs leave each of their warps of an SM's 228 KB
   const int span = pool.bs < 32 ? 32 : pool.bs;
   const int stage = p.slot_bytes * span / pool.bs + static_cast<int>(sizeof(StageInfo)) + 8;
+  if (p.d.S > 227 * 1024 / 4) return cudaErrorInvalidValue;  // (its prefix alone: the sums below stay in 32 bits)
   const int fixed = kWeightsWarps * (512 + 4) + (p.d.S + 1) * 4;
   auto stages_of = [&](int ctas) { return (228 * 1024 / ctas - 1024 - fixed) / kWeightsWarps / stage; };
   int room = stages_of(kWeightsCtas);
@@ -409,7 +410,7 @@ cudaError_t run_weights(const WeightsLaunch& l) {
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
   // one warp per stage at most
   const int64_t stages = (int64_t)((p.d.max_ctx + span - 1) / span) * p.d.S * pool.Hkv;
-  if (stages > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (stages > 0x7fffffffLL - (1 << 17)) return cudaErrorInvalidValue;  // (the kernel rounds them up to its warps)
   const int fit = 228 * 1024 / (smem + 1024);
   const int64_t full = (int64_t)l.sms * (fit < kWeightsCtas ? fit : kWeightsCtas), need = (stages + kWeightsWarps - 1) / kWeightsWarps;
   const int64_t grid = need < full ? need : full;
