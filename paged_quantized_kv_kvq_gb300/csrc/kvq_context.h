@@ -95,14 +95,15 @@ class PerContext {
 // kvq_api.cu.
 cudaError_t phase_mark(cudaStream_t st, cudaError_t launched);
 
-// Opt a kernel in to up to 227 KB of dynamic shared memory, once per
-// context (one cache per kernel: the kernel is a template argument).
-template <auto Kernel>
+// Opt a kernel in to up to 227 KB of shared memory, once per context (one
+// cache per kernel: the kernel is a template argument).  What it declares
+// statically (`Static` bytes) comes off the dynamic share.
+template <auto Kernel, int Static = 0>
 cudaError_t allow_big_smem() {
   static PerContext<char> done;
   char v = 0;
   return done.get(&v, [](char*) {
-    return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - Static);
   });
 }
 

@@ -809,8 +809,9 @@ struct IngestLaunch {
 
 template <int FMT, int D, int CPT>
 cudaError_t run_ingest_c(const IngestLaunch& l) {
-  if (l.smem > 48 * 1024) {
-    const cudaError_t e = allow_big_smem<kvq_ingest_kernel<FMT, D, CPT>>();
+  constexpr int own = sizeof(IngestShared);  // (FP16 blocks of 64 x 128, wholly rotated: 48 KB beside it)
+  if (l.smem + own > 48 * 1024) {
+    const cudaError_t e = allow_big_smem<kvq_ingest_kernel<FMT, D, CPT>, own>();
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
