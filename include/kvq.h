@@ -196,7 +196,7 @@ typedef enum {
     KVQ_ROPE_PARTS = 3,  /* f_i for pairs that turn more than `high` times over
                             orig_len positions, f_i / factor below `low` turns, in
                             between a ramp linear in i, its ends rounded outwards
-                            to whole pairs                                        */
+                            to whole pairs and kept within 0 .. r - 1             */
     KVQ_ROPE_BANDS = 4   /* the same with a ramp linear in the number of turns    */
 } kvq_rope_scaling;
 

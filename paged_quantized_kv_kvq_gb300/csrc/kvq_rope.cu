@@ -103,6 +103,7 @@ extern "C" kvq_status kvq_rope_init(const kvq_rope_config* c, kvq_rope_plan* out
                    !std::isfinite(c->high)))
     return KVQ_ERR_INVALID_ARG;
   double base = c->base, lo = 0.0, hi = 0.0;
+  bool all = false, none = false;  // KVQ_ROPE_PARTS: every pair is divided, or no pair
   if (c->scaling == KVQ_ROPE_BASE) {
     base *= std::pow(s, r / (r - 2.0));
     if (!std::isfinite(base)) return KVQ_ERR_INVALID_ARG;
@@ -110,8 +111,14 @@ extern "C" kvq_status kvq_rope_init(const kvq_rope_config* c, kvq_rope_plan* out
   if (c->scaling == KVQ_ROPE_PARTS) {
     // the (fractional) pair that turns `high` / `low` times over orig_len
     const double ln = 2.0 * std::log(base);
-    lo = std::max(std::floor(r * std::log(n / (2.0 * pi * c->high)) / ln), 0.0);
-    hi = std::min(std::ceil(r * std::log(n / (2.0 * pi * c->low)) / ln), r - 1.0);
+    lo = std::floor(r * std::log(n / (2.0 * pi * c->high)) / ln);
+    hi = std::ceil(r * std::log(n / (2.0 * pi * c->low)) / ln);
+    // even pair 0 turns no more than `low` times, or every pair more than `high`:
+    // the ends, each kept within 0 .. r-1, would meet or cross there
+    all = hi <= 0.0;
+    none = lo >= r - 1.0;
+    lo = std::max(lo, 0.0);
+    hi = std::min(hi, r - 1.0);
   }
   kvq_rope_plan p{};
   p.rotary_dim = r;
@@ -124,7 +131,7 @@ extern "C" kvq_status kvq_rope_init(const kvq_rope_config* c, kvq_rope_plan* out
       f /= s;
     } else if (c->scaling == KVQ_ROPE_PARTS) {
       const double width = hi != lo ? hi - lo : 0.001;
-      const double ramp = std::min(std::max((i - lo) / width, 0.0), 1.0);
+      const double ramp = all ? 1.0 : none ? 0.0 : std::min(std::max((i - lo) / width, 0.0), 1.0);
       f = f / s * ramp + f * (1.0 - ramp);
     } else if (c->scaling == KVQ_ROPE_BANDS) {
       const double turns = n * f / (2.0 * pi);
