@@ -516,7 +516,7 @@ kvq_status kvq_selftest_decode_timeout(const kvq_pool* pool, const kvq_half* q, 
 
 /* kvq_paged_decode_ex that also writes each row's log-sum-exp:
  *   lse : fp32 [num_seqs][num_q_heads], ln sum_t exp(q . k^_t * sm_scale); -inf
- *         for a sequence with L == 0
+ *         for a sequence with L == 0, NaN where a score is NaN
  * Results in `out` are those of kvq_paged_decode_ex, bit for bit. */
 kvq_status kvq_paged_decode_lse(const kvq_pool* pool, const kvq_half* q, int num_seqs,
                                 int num_q_heads, const int32_t* block_table,

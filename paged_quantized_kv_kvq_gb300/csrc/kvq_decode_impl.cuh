@@ -91,9 +91,9 @@ __device__ __forceinline__ int exponent_of(float x) {  // floor(log2 x) for norm
 }
 
 // Natural log of sum exp(z) from a base-2 running maximum and sum; -inf for an
-// empty row.
+// empty row, NaN for one with a NaN score (its sum is NaN).
 __device__ __forceinline__ float row_lse(float m, float l) {
-  return l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : __int_as_float(0xff800000u);
+  return l == 0.f ? __int_as_float(0xff800000u) : (m + log2f(l)) * 0.6931471805599453f;
 }
 
 __device__ __forceinline__ float warp_max_over_rows(float v) {  // reduce over lane>>2
@@ -1307,7 +1307,11 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const DecodePa
       float cm = M;
 #pragma unroll
       for (int c = 0; c < CH; ++c) cm = fmaxf(cm, mk[c]);
-      if (cm == kNegInf) continue;
+      if (cm == kNegInf) {  // no token yet, or NaN scores alone: sums of 0 or NaN
+#pragma unroll
+        for (int c = 0; c < CH; ++c) Lsum += lk[c];
+        continue;
+      }
       const float fo = M == kNegInf ? 0.f : fast_exp2(M - cm);
       Lsum *= fo;
 #pragma unroll
