@@ -214,7 +214,8 @@ typedef struct {
 } kvq_rope_config;
 
 /* A rotation ready for the kernels: plain data that the caller owns (no device
- * memory), good for any position, stream and device. */
+ * memory), good for any stream and device, and for any position within the
+ * accuracy that kvq_rope states. */
 typedef struct {
     int rotary_dim, layout;
     float magnitude;
@@ -245,7 +246,8 @@ typedef enum { KVQ_X_FP16 = 0, KVQ_X_BF16 = 1 } kvq_x_type;
  *                 out may be its own input (same pointer and stride); any other
  *                 overlap gives unspecified results
  * The arithmetic is fp32, rounded once to fp16; a cosine or sine is within 2^-20
- * at any position.  Errors: INVALID_ARG, UNSUPPORTED (head_dim, more than 8192
+ * at positions up to 2^27 either way, and within |position| * 2^-49 plus that
+ * farther out (the plan's fractions come from fp64).  Errors: INVALID_ARG, UNSUPPORTED (head_dim, more than 8192
  * heads, 2^31 tokens or more), CUDA. */
 kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
                     int64_t q_row_stride, int num_q_heads, const void* k, int64_t k_row_stride,

@@ -8,12 +8,14 @@
 // the pair being channels (i, i + r/2) or (2i, 2i+1).
 //
 // The angle.  A plan holds f_i / 2pi -- turns per position -- as a 64-bit
-// fraction; pos times it, modulo 2^64, is the position's fraction of a turn,
-// exact but for the 2^-65 of f_i itself (2^-34 of a turn at position 2^31),
-// where an fp32 angle at position 10^5 would be off by 2^-8.  Its top 32 bits,
-// taken as signed, give an angle in [-pi, pi) within 2^-23, and there the
-// hardware's sine and cosine are good to 2^-21: both sit far below the
-// rounding of what is stored (fp16, 2^-11, or 8-bit codes).  No table of
+// fraction; pos times it, modulo 2^64, is the position's fraction of a turn
+// without a rounding, where an fp32 angle at position 10^5 would be off by 2^-8.
+// What is off is the fraction itself: it comes from fp64 and is good to 2^-52 of a
+// turn (2^-55 measured), so 2^-22.3 radians at position 2^27, in proportion beyond.
+// Its top 32 bits, taken as signed, give an angle in [-pi, pi) within 2^-21.6 (the
+// conversion 2^-23.3, the factor 2^-23.5, the product 2^-23), and there the
+// hardware's sine and cosine are good to 2^-21.2: 2^-20 in all up to 2^27, far below
+// the rounding of what is stored (fp16, 2^-11, or 8-bit codes).  No table of
 // positions is read, so there is no longest position and no cache traffic.
 #pragma once
 #include <cstdint>
