@@ -13,6 +13,7 @@ codes with per-token, per-channel or per-group fp32 scales, or FP16
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -193,6 +194,18 @@ def _stream(stream):
         except AttributeError:
             stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """Context in which tensors are allocated for `stream`, the one that will use them:
+    filled in its order, and given to no other stream's work when they are freed while
+    it still runs.  (The current stream's needs none.)"""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _th()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t, dtype=None, name="tensor"):
@@ -734,7 +747,8 @@ def kvq_set_phase_events(events) -> None:
 
 # ------------------------------------------------------------------ convenience
 class KVPool:
-    """One layer's pool in caller-owned (torch) device memory."""
+    """One layer's pool in caller-owned (torch) device memory.  Calls with a `stream`
+    allocate what they return, and their workspaces, on that stream."""
 
     def __init__(self, num_blocks, block_size, kv_heads, head_dim, dtype, group=0, device="cuda",
                  fill_byte: int | None = None):
@@ -771,7 +785,8 @@ class KVPool:
         """Rotated (and normed) fp16 queries; keys and values go to the pool."""
         torch = _th()
         if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=torch.float16, device=q.device)
         kvq_rope_append(self.handle, plan, q, k, v, positions, slot_mapping, q_out, q_weight,
                         k_weight, eps, stream)
         return q_out
@@ -782,10 +797,11 @@ class KVPool:
         S, Hq, D = q.shape
         if sm_scale is None:
             sm_scale = D ** -0.5
-        if out is None:
-            out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
         nws = kvq_decode_workspace_bytes(self.handle, S, Hq, max_context_len, split_blocks)
-        ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=q.device) if nws else None
+        with _on(stream):
+            if out is None:
+                out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
+            ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=q.device) if nws else None
         kvq_paged_decode(self.handle, q, block_table, context_lens, max_context_len, sm_scale, out,
                          ws, split_blocks, stream)
         return out
@@ -796,10 +812,11 @@ class KVPool:
         S, Hq, D = q.shape
         if sm_scale is None:
             sm_scale = D ** -0.5
-        if out is None:
-            out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
         nws = kvq_decode_workspace_bytes(self.handle, S, Hq, max_context_len)
-        ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=q.device) if nws else None
+        with _on(stream):
+            if out is None:
+                out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
+            ws = torch.empty(max(nws, 1), dtype=torch.uint8, device=q.device) if nws else None
         kvq_decode_step(self.handle, k_new, v_new, q, block_table, context_lens, max_context_len,
                         sm_scale, out, ws, stream)
         return out
@@ -808,10 +825,11 @@ class KVPool:
         """decode's output and each row's log-sum-exp [S, Hq]."""
         torch = _th()
         S, Hq, D = q.shape
-        out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
-        lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
         nws = kvq_decode_workspace_bytes(self.handle, S, Hq, max_context_len)
-        ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
+        with _on(stream):
+            out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
+            lse = torch.empty((S, Hq), dtype=torch.float32, device=q.device)
+            ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
         kvq_paged_decode_lse(self.handle, q, block_table, context_lens, max_context_len,
                              D ** -0.5 if sm_scale is None else sm_scale, out, lse, ws, 0, stream)
         return out, lse
@@ -829,10 +847,11 @@ class KVPool:
         """(table, lens, kept, scores) after the eviction, in new tensors."""
         torch = _th()
         S = context_lens.numel()
-        table, lens = torch.empty_like(block_table), torch.empty_like(context_lens)
-        kept = torch.empty((S, budget_blocks), dtype=torch.int32, device=scores.device)
-        out = torch.zeros((S, self.kv_heads, max(budget_blocks * self.block_size, scores.shape[2])),
-                          dtype=torch.float32, device=scores.device)
+        with _on(stream):
+            table, lens = torch.empty_like(block_table), torch.empty_like(context_lens)
+            kept = torch.empty((S, budget_blocks), dtype=torch.int32, device=scores.device)
+            out = torch.zeros((S, self.kv_heads, max(budget_blocks * self.block_size, scores.shape[2])),
+                              dtype=torch.float32, device=scores.device)
         kvq_evict_blocks(self.handle, scores, block_table, context_lens, max_context_len,
                          budget_blocks, sink_blocks, recent_blocks, table, lens, kept, out, stream)
         return table, lens, kept, out
@@ -843,10 +862,11 @@ class KVPool:
         S, Hq, D = q.shape
         if sm_scale is None:
             sm_scale = D ** -0.5
-        if out is None:
-            out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
         nws = kvq_cascade_workspace_bytes(self.handle, S, Hq, max_context_len)
-        ws = torch.empty(max(nws, 256), dtype=torch.uint8, device=q.device)
+        with _on(stream):
+            if out is None:
+                out = torch.empty((S, Hq, D), dtype=torch.float32, device=q.device)
+            ws = torch.empty(max(nws, 256), dtype=torch.uint8, device=q.device)
         kvq_cascade_decode(self.handle, q, block_table, context_lens, max_context_len,
                            prefix_blocks, sm_scale, out, ws, stream)
         return out
@@ -857,23 +877,25 @@ class KVPool:
         cdt = torch.float16 if self.dtype == KVQ_FP16 else (
             torch.uint8 if self.dtype in (KVQ_FP8_E4M3_PER_TOKEN, KVQ_FP8_E5M2,
                                           KVQ_FP8_E4M3_PER_BLOCK) else torch.int8)
-        codes = torch.empty((n, 2, self.kv_heads, self.head_dim), dtype=cdt, device=slots.device)
-        scales = None
-        if self.dtype in GROUP_FORMATS:
-            scales = torch.empty((n, 2, self.kv_heads, self.head_dim // self.group),
-                                 dtype=torch.float32, device=slots.device)
-        elif self.dtype in (KVQ_INT8_PER_TOKEN, KVQ_FP8_E4M3_PER_TOKEN):
-            scales = torch.empty((n, 2), dtype=torch.float32, device=slots.device)
-        elif self.dtype in BLOCK_FORMATS:
-            scales = torch.empty((n, 2, self.kv_heads), dtype=torch.float32, device=slots.device)
+        with _on(stream):
+            codes = torch.empty((n, 2, self.kv_heads, self.head_dim), dtype=cdt, device=slots.device)
+            scales = None
+            if self.dtype in GROUP_FORMATS:
+                scales = torch.empty((n, 2, self.kv_heads, self.head_dim // self.group),
+                                     dtype=torch.float32, device=slots.device)
+            elif self.dtype in (KVQ_INT8_PER_TOKEN, KVQ_FP8_E4M3_PER_TOKEN):
+                scales = torch.empty((n, 2), dtype=torch.float32, device=slots.device)
+            elif self.dtype in BLOCK_FORMATS:
+                scales = torch.empty((n, 2, self.kv_heads), dtype=torch.float32, device=slots.device)
         kvq_read_slots(self.handle, slots, codes, scales, stream)
         return codes, scales
 
     def read_values(self, slots, stream=None):
         torch = _th()
-        k = torch.empty((slots.numel(), self.kv_heads, self.head_dim), dtype=torch.float16,
-                        device=slots.device)
-        v = torch.empty_like(k)
+        with _on(stream):
+            k = torch.empty((slots.numel(), self.kv_heads, self.head_dim), dtype=torch.float16,
+                            device=slots.device)
+            v = torch.empty_like(k)
         kvq_read_values(self.handle, slots, k, v, stream)
         return k, v
 
