@@ -891,11 +891,13 @@ class KVPool:
         return codes, scales
 
     def read_values(self, slots, stream=None):
+        """fp16 K and V [n, kv_heads, head_dim] of the slots; zeros for negative ones and
+        for slots outside the pool."""
         torch = _th()
         with _on(stream):
-            k = torch.empty((slots.numel(), self.kv_heads, self.head_dim), dtype=torch.float16,
+            k = torch.zeros((slots.numel(), self.kv_heads, self.head_dim), dtype=torch.float16,
                             device=slots.device)
-            v = torch.empty_like(k)
+            v = torch.zeros_like(k)
         kvq_read_values(self.handle, slots, k, v, stream)
         return k, v
 

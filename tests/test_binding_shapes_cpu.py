@@ -98,3 +98,15 @@ def test_a_handle_carries_its_shape(monkeypatch):
 
     monkeypatch.setattr(kvq, "lib", lambda: Lib())
     assert kvq.kvq_alloc_pool(7, 32, 5, 64, kvq.KVQ_FP16).shape == (32, 5, 64)
+
+
+def test_read_values_leaves_no_row_undefined(monkeypatch):
+    """Rows of padding and of slots outside the pool, which the library does not write."""
+    pool = kvq.KVPool.__new__(kvq.KVPool)
+    pool.handle, pool.kv_heads, pool.head_dim = HANDLE, HKV, D
+    monkeypatch.setattr(kvq, "kvq_read_values", lambda *a: None)
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: torch.full(*a, float("nan"), **kw))
+    monkeypatch.setattr(torch, "empty_like", lambda t: torch.full(t.shape, float("nan"), dtype=t.dtype))
+    k, v = kvq.KVPool.read_values(pool, _ints(3, dtype=torch.int64))
+    pool.handle = None
+    assert k.shape == v.shape == (3, HKV, D) and (k == 0).all() and (v == 0).all()
