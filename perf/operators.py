@@ -37,7 +37,8 @@ def listed():
         # a decode step's new tokens of 64 sequences into an INT8 per-group pool
         {"name": "append_step", "op": "append", "S": 64, "n": 1, "hq": 32, "hkv": 8, "d": 128, "rot": 128,
          "interleaved": False, "scaling": "none", "norm": True, "dtype": "fp16", "fmt": "int8_group", "group": 128, "bs": 16},
-        # the same into partly filled blocks with one scale each (their older codes are rescaled)
+        # the same into partly filled blocks with one scale each, whose older codes are rescaled: sequences forked from
+        # one prompt, each of which takes its own copy of its last block before it appends to it
         {"name": "append_step_block", "op": "append", "S": 61, "n": 1, "hq": 24, "hkv": 4, "d": 128, "rot": 128,
          "interleaved": True, "scaling": "linear", "norm": False, "dtype": "bf16", "fmt": "int8_block", "group": 0, "bs": 32},
         # prompts of 8 x 2048 tokens into blocks with one scale each
@@ -355,11 +356,17 @@ def prepare(c, seed):
         else:
             s["read"] = s["slots"]
         if own:
-            s["pool"] = kvq.KVPool(num, c["bs"], c["hkv"], c["d"], getattr(kvq, FORMATS[c["fmt"]][0]), c["group"], device=DEV)
-            if "block" in c["fmt"] and s["before"] is not None:
+            # a block that grows takes its scale with it, so the older tokens stay in blocks of their own, which every
+            # pass copies: appending to the same blocks once more would find their scales grown already
+            forks = "block" in c["fmt"] and s["before"] is not None
+            s["pool"] = kvq.KVPool(2 * num if forks else num, c["bs"], c["hkv"], c["d"], getattr(kvq, FORMATS[c["fmt"]][0]),
+                                   c["group"], device=DEV)
+            if forks:
                 o = np.arange(c["bs"])
-                was = np.where(o < old[:, None], blocks[:, None] * c["bs"] + o, -1).reshape(-1)
+                was = np.where(o < old[:, None], (num + blocks[:, None]) * c["bs"] + o, -1).reshape(-1)
                 s["pool"].append(s["before"][0].flatten(0, 1), s["before"][1].flatten(0, 1), torch.from_numpy(was).to(DEV))
+                s["to"] = torch.from_numpy(blocks.astype(np.int32)).to(DEV)
+                s["from"] = s["to"] + num
             n = s["read"].numel()
             s["k_values"] = torch.empty((n, c["hkv"], c["d"]), dtype=torch.float16, device=DEV)
             s["v_values"] = torch.empty_like(s["k_values"])
@@ -419,6 +426,8 @@ def _own(s):
         return {"q": s["q_out"], "k": s["k_out"]}
     h = s["pool"].handle
     if c["op"] == "append":
+        if "from" in s:
+            kvq.kvq_copy_blocks(h, s["from"], s["to"])
         kvq.kvq_rope_append(h, s["plan"], s["q"], s["k"], s["v"], s["positions"], s["slots"], s["q_out"], s["q_weight"],
                             s["k_weight"], EPS)
         kvq.kvq_read_values(h, s["read"], s["k_values"], s["v_values"])
