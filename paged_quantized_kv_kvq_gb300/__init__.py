@@ -92,7 +92,15 @@ class PoolHandle(ctypes.c_void_p):
     """A kvq_pool* with the shape it was allocated with: (block_size, kv_heads,
     head_dim).  The library sees addresses only; tensors are held against this."""
 
-    shape = None
+    rows = None  # (kv_heads, head_dim) of a token, as a tensor's shape would have them
+
+    @property
+    def shape(self):
+        return self._shape
+
+    @shape.setter
+    def shape(self, shape):
+        self._shape, self.rows = shape, tuple(shape[1:])
 
 
 def header_functions() -> list[str]:
@@ -344,42 +352,39 @@ def _x_rows(t, dtype, T, D, name, dev):
     return t.data_ptr(), stride[0], shape[1]
 
 
-def _pool_shape(pool):
+def _pool_rows(pool):
     """(kv_heads, head_dim) of a handle made by kvq_alloc_pool; None for any other,
     which has to be the caller's care."""
-    shape = getattr(pool, "shape", None)
-    return None if shape is None else shape[1:]
+    return getattr(pool, "rows", None)
 
 
-def _check_pool_rows(pool, k, D):
-    """[T, kv_heads, head_dim] rows that the kernels read with the pool's own sizes."""
-    shape = _pool_shape(pool)
-    if shape is not None and (k.shape[1] != shape[0] or D != shape[1]):
-        raise ValueError("k, v must have the pool's %d kv heads of %d channels" % shape)
-
-
-def _check_seqs(pool, q, block_table, context_lens):
-    """S, Hq of q [S, Hq, head_dim], held against the pool, the table and the lengths."""
-    if len(q.shape) != 3:
+def _seqs(pool, q, block_table, context_lens):
+    """S, Hq of q [S, Hq, head_dim] and max_blocks_per_seq, held against each other and
+    the pool."""
+    shape, table = q.shape, block_table.shape
+    if len(shape) != 3:
         raise ValueError("q must be [num_seqs, num_q_heads, head_dim]")
-    S, Hq, D = q.shape
-    shape = _pool_shape(pool)
-    if shape is not None:
-        if D != shape[1]:
-            raise ValueError("q must have the pool's head_dim of %d" % shape[1])
-        if Hq % shape[0] != 0:
-            raise ValueError("q's heads must be a multiple of the pool's %d kv heads" % shape[0])
-    if len(block_table.shape) != 2 or block_table.shape[0] != S:
+    S, Hq, D = shape
+    rows = _pool_rows(pool)
+    if rows is not None and (D != rows[1] or Hq % rows[0] != 0):
+        raise ValueError("q must have the pool's head_dim of %d and a multiple of its %d kv heads"
+                         % (rows[1], rows[0]))
+    if len(table) != 2 or table[0] != S:
         raise ValueError("block_table must be [num_seqs, max_blocks_per_seq]")
     if context_lens.numel() != S:
         raise ValueError("context_lens must be [num_seqs]")
-    return S, Hq
+    return S, Hq, table[1]
 
 
-def _check_score_heads(pool, scores):
-    shape = _pool_shape(pool)
-    if shape is not None and scores.shape[1] != shape[0]:
-        raise ValueError("scores must have the pool's %d kv heads" % shape[0])
+def _scores_width(pool, scores, S):
+    """Tokens of scores [S, kv_heads, tokens], held against the pool."""
+    shape = scores.shape
+    if len(shape) != 3 or shape[0] != S:
+        raise ValueError("scores must be [num_seqs, kv_heads, tokens]")
+    rows = _pool_rows(pool)
+    if rows is not None and shape[1] != rows[0]:
+        raise ValueError("scores must have the pool's %d kv heads" % rows[0])
+    return shape[2]
 
 
 def _x_type(dtype, name):
@@ -450,10 +455,12 @@ def kvq_rope_append(pool, plan, q, k, v, positions, slot_mapping, q_out=None, q_
     dtype = k.dtype
     x_type = _x_type(dtype, "k")
     dev = _device()
-    T, _, D = k.shape
-    if v.shape != k.shape or slot_mapping.numel() != T:
+    shape, rows = k.shape, _pool_rows(pool)
+    if v.shape != shape or len(shape) != 3 or slot_mapping.numel() != shape[0]:
         raise ValueError("k, v must be [T, kv_heads, head_dim] and slot_mapping [T]")
-    _check_pool_rows(pool, k, D)
+    T, H, D = shape
+    if rows is not None and rows != (H, D):
+        raise ValueError("k, v must have the pool's %d kv heads of %d channels" % rows)
     kp, ks, _ = _x_rows(k, dtype, T, D, "k", dev)
     vp, vs, _ = _x_rows(v, dtype, T, D, "v", dev)
     qp, qs, hq, qo, qos = None, 0, 0, None, 0
@@ -517,7 +524,7 @@ def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm
     """kvq_paged_decode that also writes each row's log-sum-exp, lse [S, Hq] fp32
     (kvq_paged_decode_lse in include/kvq.h)."""
     torch = _th()
-    S, Hq = _check_seqs(pool, q, block_table, context_lens)
+    S, Hq, max_blocks = _seqs(pool, q, block_table, context_lens)
     if lse.shape != (S, Hq):
         raise ValueError("lse must be [num_seqs, num_q_heads]")
     if out.shape != q.shape:
@@ -526,7 +533,7 @@ def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_paged_decode_lse(
         pool, _at(q, torch.float16, "q", dev), S, Hq, _at(block_table, torch.int32, "block_table", dev),
-        block_table.shape[1], _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len),
+        max_blocks, _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len),
         float(sm_scale), _at(out, torch.float32, "out", dev), _at(lse, torch.float32, "lse", dev),
         None if workspace is None else _at(workspace, workspace.dtype, "workspace", dev), ws_bytes,
         int(split_blocks), _stream(stream)), "kvq_paged_decode_lse")
@@ -538,18 +545,18 @@ def kvq_attention_weights(pool, q, block_table, context_lens, max_context_len, s
     added to decay * prev: scores [S, Hkv, >= max_context_len] fp32
     (kvq_attention_weights in include/kvq.h).  prev may be scores itself."""
     torch = _th()
-    S, Hq = _check_seqs(pool, q, block_table, context_lens)
-    if scores.dim() != 3 or scores.shape[0] != S or lse.shape != (S, Hq):
-        raise ValueError("scores must be [num_seqs, kv_heads, tokens] and lse [num_seqs, num_q_heads]")
-    _check_score_heads(pool, scores)
-    if prev is not None and prev.shape != scores.shape:
+    S, Hq, max_blocks = _seqs(pool, q, block_table, context_lens)
+    width = _scores_width(pool, scores, S)
+    if lse.shape != (S, Hq):
+        raise ValueError("lse must be [num_seqs, num_q_heads]")
+    if prev is not None and prev is not scores and prev.shape != scores.shape:
         raise ValueError("prev must have the shape of scores")
     dev = _device()
     _check(lib().kvq_attention_weights(
         pool, _at(q, torch.float16, "q", dev), S, Hq, _at(block_table, torch.int32, "block_table", dev),
-        block_table.shape[1], _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len),
+        max_blocks, _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len),
         float(sm_scale), _at(lse, torch.float32, "lse", dev), float(decay),
-        _at(prev, torch.float32, "prev", dev), _at(scores, torch.float32, "scores", dev), scores.shape[2],
+        _at(prev, torch.float32, "prev", dev), _at(scores, torch.float32, "scores", dev), width,
         _stream(stream)), "kvq_attention_weights")
 
 
@@ -562,10 +569,10 @@ def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, b
     table_out and lens_out may be block_table and context_lens themselves."""
     torch = _th()
     S = context_lens.numel()
-    if scores.dim() != 3 or scores.shape[0] != S or block_table.dim() != 2 or block_table.shape[0] != S:
-        raise ValueError("scores must be [num_seqs, kv_heads, tokens] and block_table [num_seqs, blocks]")
-    _check_score_heads(pool, scores)
-    if table_out.shape != block_table.shape or lens_out.numel() != S:
+    width, table = _scores_width(pool, scores, S), block_table.shape
+    if len(table) != 2 or table[0] != S:
+        raise ValueError("block_table must be [num_seqs, blocks]")
+    if (table_out is not block_table and table_out.shape != table) or lens_out.numel() != S:
         raise ValueError("table_out and lens_out must be shaped like block_table and context_lens")
     if kept is not None and kept.shape != (S, budget_blocks):
         raise ValueError("kept must be [num_seqs, budget_blocks]")
@@ -573,8 +580,8 @@ def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, b
         raise ValueError("scores_out must be [num_seqs, kv_heads, tokens]")
     dev = _device()
     _check(lib().kvq_evict_blocks(
-        pool, _at(scores, torch.float32, "scores", dev), scores.shape[2], S,
-        _at(block_table, torch.int32, "block_table", dev), block_table.shape[1],
+        pool, _at(scores, torch.float32, "scores", dev), width, S,
+        _at(block_table, torch.int32, "block_table", dev), table[1],
         _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len), int(budget_blocks),
         int(sink_blocks), int(recent_blocks), _at(table_out, torch.int32, "table_out", dev),
         _at(lens_out, torch.int32, "lens_out", dev), _at(kept, torch.int32, "kept", dev),
@@ -716,12 +723,11 @@ def kvq_read_values(pool, slots, k_out, v_out, stream=None) -> None:
     """Cached K and V of the slots as fp16 values, [n, kv_heads, head_dim] each
     (kvq_read_values in include/kvq.h)."""
     torch = _th()
-    shape = _pool_shape(pool)
-    if k_out.shape != v_out.shape or k_out.dim() != 3 or k_out.shape[0] != slots.numel() or (
-            shape is not None and k_out.shape[1:] != shape):
+    shape, rows, n = k_out.shape, _pool_rows(pool), slots.numel()
+    if v_out.shape != shape or len(shape) != 3 or shape[0] != n or (rows is not None and shape[1:] != rows):
         raise ValueError("k_out, v_out must be [n, kv_heads, head_dim]")
     dev = _device()
-    _check(lib().kvq_read_values(pool, _at(slots, torch.int64, "slots", dev), slots.numel(),
+    _check(lib().kvq_read_values(pool, _at(slots, torch.int64, "slots", dev), n,
                                  _at(k_out, torch.float16, "k_out", dev),
                                  _at(v_out, torch.float16, "v_out", dev), _stream(stream)),
            "kvq_read_values")

@@ -48,7 +48,7 @@ def _decode(**kw):
 
 @pytest.mark.parametrize("kw,match", [
     (dict(q=_half(3, 4, 64), out=torch.zeros((3, 4, 64))), "head_dim of 128"), (dict(q=_half(3, 3, D), out=torch.zeros((3, 3, D)),
-                                                                                lse=torch.zeros((3, 3))), "multiple"),
+                                                                                lse=torch.zeros((3, 3))), "multiple of its 2"),
     (dict(block_table=_ints(2, 6)), "block_table"), (dict(block_table=_ints(18)), "block_table"),
     (dict(context_lens=_ints(2)), "context_lens"), (dict(out=torch.zeros((3, 4, 64))), "out must"),
     (dict(out=torch.zeros((2, 4, D))), "out must"), (dict(q=_half(12, D)), "q must"), (dict(lse=torch.zeros((2, 4))), "lse must")])
