@@ -183,7 +183,9 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
 cudaError_t launch_read_values(const PoolView& pool, const int64_t* slots, int64_t n, __half* k,
                                __half* v, cudaStream_t st) {
   // Threads of 16 slots: all 128 for a short call's latency, the 4 per 8 channels that
-  // a sub-tile takes for a long one.
+  // a sub-tile takes for a long one.  (8 heads of 128, slots in order: 1024 slots 2.7 and
+  // 2.8 us, 2048 4.0 and 3.7, 16384 22.2 and 19.4; scattered: 256 2.9 and 3.7, 2048 5.9
+  // and 6.1, 16384 36.1 and 32.4.)
   const int tpt_log2 = n < 2048 ? 7 : pool.D == 64 ? 5 : 6;
   const int64_t spc = kValueSlots << (7 - tpt_log2), gx = (n + spc - 1) / spc;
   if (gx > 0x7fffffffLL || pool.Hkv > 65535) return cudaErrorInvalidValue;
@@ -234,18 +236,27 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   if (a.plan != nullptr) p.plan = *a.plan;
   while ((1 << p.bs_log2) < a.pool.bs) ++p.bs_log2;
   // Few tokens (a decode step, a short prompt): one per CTA, and one head per CTA
-  // (four above 128 tokens) for the latency of a run.  Many: a block's worth of
-  // tokens per CTA, and heads for kIngestRounds rounds of its warps, which share its
-  // angles.  Formats with one scale per token need every head of a token in one CTA.
+  // (four above 128 tokens) for the latency of a run.  Many: several tokens per
+  // CTA, and heads for kIngestRounds rounds of its warps, which share its angles.
+  // (Prompts with 32 query heads: 1000 tokens 19.6 us as few, 23.2 as many, 2048
+  // tokens 33.8 and 17.2; single tokens 23.9 and 25.7, 46.1 and 30.0.  One head per CTA
+  // against four: 128 tokens 7.3 and 7.8 us, 256 tokens 10.3 and 8.7, single tokens
+  // 7.6 and 5.3, 11.6 and 6.5.)  Formats with one scale per token need every head of a
+  // token in one CTA.
   // A long call's query rows go to a kernel of their own, launched beside this
   // one: this one's 128 registers leave an SM 16 warps, too few loads in flight
   // for the rows that are most of the bytes (16384 tokens, 32 Q and 8 kv heads:
   // 154 us in one kernel).
   const bool many = a.T >= 1024;
   const bool tok = a.pool.fmt == FMT_INT8_TOKEN || a.pool.fmt == FMT_FP8_TOKEN;
-  // (A long call may also be a step of many sequences, each token a run of its own,
-  // which a CTA takes one after the other: 8 tokens per CTA below 16384.)
-  p.tpc = !many || a.slots == nullptr ? 1 : a.T < 16384 ? std::min(a.pool.bs, 8) : a.pool.bs;
+  // A long call's CTA takes 8 tokens whatever the call's length: its runs may be whole
+  // blocks, chunks that begin inside one, or single tokens, and the last two it takes one
+  // after the other.  8 kv heads, blocks of 16, 16384 tokens with 4, 8 and 16 a CTA:
+  // prompts of whole blocks 52.3, 45.8 and 42.5 us (the CTAs that own no run cost that
+  // much), chunks from inside a block 84.4, 76.7 and 81.9, single tokens 153.5, 158.7
+  // and 163.6, a prompt with 64 single tokens 52.6, 54.6 and 69.5; 2048 tokens: 16.7,
+  // 15.2 and 13.1; 40.2, 38.3 and 47.7; 29.7, 27.5 and 44.0; 16.9, 23.5 and 40.0.
+  p.tpc = !many || a.slots == nullptr ? 1 : std::min(a.pool.bs, 8);
   const int round_heads = std::max(1, kIngestWarps * 1024 / (std::max(a.pool.bs, 16) * a.pool.D));
   p.hpc = tok ? a.pool.Hkv : many ? kIngestRounds * round_heads : a.T > 128 ? 4 : 1;
   p.hsplit = (a.pool.Hkv + p.hpc - 1) / p.hpc;
