@@ -345,11 +345,13 @@ def _x_rows(t, dtype, T, D, name, dev):
     shape, stride = t.shape, t.stride()
     if t.dtype != dtype or len(shape) != 3 or shape[0] != T or shape[2] != D:
         raise ValueError("%s must be [%d, heads, %d] of %s like the other rows" % (name, T, D, dtype))
-    if stride[2] != 1 or stride[1] != D:
+    H = shape[1]
+    if stride[2] != 1 or (stride[1] != D and H != 1):
         raise ValueError("%s must be [rows, heads, head_dim] with contiguous heads" % name)
     if t.get_device() != dev:
         raise ValueError("%s must be on the current CUDA device" % name)
-    return t.data_ptr(), stride[0], shape[1]
+    # (the stride along a dimension of one says nothing)
+    return t.data_ptr(), stride[0] if T > 1 else H * D, H
 
 
 def _pool_rows(pool):
