@@ -161,12 +161,12 @@ kvq_status kvq_calibrate_channel_scales(kvq_pool* pool, const kvq_half* k, const
  * per-block formats that of the whole block).
  * Formats with one scale per block quantize a block's tokens together, so the
  * tokens of one call that fall into one block must stand next to each other in
- * slot_mapping, with no padding between them (as every mapping made sequence by
- * sequence has them; otherwise that block's contents are unspecified).  The
- * block's scale becomes
+ * slot_mapping, with nothing between them, be it padding, a slot outside the pool
+ * or another block's token (as every mapping made sequence by sequence has them;
+ * otherwise that block's contents are unspecified).  The block's scale becomes
  * s = max(s_old, absmax of the call's tokens in it / 127 (448)); a token at
- * offset 0 starts the block anew, with no s_old and nothing kept of what it
- * held.  Where s grew, the block's other codes are rounded again at the new
+ * offset 0 starts the block anew, with no s_old, and offsets that the call does
+ * not write are unspecified from then on.  Where s grew, the block's other codes are rounded again at the new
  * scale: code' = round(code * s_old / s) in fp32.  The append owns the whole
  * block: no other work may read or write it meanwhile.
  * Device errors: a slot >= num_blocks*block_size sets OUT_OF_RANGE and the
@@ -245,7 +245,9 @@ typedef enum { KVQ_X_FP16 = 0, KVQ_X_BF16 = 1 } kvq_x_type;
  *   q_out, k_out : fp16, laid out like q and k with strides of their own.  An
  *                 out may be its own input (same pointer and stride); any other
  *                 overlap gives unspecified results
- * The arithmetic is fp32, rounded once to fp16; a cosine or sine is within 2^-20
+ * The arithmetic is fp32, rounded once to fp16 (beyond 65504, as bf16 rows may be,
+ * to an infinity).  The norm's squares are summed in fp32: heads with values beyond
+ * 1e18, or with eps = 0 all below 1e-19, are outside its range.  A cosine or sine is within 2^-20
  * at positions up to 2^27 either way, and within |position| * 2^-49 plus that
  * farther out (the plan's fractions come from fp64).  Errors: INVALID_ARG, UNSUPPORTED (head_dim, more than 8192
  * heads, 2^31 tokens or more), CUDA. */
@@ -258,7 +260,8 @@ kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
 
 /* kvq_rope of queries and keys and kvq_append of keys and values in one kernel:
  * the normed and rotated keys are quantized from fp32 (an append of kvq_rope's
- * k_out would first have rounded them to fp16) and reach memory only as codes.
+ * k_out would first have rounded them to fp16) and reach memory only as codes (an
+ * FP16 pool's with fp16's range, as above).
  *   k, v        : [T][kv_heads][head_dim] of the pool, fp16 or bf16, strided as
  *                 above; v is neither normed nor rotated
  *   slot_mapping : as for kvq_append, with its rule for per-block formats (a slot
@@ -553,7 +556,8 @@ kvq_status kvq_attention_weights(const kvq_pool* pool, const kvq_half* q, int nu
  * weighs the sum of its tokens' scores over the kv heads, rounded once to fp32.
  * Of a sequence with more than budget_blocks blocks the first sink_blocks and
  * the last recent_blocks stay, and the heaviest of the others up to
- * budget_blocks in all (equal weights: the lower index stays; NaN weighs -inf).
+ * budget_blocks in all (equal weights: the lower index stays; NaN weighs -inf; a
+ * sum of mixed signs that leaves fp32's range on its way is infinite or NaN).
  * No cached data moves.  Keys are cached with their positions' rotation in them,
  * so attention over the kept blocks needs no more than the new row.
  *   pool          : only its block size, kv heads and error word are used

@@ -22,9 +22,12 @@
 //
 // Sums.  Two blocks next to the border may differ in the last bits, and which
 // of them stays must not depend on the order of a sum: each block's is carried
-// as an fp32 sum with the sum of its rounding errors (good to 2^-44) and rounded
-// to fp32 once, the same value that a sum in fp64 rounds to.  (fp64 itself runs at 1/64 of the
-// fp32 rate here.)
+// as an fp32 sum with the sum of its rounding errors and rounded to fp32 once.  Over
+// n additions in a chain (heads and log2 of the block size) the errors sum to at most
+// n 2^-25 of the magnitudes and are themselves rounded n times: good to n^2 2^-49 (12
+// for 8 heads, 2^-41), so the value is that of a sum in fp64 unless this one
+// lies that close to the middle between two fp32 values.  (fp64 itself runs at 1/64 of
+// the fp32 rate here.)
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -11,9 +11,11 @@
 //  * a 16-token sub-tile that the run covers is assembled in shared memory and
 //    leaves as 16-byte stores, although its bytes interleave tokens.
 // Bounds: the instructions that norm, rotate and quantize for prompts (16384
-// tokens x 8 heads into INT8 blocks: 46 us, 26 million warp instructions, where HBM
+// tokens x 8 heads into INT8 blocks: 46 us, 27 million warp instructions, where HBM
 // would take 15), latency for a decode step (one token per run: slot -> rows ->
-// absmax -> codes; 8.5 us for 64 tokens with their 32 query heads).
+// absmax -> codes; 5.9 us for 64 tokens with their 32 query heads into INT8 groups;
+// into INT8 blocks 61 tokens take 4.4 us where no scale grows and 11 where nearly
+// every one does, whose older codes are read, rounded again and written).
 //
 // One scale per (block, head): s = max(s_old, absmax / top) in fp32, where top
 // is 127 or 448 and s_old the block's scale, unless the run writes offset 0,
@@ -474,6 +476,11 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
 // memory.  A warp's unit is 8 such tokens of one head of 128 channels (16 of one of
 // 64): 32 values a lane.  (Whole sub-tiles, 64 values, left an SM 16 warps and the
 // kernel waiting for its loads: 75 us for 16384 tokens x 8 heads.)
+// INT4, whose words pack tokens t and t + 8, and the formats whose scale spans a
+// token's heads are not built this way; they take every run through shared memory, the
+// latter loading and rotating each row twice: 16384 tokens x 8 heads of 128 in 132 us
+// and 111 to 119, where FP16 takes 36, e5m2 38, INT8 blocks 46, INT8 groups and e4m3
+// blocks 59, per-channel 72.
 template <int FMT>
 constexpr bool whole_blocks() {
   return FMT != FMT_INT4_GROUP && FMT != FMT_INT8_TOKEN && FMT != FMT_FP8_TOKEN;
@@ -690,8 +697,8 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
 
 // Resident CTAs to compile for: whole blocks need some 96 registers with the rows of
 // the next round on their way, a run held in registers 8 more per chunk.  (16384
-// tokens with their queries and the read-back: 96.1 us; with four CTAs 96.6, with six
-// 98.0, with six and no rows ahead 96.9.)
+// tokens with their queries and the read-back, 16 tokens a CTA: 96.1 us; with four
+// CTAs 96.6, with six 98.0, with six and no rows ahead 96.9.)
 constexpr int ingest_ctas(int cpt) { return cpt <= 4 ? 5 : 3; }
 
 template <int FMT, int D, int CPT>

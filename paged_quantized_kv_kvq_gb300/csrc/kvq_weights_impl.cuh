@@ -10,8 +10,9 @@
 //
 // Bound: HBM -- the K half of the pages once (half of a decode's bytes) and
 // 8 bytes of scores per (token, kv head) -- and close behind it the conversion of
-// the codes: a 16-token sub-tile of 128 channels is 2 KB and some 120 warp
-// instructions, 64 of them to make fp16 fragments.
+// the codes: a 16-token sub-tile of 128 channels is 2 KB and some 240 warp
+// instructions (counted over 8 x 32768 tokens x 8 heads), 64 of them to make fp16
+// fragments and 8 products; the rest looks after pages, stages and partial sums.
 // The grid is persistent and balanced like the decode's: the stages (32 tokens or
 // a page) of all (sequence, kv head) rows form one index space that the warps cut
 // into equal contiguous ranges, so no warp idles behind a short sequence and the
