@@ -247,8 +247,8 @@ typedef enum { KVQ_X_FP16 = 0, KVQ_X_BF16 = 1 } kvq_x_type;
  *                 overlap gives unspecified results
  * The arithmetic is fp32, rounded once to fp16 (beyond 65504, as bf16 rows may be,
  * to an infinity).  The norm's squares are summed in fp32: heads with values beyond
- * 1e18, or with eps = 0 all below 1e-19, are outside its range.  A cosine or sine is within 2^-20
- * at positions up to 2^27 either way, and within |position| * 2^-49 plus that
+ * 1e18, or with eps = 0 all below 1e-19, are outside its range.  A cosine or sine is within 2^-22
+ * at positions up to 2^26 either way, and within |position| * 2^-49 plus that
  * farther out (the plan's fractions come from fp64).  Errors: INVALID_ARG, UNSUPPORTED (head_dim, more than 8192
  * heads, 2^31 tokens or more), CUDA. */
 kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,

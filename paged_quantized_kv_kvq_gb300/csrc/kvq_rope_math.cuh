@@ -11,12 +11,16 @@
 // fraction; pos times it, modulo 2^64, is the position's fraction of a turn
 // without a rounding, where an fp32 angle at position 10^5 would be off by 2^-8.
 // What is off is the fraction itself: it comes from fp64 and is good to 2^-52 of a
-// turn (2^-55 measured), so 2^-22.3 radians at position 2^27, in proportion beyond.
-// Its top 32 bits, taken as signed, give an angle in [-pi, pi) within 2^-21.6 (the
-// conversion 2^-23.3, the factor 2^-23.5, the product 2^-23), and there the
-// hardware's sine and cosine are good to 2^-21.2: 2^-20 in all up to 2^27, far below
-// the rounding of what is stored (fp16, 2^-11, or 8-bit codes).  No table of
-// positions is read, so there is no longest position and no cache traffic.
+// turn (2^-55 measured), so 2^-23.3 radians at position 2^26, in proportion beyond.
+// The top 32 bits, less the nearest quarter turn, give an angle in [-pi/4, pi/4] within
+// 2^-23.6 (the conversion 2^-25.3, the factor 2^-25.4, the product 2^-25), and the
+// Taylor series of sine and cosine there, to x^9 and x^10 (the next terms are below
+// 2^-29), round by 2^-24: 2^-23 in all, 2^-22 with the fraction up to position 2^26.
+// That is at the level of the norm's and the rotation's own roundings, so that a key
+// falls on the other side of a code's border no more often for it.  (The hardware's
+// sine and cosine, 2^-21, did so three times as often: 12 codes of 64 x 8 x 128 x 60
+// against 4 of fp64 angles.)  No table of positions is read, so there is no longest
+// position and no cache traffic.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -29,11 +33,16 @@ namespace kvq {
 
 // cos and sin (times the plan's magnitude) of `pos` at `turn` turns per position.
 __device__ __forceinline__ float2 rope_cs(uint64_t turn, int64_t pos, float magnitude) {
-  const uint64_t frac = turn * static_cast<uint64_t>(pos);
-  const float a = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 1.4629180792671596e-9f;
-  float s, c;
-  __sincosf(a, &s, &c);  // a = 2 pi * fraction of a turn
-  return make_float2(c * magnitude, s * magnitude);
+  const uint32_t frac = static_cast<uint32_t>(turn * static_cast<uint64_t>(pos) >> 32);
+  const uint32_t quarter = (frac + 0x20000000u) >> 30;  // the nearest, modulo four
+  const float a = static_cast<float>(static_cast<int32_t>(frac - (quarter << 30))) * 1.4629180792671596e-9f;
+  const float x = a * a;  // (a: 2 pi / 2^32 times what is left)
+  const float s = fmaf(a * x, fmaf(fmaf(fmaf(1.f / 362880, x, -1.f / 5040), x, 1.f / 120), x, -1.f / 6), a);
+  const float c = fmaf(fmaf(fmaf(fmaf(fmaf(-1.f / 3628800, x, 1.f / 40320), x, -1.f / 720), x, 1.f / 24), x, -0.5f), x, 1.f);
+  // a quarter turn takes (cos, sin) to (-sin, cos)
+  const uint32_t u = __float_as_uint(quarter & 1 ? s : c) ^ ((quarter + 1) & 2) << 30;
+  const uint32_t v = __float_as_uint(quarter & 1 ? c : s) ^ (quarter & 2) << 30;
+  return make_float2(__uint_as_float(u) * magnitude, __uint_as_float(v) * magnitude);
 }
 
 // Cosines and sines of tokens 0 .. n-1 (their positions at `pos`): cs[t][pair].
