@@ -238,10 +238,10 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   // Few tokens (a decode step, a short prompt): one per CTA, and one head per CTA
   // (four above 128 tokens) for the latency of a run.  Many: several tokens per
   // CTA, and heads for kIngestRounds rounds of its warps, which share its angles.
-  // (Prompts with 32 query heads: 1000 tokens 19.6 us as few, 23.2 as many, 2048
-  // tokens 33.8 and 17.2; single tokens 23.9 and 25.7, 46.1 and 30.0.  One head per CTA
-  // against four: 128 tokens 7.3 and 7.8 us, 256 tokens 10.3 and 8.7, single tokens
-  // 7.6 and 5.3, 11.6 and 6.5.)  Formats with one scale per token need every head of a
+  // (Prompts with 32 query heads: 1000 tokens 19.7 us as few, 23.5 as many, 2048
+  // tokens 34.5 and 17.7; single tokens 24.4 and 26.0, 47.0 and 30.4.  One head per CTA
+  // against four: 128 tokens 7.5 and 8.0 us, 256 tokens 10.5 and 8.8, single tokens
+  // 7.6 and 5.2, 11.7 and 6.5.)  Formats with one scale per token need every head of a
   // token in one CTA.
   // A long call's query rows go to a kernel of their own, launched beside this
   // one: this one's 128 registers leave an SM 16 warps, too few loads in flight
@@ -252,10 +252,10 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
   // A long call's CTA takes 8 tokens whatever the call's length: its runs may be whole
   // blocks, chunks that begin inside one, or single tokens, and the last two it takes one
   // after the other.  8 kv heads, blocks of 16, 16384 tokens with 4, 8 and 16 a CTA:
-  // prompts of whole blocks 52.3, 45.8 and 42.5 us (the CTAs that own no run cost that
-  // much), chunks from inside a block 84.4, 76.7 and 81.9, single tokens 153.5, 158.7
-  // and 163.6, a prompt with 64 single tokens 52.6, 54.6 and 69.5; 2048 tokens: 16.7,
-  // 15.2 and 13.1; 40.2, 38.3 and 47.7; 29.7, 27.5 and 44.0; 16.9, 23.5 and 40.0.
+  // prompts of whole blocks 54.5, 47.5 and 44.3 us (the CTAs that own no run cost that
+  // much), chunks from inside a block 89.1, 80.5 and 85.3, single tokens 154.7, 159.3
+  // and 163.8, a prompt with 64 single tokens 54.7, 56.3 and 71.5; 2048 tokens: 17.1,
+  // 15.5 and 13.4; 40.9, 38.9 and 48.6; 29.8, 27.7 and 44.5; 17.4, 23.8 and 40.0.
   p.tpc = !many || a.slots == nullptr ? 1 : std::min(a.pool.bs, 8);
   const int round_heads = std::max(1, kIngestWarps * 1024 / (std::max(a.pool.bs, 16) * a.pool.D));
   p.hpc = tok ? a.pool.Hkv : many ? kIngestRounds * round_heads : a.T > 128 ? 4 : 1;

@@ -11,7 +11,7 @@
 //  * a 16-token sub-tile that the run covers is assembled in shared memory and
 //    leaves as 16-byte stores, although its bytes interleave tokens.
 // Bounds: the instructions that norm, rotate and quantize for prompts (16384
-// tokens x 8 heads into INT8 blocks: 46 us, 27 million warp instructions, where HBM
+// tokens x 8 heads into INT8 blocks: 47 us, 27 million warp instructions, where HBM
 // would take 15), latency for a decode step (one token per run: slot -> rows ->
 // absmax -> codes; 5.9 us for 64 tokens with their 32 query heads into INT8 groups;
 // into INT8 blocks 61 tokens take 4.4 us where no scale grows and 11 where nearly
@@ -478,9 +478,9 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
 // kernel waiting for its loads: 75 us for 16384 tokens x 8 heads.)
 // INT4, whose words pack tokens t and t + 8, and the formats whose scale spans a
 // token's heads are not built this way; they take every run through shared memory, the
-// latter loading and rotating each row twice: 16384 tokens x 8 heads of 128 in 132 us
-// and 111 to 119, where FP16 takes 36, e5m2 38, INT8 blocks 46, INT8 groups and e4m3
-// blocks 59, per-channel 72.
+// latter loading and rotating each row twice: 16384 tokens x 8 heads of 128 in 133 us
+// and 112 to 120, where FP16 takes 36, e5m2 39, INT8 blocks 47, INT8 groups and e4m3
+// blocks 60, per-channel 72.
 template <int FMT>
 constexpr bool whole_blocks() {
   return FMT != FMT_INT4_GROUP && FMT != FMT_INT8_TOKEN && FMT != FMT_FP8_TOKEN;

@@ -173,8 +173,8 @@ __host__ __device__ constexpr int rope_smem(int rotary_dim) {
 // 4c .. 4c+3.  The row's pointers and weights are set up once for all nt tokens,
 // whose loads are issued together, and the arithmetic is packed two by two:
 // after HBM it is the instructions that bound this (16384 tokens x 40 heads with
-// norms, interleaved: 52.1 us, 0.95 of the copy rate, at 116 instructions per 16 bytes of input;
-// half layout 56.0 with the whole head turned, 53.2 interleaved; with
+// norms, interleaved: 52.0 us, 0.95 of the copy rate, at 117 instructions per 16 bytes of input;
+// half layout 56.0 with the whole head turned, 54.0 interleaved; with
 // checks of rows and tokens 142 and 55.5 us, one row at a time 161 and 65 us).
 template <int D, bool BF16, bool INTER, bool full>
 __device__ __forceinline__ void rope_tokens_of(const RopeRows& A, int hA, const RopeRows& B, int hB,
