@@ -166,7 +166,8 @@ kvq_status kvq_calibrate_channel_scales(kvq_pool* pool, const kvq_half* k, const
  * otherwise that block's contents are unspecified).  The block's scale becomes
  * s = max(s_old, absmax of the call's tokens in it / 127 (448)); a token at
  * offset 0 starts the block anew, with no s_old, and offsets that the call does
- * not write are unspecified from then on.  Where s grew, the block's other codes are rounded again at the new
+ * not write are unspecified from then on.
+ * Where s grew, the block's other codes are rounded again at the new
  * scale: code' = round(code * s_old / s) in fp32.  The append owns the whole
  * block: no other work may read or write it meanwhile.
  * Device errors: a slot >= num_blocks*block_size sets OUT_OF_RANGE and the
@@ -247,9 +248,10 @@ typedef enum { KVQ_X_FP16 = 0, KVQ_X_BF16 = 1 } kvq_x_type;
  *                 overlap gives unspecified results
  * The arithmetic is fp32, rounded once to fp16 (beyond 65504, as bf16 rows may be,
  * to an infinity).  The norm's squares are summed in fp32: heads with values beyond
- * 1e18, or with eps = 0 all below 1e-19, are outside its range.  A cosine or sine is within 2^-22
- * at positions up to 2^26 either way, and within |position| * 2^-49 plus that
- * farther out (the plan's fractions come from fp64).  Errors: INVALID_ARG, UNSUPPORTED (head_dim, more than 8192
+ * 1e18, or with eps = 0 all below 1e-19, are outside its range.  A cosine or sine is
+ * within 2^-22 at positions up to 2^26 either way, and within |position| * 2^-49 plus
+ * that farther out (the plan's fractions come from fp64).
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim, more than 8192
  * heads, 2^31 tokens or more), CUDA. */
 kvq_status kvq_rope(const kvq_rope_plan* plan, kvq_x_type x_type, const void* q,
                     int64_t q_row_stride, int num_q_heads, const void* k, int64_t k_row_stride,
@@ -521,7 +523,7 @@ kvq_status kvq_selftest_decode_timeout(const kvq_pool* pool, const kvq_half* q, 
 
 /* kvq_paged_decode_ex that also writes each row's log-sum-exp:
  *   lse : fp32 [num_seqs][num_q_heads], ln sum_t exp(q . k^_t * sm_scale); -inf
- *         for a sequence with L == 0, NaN where a score is NaN
+ *         for a sequence with L == 0, NaN where a score is NaN or +inf
  * Results in `out` are those of kvq_paged_decode_ex, bit for bit. */
 kvq_status kvq_paged_decode_lse(const kvq_pool* pool, const kvq_half* q, int num_seqs,
                                 int num_q_heads, const int32_t* block_table,

@@ -92,6 +92,7 @@ class PoolHandle(ctypes.c_void_p):
     """A kvq_pool* with the shape it was allocated with: (block_size, kv_heads,
     head_dim).  The library sees addresses only; tensors are held against this."""
 
+    _shape = None
     rows = None  # (kv_heads, head_dim) of a token, as a tensor's shape would have them
 
     @property
@@ -529,8 +530,8 @@ def kvq_paged_decode_lse(pool, q, block_table, context_lens, max_context_len, sm
     S, Hq, max_blocks = _seqs(pool, q, block_table, context_lens)
     if lse.shape != (S, Hq):
         raise ValueError("lse must be [num_seqs, num_q_heads]")
-    if out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
+    if out.numel() != q.numel():
+        raise ValueError("out must have the size of q")
     dev = _device()
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib().kvq_paged_decode_lse(
@@ -726,7 +727,7 @@ def kvq_read_values(pool, slots, k_out, v_out, stream=None) -> None:
     (kvq_read_values in include/kvq.h)."""
     torch = _th()
     shape, rows, n = k_out.shape, _pool_rows(pool), slots.numel()
-    if v_out.shape != shape or len(shape) != 3 or shape[0] != n or (rows is not None and shape[1:] != rows):
+    if v_out.shape != shape or shape[0] != n or (rows is not None and k_out.numel() != n * rows[0] * rows[1]):
         raise ValueError("k_out, v_out must be [n, kv_heads, head_dim]")
     dev = _device()
     _check(lib().kvq_read_values(pool, _at(slots, torch.int64, "slots", dev), n,

@@ -34,9 +34,16 @@ def test_rope_append_rows_of_another_pool(heads, d, strided):
     _refused("2 kv heads of 128", kvq.kvq_rope_append, HANDLE, None, None, k, v, None, _ints(4, dtype=torch.int64))
 
 
-@pytest.mark.parametrize("shape", [(5, 1, D), (5, HKV, 64), (5, HKV * D), (4, HKV, D)])
+@pytest.mark.parametrize("shape", [(5, 1, D), (5, HKV, 64), (5, HKV * D - 8), (4, HKV, D)])
 def test_read_values(shape):
     _refused("k_out, v_out must be", kvq.kvq_read_values, HANDLE, _ints(5, dtype=torch.int64), _half(*shape), _half(*shape))
+
+
+def test_flattened_rows_are_as_good():
+    """[n, kv_heads * head_dim] and [num_seqs, num_q_heads * head_dim]: the same memory
+    (refused here for being a host's)."""
+    _refused("CUDA device", kvq.kvq_read_values, HANDLE, _ints(5, dtype=torch.int64), _half(5, HKV * D), _half(5, HKV * D))
+    _refused("CUDA device", kvq.kvq_paged_decode_lse, HANDLE, **_decode(out=torch.zeros((3, 4 * D))))
 
 
 def _decode(**kw):
