@@ -76,7 +76,10 @@ typedef enum {
                                   ([P312] §三: kv_cache_dtype fp8_e5m2); saturating  */
     KVQ_INT8_PER_BLOCK = 7,    /* one fp32 scale per (block, kv head, K|V): the
                                   absmax of the block's tokens over 127              */
-    KVQ_FP8_E4M3_PER_BLOCK = 8 /* the same with e4m3 codes, absmax / 448             */
+    KVQ_FP8_E4M3_PER_BLOCK = 8, /* the same with e4m3 codes, absmax / 448            */
+    KVQ_FP4_E2M1 = 10          /* 4-bit floats (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+                                  their negatives), one 8-bit scale per 16 channels of
+                                  one (token, kv head, K|V) vector: 4.5 bits a value  */
 } kvq_dtype;
 
 typedef struct kvq_pool kvq_pool; /* opaque; one per layer */
@@ -90,7 +93,8 @@ typedef struct {
     size_t scale_bytes;  /* fp32 scales of every format that has them (per-block
                             formats: 16 per page, two scales and padding)       */
     size_t header_bytes; /* device error word and padding                       */
-    size_t page_bytes;   /* bytes of one (block, kv head) page: K+V codes (+ group or block scales) */
+    size_t page_bytes;   /* bytes of one (block, kv head) page: K+V codes (+ group or block scales,
+                            or 4-bit floats' scale bytes) */
 } kvq_pool_layout;
 
 /* Byte accounting for the given geometry, without allocating.  Returns
@@ -110,7 +114,7 @@ size_t kvq_pool_bytes(int64_t num_blocks, int block_size, int kv_heads, int head
  *   num_blocks : physical blocks (>= 1)
  *   block_size : tokens per block: 8, 16, 32 or 64 ([KVC] §3.2: 8 for short
  *                contexts at high concurrency, 16 or 32 for long ones); other
- *                sizes return UNSUPPORTED.  INT4 pools take 16 or more; pools
+ *                sizes return UNSUPPORTED.  Pools of 4-bit codes take 16 or more; pools
  *                of 8-token blocks serve append, decode and block copy, while
  *                kvq_prefill and the cascade with prefix_blocks > 0 refuse
  *                them with UNSUPPORTED.
@@ -157,6 +161,12 @@ kvq_status kvq_calibrate_channel_scales(kvq_pool* pool, const kvq_half* k, const
  * itself saturating at 57344 for KVQ_FP8_E5M2,
  * e4m3 round-to-nearest-even saturating for FP8; an all-zero group stores s=0
  * and zero codes.  Per-channel uses the pool's static scales.  FP16 stores x.
+ * KVQ_FP4_E2M1: s = absmax/6 (fp32 division) rounded to nearest even in an unsigned
+ * 8-bit float of 5 exponent and 3 mantissa bits (bias 15, with subnormals: the upper
+ * bits of an fp16 without its sign), at most 10240; code = x/s (fp32 division) rounded
+ * to the nearest e2m1 value, ties to the even code, saturating at 6, the sign of a value
+ * that rounds to zero kept; NaN stores 6.  A group whose s is 0 (absmax <= 6 * 2^-18)
+ * stores zero codes.
  * Two tokens with the same slot in one call race (result unspecified; with
  * per-block formats that of the whole block).
  * Formats with one scale per block quantize a block's tokens together, so the
@@ -596,8 +606,10 @@ kvq_status kvq_read_values(const kvq_pool* pool, const int64_t* slots, int64_t n
 
 /* Read back n slots in a canonical layout (for tests and debugging).
  *   codes_out  : [n][2][kv_heads][head_dim] elements of the pool's code type
- *                (int8, e4m3 byte, or fp16; INT4 codes come back one per int8)
- *   scales_out : per-group [n][2][kv_heads][head_dim/group] fp32;
+ *                (int8, e4m3 byte, or fp16; INT4 codes come back one per int8,
+ *                e2m1 codes one per byte, its upper half zero)
+ *   scales_out : per-group [n][2][kv_heads][head_dim/group] fp32 (KVQ_FP4_E2M1:
+ *                head_dim/16, the scale's value);
  *                per-token [n][2] fp32; per-block [n][2][kv_heads] fp32 (the
  *                slot's block's scales); may be NULL (and is ignored) for
  *                FP16 and per-channel pools

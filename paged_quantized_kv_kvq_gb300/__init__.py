@@ -33,6 +33,7 @@ KVQ_INT4_PER_GROUP = 5
 KVQ_FP8_E5M2 = 6
 KVQ_INT8_PER_BLOCK = 7
 KVQ_FP8_E4M3_PER_BLOCK = 8
+KVQ_FP4_E2M1 = 10
 GROUP_FORMATS = (KVQ_INT8_PER_GROUP, KVQ_INT4_PER_GROUP)
 BLOCK_FORMATS = (KVQ_INT8_PER_BLOCK, KVQ_FP8_E4M3_PER_BLOCK)
 
@@ -885,12 +886,13 @@ class KVPool:
         n = slots.numel()
         cdt = torch.float16 if self.dtype == KVQ_FP16 else (
             torch.uint8 if self.dtype in (KVQ_FP8_E4M3_PER_TOKEN, KVQ_FP8_E5M2,
-                                          KVQ_FP8_E4M3_PER_BLOCK) else torch.int8)
+                                          KVQ_FP8_E4M3_PER_BLOCK, KVQ_FP4_E2M1) else torch.int8)
         with _on(stream):
             codes = torch.empty((n, 2, self.kv_heads, self.head_dim), dtype=cdt, device=slots.device)
             scales = None
-            if self.dtype in GROUP_FORMATS:
-                scales = torch.empty((n, 2, self.kv_heads, self.head_dim // self.group),
+            if self.dtype in GROUP_FORMATS or self.dtype == KVQ_FP4_E2M1:
+                group = self.group or 16
+                scales = torch.empty((n, 2, self.kv_heads, self.head_dim // group),
                                      dtype=torch.float32, device=slots.device)
             elif self.dtype in (KVQ_INT8_PER_TOKEN, KVQ_FP8_E4M3_PER_TOKEN):
                 scales = torch.empty((n, 2), dtype=torch.float32, device=slots.device)

@@ -43,7 +43,7 @@ namespace {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-bool valid_dtype(int d) { return d >= KVQ_FP16 && d <= KVQ_FP8_E4M3_PER_BLOCK; }
+bool valid_dtype(int d) { return (d >= KVQ_FP16 && d <= KVQ_FP8_E4M3_PER_BLOCK) || d == KVQ_FP4_E2M1; }
 
 // Geometry check + byte accounting.  Fills `view` offsets relative to base 0.
 kvq_status layout_for(int64_t num_blocks, int bs, int Hkv, int D, int dtype, int group,
@@ -54,9 +54,9 @@ kvq_status layout_for(int64_t num_blocks, int bs, int Hkv, int D, int dtype, int
   if (D % 16 != 0) return KVQ_ERR_INVALID_ARG;
   // blocks of 8 tokens (half a sub-tile per page), 16, 32 or 64 -- the sizes
   // the kernels have been run and checked at (others are refused until they
-  // have); INT4's words pack tokens t and t+8 together and take 16 or more
+  // have); words of 4-bit codes pack tokens t and t+8 together and take 16 or more
   if (bs != 8 && bs != 16 && bs != 32 && bs != 64) return KVQ_ERR_UNSUPPORTED;
-  if (bs == 8 && dtype == KVQ_INT4_PER_GROUP) return KVQ_ERR_UNSUPPORTED;
+  if (bs == 8 && kvq::fmt_4bit(dtype)) return KVQ_ERR_UNSUPPORTED;
   if (D != 64 && D != 128) return KVQ_ERR_UNSUPPORTED;
   int ng = 1;
   const bool grouped = dtype == KVQ_INT8_PER_GROUP || dtype == KVQ_INT4_PER_GROUP;
@@ -64,15 +64,19 @@ kvq_status layout_for(int64_t num_blocks, int bs, int Hkv, int D, int dtype, int
     if (group <= 0 || D % group != 0) return KVQ_ERR_INVALID_ARG;
     if (group % 16 != 0) return KVQ_ERR_UNSUPPORTED;
     ng = D / group;
+  } else if (dtype == KVQ_FP4_E2M1) {
+    group = kvq::kFp4Group;
+    ng = D / group;
   } else {
     group = 0;
   }
   const int esize = dtype == KVQ_FP16 ? 2 : 1;
-  // bytes of one 16-token sub-tile of K (or V) codes: INT4 packs two per byte
-  const int sub_bytes = dtype == KVQ_INT4_PER_GROUP ? 8 * D : 16 * D * esize;
+  // bytes of one 16-token sub-tile of K (or V) codes: 4-bit codes lie two to a byte
+  const int sub_bytes = kvq::fmt_4bit(dtype) ? 8 * D : 16 * D * esize;
   const size_t code_bytes = (size_t)bs * sub_bytes / 16;  // K (or V) codes of one page
   const size_t page_scale = grouped ? 2 * (size_t)bs * ng * 4
-                                     : kvq::fmt_block(dtype) ? kvq::kBlockScaleBytes : 0;
+                            : kvq::fmt_block(dtype) ? kvq::kBlockScaleBytes
+                            : dtype == KVQ_FP4_E2M1 ? 2 * (size_t)bs * ng : 0;
   const size_t page_bytes = 2 * code_bytes + page_scale;
   const size_t n_pages = (size_t)num_blocks * Hkv;
   size_t off = kvq::kHeaderBytes;
@@ -765,7 +769,7 @@ kvq_status kvq_read_slots(const kvq_pool* pool, const int64_t* slots, int64_t n,
   const int f = pool->view.fmt;
   const bool has_scales = f == KVQ_INT8_PER_GROUP || f == KVQ_INT4_PER_GROUP ||
                           f == KVQ_INT8_PER_TOKEN || f == KVQ_FP8_E4M3_PER_TOKEN ||
-                          kvq::fmt_block(f);
+                          f == KVQ_FP4_E2M1 || kvq::fmt_block(f);
   return from_cuda(kvq::launch_read_slots(pool->view, slots, n, codes_out,
                                           has_scales ? scales_out : nullptr, stream));
 }

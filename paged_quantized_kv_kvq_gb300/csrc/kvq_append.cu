@@ -17,6 +17,7 @@
 
 #include "kvq_common.cuh"
 #include "kvq_context.h"
+#include "kvq_fp4.cuh"
 #include "kvq_internal.h"
 #include "kvq_quant.cuh"
 
@@ -153,6 +154,19 @@ __global__ void __launch_bounds__(kAppendThreads) kvq_append_kernel(const Append
           store_nibbles(tile + o, 0xFu << sh, u[i] << sh);
         }
       }
+    } else if constexpr (FMT == FMT_FP4) {
+      // a scale for 16 channels: two lanes
+      float a = absmax8(xv);
+      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+      const uint32_t sc = fp4_scale_code(a);
+      const uint32_t codes = quant8_fp4(f, fp4_scale_value(sc));
+      if (!act) continue;
+      if ((d0 & 15) == 0) {
+        const int gi = d0 >> 4, ng = pool.ng;
+        page[2 * pool.code_bytes + kv * pool.bs * ng + sub * 16 * ng +
+             (kv == 0 ? fp4_k_scale(tt, gi, ng) : fp4_v_scale(tt, gi, ng))] = static_cast<char>(sc);
+      }
+      store_fp4x8<false>(tile, kv, tt, d0, codes);
     } else if constexpr (FMT == FMT_FP16) {
       if (!act) continue;
       const uint16_t* hb = reinterpret_cast<const uint16_t*>(&raw);
@@ -260,6 +274,13 @@ __global__ void kvq_read_slots_kernel(PoolView pool, const int64_t* slots, int64
           static_cast<int8_t>(static_cast<int>((w >> sh) & 0xFu) - static_cast<int>(kInt4Bias));
       continue;
     }
+    if (pool.fmt == FMT_FP4) {  // the 4-bit code as it is, in a byte
+      const int ln = kv == 0 ? (tt & 7) * 4 + ((d & 15) >> 2) : (d & 7) * 4 + ((tt & 7) >> 1);
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(tile + int4_word_offset(ln, d >> 4));
+      reinterpret_cast<uint8_t*>(codes_out)[dst] =
+          static_cast<uint8_t>(w >> (kv == 0 ? fp4_k_shift(tt, d) : fp4_v_shift(tt, d)) & 0xFu);
+      continue;
+    }
     const int o = kv == 0 ? k_tile_offset(tt, d, D, es) : v_code_offset(tt, d, D, es, pool.bs);
     if (es == 2)
       reinterpret_cast<uint16_t*>(codes_out)[dst] = *reinterpret_cast<const uint16_t*>(tile + o);
@@ -276,6 +297,15 @@ __global__ void kvq_read_slots_kernel(PoolView pool, const int64_t* slots, int64
       const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
       const float* sc = reinterpret_cast<const float*>(page + 2 * pool.code_bytes);
       scales_out[(i * 2 + kv) * ns + c] = sc[(kv * pool.bs + off) * pool.ng + gi];
+    }
+  } else if (pool.fmt == FMT_FP4) {
+    const int ng = pool.ng, ns = pool.Hkv * ng;
+    for (int c = threadIdx.x; c < ns; c += blockDim.x) {
+      const int h = c / ng, gi = c - h * ng;
+      const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
+      scales_out[(i * 2 + kv) * ns + c] = fp4_scale_value(static_cast<uint8_t>(
+          page[2 * pool.code_bytes + kv * pool.bs * ng + sub * 16 * ng +
+               (kv == 0 ? fp4_k_scale(tt, gi, ng) : fp4_v_scale(tt, gi, ng))]));
     }
   } else if (fmt_block(pool.fmt)) {  // the scale of the slot's block, per head
     for (int h = threadIdx.x; h < pool.Hkv; h += blockDim.x) {
@@ -368,6 +398,7 @@ cudaError_t launch_step_append(const PoolView& pool, const __half* k, const __ha
     case FMT_FP8_TOKEN: return launch_append_fmt<FMT_FP8_TOKEN>(p, grid, st, dependent);
     case FMT_INT4_GROUP: return launch_append_fmt<FMT_INT4_GROUP>(p, grid, st, dependent);
     case FMT_FP8_E5M2: return launch_append_fmt<FMT_FP8_E5M2>(p, grid, st, dependent);
+    case FMT_FP4: return launch_append_fmt<FMT_FP4>(p, grid, st, dependent);
     default: return cudaErrorInvalidValue;
   }
 }

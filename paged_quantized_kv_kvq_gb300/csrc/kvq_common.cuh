@@ -9,7 +9,8 @@
 //
 //   header      : 256 B, int32 error word at offset 0
 //   (INT8 codes are stored biased by +128, see kInt8Bias; INT4 codes as
-//    nibbles biased by +8, see the INT4 sub-tile layout below)
+//    nibbles biased by +8, see the INT4 sub-tile layout below; 4-bit floats as
+//    they are, see kvq_fp4.cuh)
 //   pages       : [num_blocks][kv_heads] pages of page_bytes each:
 //                   K codes : block_size/16 sub-tiles of 16 tokens x D
 //                             (block size 8: half a sub-tile, see below)
@@ -17,6 +18,8 @@
 //                   K scales: [block_size][D/group] fp32   (per-group only)
 //                   V scales: [block_size][D/group] fp32   (per-group only)
 //                   K scale, V scale fp32, 8 B padding     (per-block only)
+//                   K scales: [block_size][D/16] bytes     (4-bit floats only)
+//                   V scales: [block_size][D/16] bytes     (4-bit floats only)
 //   token scales: [num_blocks][2][block_size] fp32         (per-token only)
 //   chan scales : [2][kv_heads][D] fp32                    (per-channel only)
 //
@@ -46,6 +49,7 @@ enum Fmt : int {
   FMT_FP8_E5M2 = 6,
   FMT_INT8_BLOCK = 7,
   FMT_FP8_BLOCK = 8,
+  FMT_FP4 = 10,
 };
 
 enum ErrBits : int {
@@ -65,6 +69,12 @@ __host__ __device__ constexpr bool fmt_e4m3(int fmt) {
   return fmt == FMT_FP8_TOKEN || fmt == FMT_FP8_BLOCK;
 }
 constexpr int kBlockScaleBytes = 16;  // the two scales, padded so that pages stay 16-byte aligned
+
+// Formats that pack two codes in a byte.
+__host__ __device__ constexpr bool fmt_4bit(int fmt) {
+  return fmt == FMT_INT4_GROUP || fmt == FMT_FP4;
+}
+constexpr int kFp4Group = 16;  // channels per scale of the 4-bit floats
 
 __host__ __device__ constexpr int fmt_esize(int fmt) { return fmt == FMT_FP16 ? 2 : 1; }
 
@@ -141,10 +151,10 @@ struct PoolView {
   int* err;
   int64_t num_blocks;
   int bs, Hkv, D, fmt, group, ng, esize;
-  int sub_bytes;    // bytes of one 16-token sub-tile: 16 * D * esize (INT4: 8 * D)
+  int sub_bytes;    // bytes of one 16-token sub-tile: 16 * D * esize (4-bit codes: 8 * D)
   int code_bytes;   // bytes of K (or V) codes in one page = bs * sub_bytes / 16
                     // (block size 8: half a sub-tile)
-  int page_bytes;   // 2*code_bytes + (per-group) 2*bs*ng*4 or (per-block) 16
+  int page_bytes;   // 2*code_bytes + (per-group) 2*bs*ng*4, (per-block) 16 or (4-bit floats) 2*bs*ng
 };
 
 __device__ __forceinline__ void set_error(int* err, int bits) { atomicOr(err, bits); }

@@ -44,6 +44,7 @@
 
 #include "kvq_common.cuh"
 #include "kvq_context.h"
+#include "kvq_fp4.cuh"
 
 namespace kvq {
 
@@ -129,16 +130,17 @@ struct FmtTraits {
   static constexpr bool maybe_nan = FMT == FMT_FP16 || fmt_e4m3(FMT) || FMT == FMT_FP8_E5M2;
 };
 
-// 32-bit words a lane holds of one 16-token sub-tile of K (or V).
+// 32-bit words a lane holds of one 16-token sub-tile of K (or V).  (4-bit floats become
+// fp16 words as they are loaded: their scales lie beside them.)
 template <int FMT, int D>
 __host__ __device__ constexpr int lane_words() {
-  return FMT == FMT_FP16 ? D / 4 : (FMT == FMT_INT4_GROUP ? D / 16 : D / 8);
+  return FMT == FMT_FP16 || FMT == FMT_FP4 ? D / 4 : (FMT == FMT_INT4_GROUP ? D / 16 : D / 8);
 }
 
 // Word w (4 elements) of a lane's sub-tile -> (lo, hi) fp16x2 pairs.
 template <int FMT>
 __device__ __forceinline__ void word_to_h2(const uint32_t* words, int w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (FMT == FMT_FP16) {
+  if constexpr (FMT == FMT_FP16 || FMT == FMT_FP4) {
     lo = words[2 * w];
     hi = words[2 * w + 1];
   } else if constexpr (fmt_e4m3(FMT)) {
@@ -252,6 +254,7 @@ struct PairRegs {
   float ks[2][2][NS];  // [tile][row g | g+8][group]
   float vs[2][2][NS];
   const char* vtile[2];  // V codes in shared memory
+  const char* vsc[2];    // 4-bit floats: their scales
   const char* vtile_b[2];  // block size 8: V codes of the tile's second page (or null)
   int rows[2];
 };
@@ -263,7 +266,13 @@ __device__ __forceinline__ void load_tile(PairRegs<FMT, D, NG>& r, int t, const 
   using T = FmtTraits<FMT>;
   constexpr int NS = PairRegs<FMT, D, NG>::NS;
   const int g = lane >> 2;
-  load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, r.kw[t]);
+  if constexpr (FMT == FMT_FP4) {
+    const char* sc = stage + 2 * pool.code_bytes + sub * D;
+    fp4_load_k<D>(stage + sub * pool.sub_bytes, sc, lane, r.kw[t]);
+    r.vsc[t] = sc + pool.bs * (D / 16);
+  } else {
+    load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, r.kw[t]);
+  }
   r.vtile[t] = stage + pool.code_bytes + sub * pool.sub_bytes;
   if constexpr (T::block_scales) {
     const float2 sc = *reinterpret_cast<const float2*>(stage + 2 * pool.code_bytes);
@@ -539,6 +548,8 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
     for (int t = 0; t < 2; ++t) {
       if constexpr (BS8)
         load_v8<FMT, D>(r.vtile[t], r.vtile_b[t], lane, vwp[t]);
+      else if constexpr (FMT == FMT_FP4)
+        fp4_load_v<D>(r.vtile[t], r.vsc[t], lane, r.rows[t], vwp[t]);
       else
         load_lane_words<FMT, D>(r.vtile[t], lane, vwp[t]);
     }

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
   const int h = blockIdx.y;
   const int unit = threadIdx.x & 127 & (tpt - 1);  // of the tpt threads (whole warps) of its 16 slots
   const int64_t i0 = (((int64_t)blockIdx.x << (7 - tpt_log2)) + ((threadIdx.x & 127) >> tpt_log2)) * kValueSlots;
-  if (FMT != FMT_FP16 && FMT != FMT_INT4_GROUP && pool.bs >= 16 && i0 + kValueSlots <= n) {
+  if (FMT != FMT_FP16 && !fmt_4bit(FMT) && pool.bs >= 16 && i0 + kValueSlots <= n) {
     const int64_t first = slots[i0];
     const int lane = threadIdx.x & 15;
     if (__all_sync(0xffffffffu, slots[i0 + lane] == first + lane) && first >= 0 && (first & 15) == 0 &&
@@ -126,12 +126,12 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
     int lane, word;
     if (kv == 0) {
       lane = (t & 7) * 4 + 2 * (ci & 1);
-      word = (FMT == FMT_INT4_GROUP ? 0 : (t >> 3) * (D >> 4)) + (ci >> 1);
+      word = (fmt_4bit(FMT) ? 0 : (t >> 3) * (D >> 4)) + (ci >> 1);
     } else {
       lane = (t & 7) >> 1;
-      word = FMT == FMT_INT4_GROUP || pool.bs == 8 ? ci >> 1 : ci;
+      word = fmt_4bit(FMT) || pool.bs == 8 ? ci >> 1 : ci;
     }
-    constexpr int WB = FMT == FMT_FP16 ? 8 : 4;  // bytes of a word of four elements (INT4: eight)
+    constexpr int WB = FMT == FMT_FP16 ? 8 : 4;  // bytes of a word of four elements (4-bit codes: eight)
     const char* at = tile + (word / (16 / WB)) * 512 + lane * 16 + word % (16 / WB) * WB;
     uint2 w[8];  // V: one word per channel; K: one per four channels
     if (kv == 0) {
@@ -148,6 +148,10 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
     float s = 1.f;
     if constexpr (FMT == FMT_INT8_GROUP || FMT == FMT_INT4_GROUP)
       s = sc[(kv * pool.bs + off) * pool.ng + d0 / pool.group];
+    else if constexpr (FMT == FMT_FP4)
+      s = fp4_scale_value(static_cast<uint8_t>(
+          page[2 * pool.code_bytes + kv * pool.bs * pool.ng + (off >> 4) * D +
+               (kv == 0 ? fp4_k_scale(t, ci >> 1, pool.ng) : fp4_v_scale(t, ci >> 1, pool.ng))]));
     else if constexpr (fmt_block(FMT))
       s = sc[kv];
     else if constexpr (FMT == FMT_INT8_TOKEN || FMT == FMT_FP8_TOKEN)
@@ -160,7 +164,10 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
     for (int e = 0; e < 8; ++e) {
       const uint2 q = kv == 0 ? w[e >> 2] : w[e];
       const int el = kv == 0 ? e & 3 : ev;
-      if constexpr (FMT == FMT_INT4_GROUP) {
+      if constexpr (FMT == FMT_FP4) {
+        const int sh = kv == 0 ? fp4_k_shift(t, el) : fp4_v_shift(t, d0);
+        x[e] = fp4_code_value(q.x >> sh & 0xFu) * s;
+      } else if constexpr (FMT == FMT_INT4_GROUP) {
         const int sh = kv == 0 ? nib_shift((t >> 3) * 4 + el) : nib_shift(el + 4 * (ci & 1));
         x[e] = static_cast<float>(static_cast<int>(q.x >> sh & 0xFu) - static_cast<int>(kInt4Bias)) * s;
       } else if constexpr (FMT == FMT_FP16) {
@@ -203,6 +210,7 @@ cudaError_t launch_read_values(const PoolView& pool, const int64_t* slots, int64
     case FMT_FP8_E5M2: run(kvq_read_values_kernel<FMT_FP8_E5M2>); break;
     case FMT_INT8_BLOCK: run(kvq_read_values_kernel<FMT_INT8_BLOCK>); break;
     case FMT_FP8_BLOCK: run(kvq_read_values_kernel<FMT_FP8_BLOCK>); break;
+    case FMT_FP4: run(kvq_read_values_kernel<FMT_FP4>); break;
     default: return cudaErrorInvalidValue;
   }
   return phase_mark(st, cudaGetLastError());
@@ -277,7 +285,8 @@ cudaError_t launch_ingest(const IngestArgs& a, cudaStream_t st, bool dependent) 
     case FMT_INT8_BLOCK:
     case FMT_FP8_BLOCK: e = launch_ingest_block(l); break;
     case FMT_INT8_GROUP:
-    case FMT_INT4_GROUP: e = launch_ingest_group(l); break;
+    case FMT_INT4_GROUP:
+    case FMT_FP4: e = launch_ingest_group(l); break;
     case FMT_INT8_TOKEN:
     case FMT_FP8_TOKEN: e = launch_ingest_token(l); break;
     default: e = launch_ingest_misc(l);

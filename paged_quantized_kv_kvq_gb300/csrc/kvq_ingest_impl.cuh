@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "kvq_context.h"
+#include "kvq_fp4.cuh"
 #include "kvq_internal.h"
 #include "kvq_quant.cuh"
 #include "kvq_rope_math.cuh"
@@ -98,6 +99,15 @@ __device__ __forceinline__ void store_codes8(char* base, int kv, int off, int d0
     for (int i = 0; i < 8; ++i)
       tile[v_code_offset(tt, d0 + i, D, 1, bs)] = static_cast<char>(c[i]);
   }
+}
+
+// The scale byte of channels 16gi .. +15 of token offset `off` (4-bit floats).
+template <int D>
+__device__ __forceinline__ void store_fp4_scale(char* page, int kv, int off, int gi, const PoolView& pool,
+                                                uint32_t code) {
+  constexpr int NG = D / 16;
+  page[2 * pool.code_bytes + kv * pool.bs * NG + (off >> 4) * D +
+       (kv == 0 ? fp4_k_scale(off & 15, gi, NG) : fp4_v_scale(off & 15, gi, NG))] = static_cast<char>(code);
 }
 
 template <int FMT>
@@ -244,6 +254,11 @@ __device__ __forceinline__ void ingest_token(const IngestParams& p, IngestShared
       s = __fdiv_rn(absmax(pool.group >> 3), kTop);
       if (act && d0 % pool.group == 0) scales[(kv * bs + off) * pool.ng + d0 / pool.group] = s;
     }
+    uint32_t sc4 = 0;
+    if constexpr (FMT == FMT_FP4) {
+      sc4 = fp4_scale_code(absmax(2));
+      if (act && (d0 & 15) == 0) store_fp4_scale<D>(page, kv, off, d0 >> 4, pool, sc4);
+    }
     if (!act) continue;
     if constexpr (FMT == FMT_FP16) {
       const uint4 o = narrow8(x);
@@ -256,6 +271,8 @@ __device__ __forceinline__ void ingest_token(const IngestParams& p, IngestShared
         for (int i = 0; i < 8; ++i)
           *reinterpret_cast<uint16_t*>(tile + v_code_offset(tt, d0 + i, D, 2, bs)) = half[i];
       }
+    } else if constexpr (FMT == FMT_FP4) {
+      store_fp4x8<false>(tile, kv, tt, d0, quant8_fp4(x, fp4_scale_value(sc4)));
     } else if constexpr (FMT == FMT_INT4_GROUP) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -388,7 +405,7 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
         reinterpret_cast<uint32_t*>(tile)[i] = v;
       }
       if (tid == 0) scales[kv] = s_block;
-    } else if constexpr (FMT == FMT_INT4_GROUP) {
+    } else if constexpr (fmt_4bit(FMT)) {
       __syncthreads();
       for (int i = tid; i < pool.code_bytes / 4; i += kIngestThreads)
         reinterpret_cast<uint32_t*>(tile)[i] = 0;
@@ -417,7 +434,13 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
         continue;
       }
       float s = 0.f;
-      if constexpr (FMT == FMT_INT8_GROUP || FMT == FMT_INT4_GROUP) {
+      if constexpr (FMT == FMT_FP4) {
+        float a = absmax(x[c]);
+        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+        const uint32_t sc4 = fp4_scale_code(a);
+        s = fp4_scale_value(sc4);
+        if (act && (d0 & 15) == 0) store_fp4_scale<D>(page, kv, off[c], d0 >> 4, pool, sc4);
+      } else if constexpr (FMT == FMT_INT8_GROUP || FMT == FMT_INT4_GROUP) {
         // a group is group/8 consecutive lanes
         float a = absmax(x[c]);
         for (int o = pool.group >> 4; o > 0; o >>= 1)
@@ -431,7 +454,14 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
         s = s_block;
       }
       if (!act) continue;
-      if constexpr (FMT == FMT_INT4_GROUP) {
+      if constexpr (FMT == FMT_FP4) {
+        char* t = dst + (off[c] >> 4) * pool.sub_bytes;
+        const uint32_t q = quant8_fp4(x[c], s);
+        if (staged)
+          store_fp4x8<true>(t, kv, off[c] & 15, d0, q);
+        else
+          store_fp4x8<false>(t, kv, off[c] & 15, d0, q);
+      } else if constexpr (FMT == FMT_INT4_GROUP) {
         char* t = dst + (off[c] >> 4) * pool.sub_bytes;
         const int tt = off[c] & 15;
 #pragma unroll
@@ -476,14 +506,14 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
 // memory.  A warp's unit is 8 such tokens of one head of 128 channels (16 of one of
 // 64): 32 values a lane.  (Whole sub-tiles, 64 values, left an SM 16 warps and the
 // kernel waiting for its loads: 75 us for 16384 tokens x 8 heads.)
-// INT4, whose words pack tokens t and t + 8, and the formats whose scale spans a
+// 4-bit codes, whose words pack tokens t and t + 8, and the formats whose scale spans a
 // token's heads are not built this way; they take every run through shared memory, the
 // latter loading and rotating each row twice: 16384 tokens x 8 heads of 128 in 133 us
 // and 112 to 120, where FP16 takes 36, e5m2 39, INT8 blocks 47, INT8 groups and e4m3
 // blocks 60, per-channel 72.
 template <int FMT>
 constexpr bool whole_blocks() {
-  return FMT != FMT_INT4_GROUP && FMT != FMT_INT8_TOKEN && FMT != FMT_FP8_TOKEN;
+  return !fmt_4bit(FMT) && FMT != FMT_INT8_TOKEN && FMT != FMT_FP8_TOKEN;
 }
 
 template <int FMT, int D>

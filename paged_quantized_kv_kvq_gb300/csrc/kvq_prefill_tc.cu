@@ -65,6 +65,7 @@ cudaError_t launch_prefill_tc(const PoolView& pool, const __half* q, int S, int 
     case FMT_FP8_E5M2: return run_tc_d<FMT_FP8_E5M2, 2>(l);
     case FMT_INT8_BLOCK: return run_tc_d<FMT_INT8_BLOCK, 2>(l);
     case FMT_FP8_BLOCK: return run_tc_d<FMT_FP8_BLOCK, 2>(l);
+    case FMT_FP4: return run_tc_d<FMT_FP4, 2>(l);
   }
   return cudaErrorInvalidValue;
 }
@@ -152,6 +153,7 @@ cudaError_t launch_prefill_ws(const PoolView& pool, const __half* q, int S, int 
     case FMT_FP8_E5M2: return run_ws_d<FMT_FP8_E5M2>(sp, ap, ntiles, st);
     case FMT_INT8_BLOCK: return run_ws_d<FMT_INT8_BLOCK>(sp, ap, ntiles, st);
     case FMT_FP8_BLOCK: return run_ws_d<FMT_FP8_BLOCK>(sp, ap, ntiles, st);
+    case FMT_FP4: return run_ws_d<FMT_FP4>(sp, ap, ntiles, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -93,15 +93,44 @@ __device__ __forceinline__ void tc_word_to_h2(uint32_t w, uint32_t& lo, uint32_t
 
 // Convert one 16-byte chunk (lane L, chunk c) of a K or V code sub-tile into
 // the fp16 tiles.  `s` is the sub-tile's slot in the step (tokens 16s..16s+15
-// of the tile); V tokens at or past `nv` are written as zero.
+// of the tile); V tokens at or past `nv` are written as zero.  `sc`: the chunk's
+// scales (4-bit floats, tc_chunk_scales).
 template <int FMT, int D>
 __device__ __forceinline__ void tc_convert_chunk(uint4 raw, int L, int c, bool isv, int s, int nv,
-                                                 char* kh, char* vt) {
+                                                 char* kh, char* vt, uint4 sc = uint4{}) {
   const int g = L >> 2, j = L & 3;
   const uint32_t wv[4] = {raw.x, raw.y, raw.z, raw.w};
   const uint32_t m0 = (2 * j < nv ? 0xFFFFu : 0u) | (2 * j + 1 < nv ? 0xFFFF0000u : 0u);
   const uint32_t m1 = (2 * j + 8 < nv ? 0xFFFFu : 0u) | (2 * j + 9 < nv ? 0xFFFF0000u : 0u);
-  if constexpr (FMT == FMT_INT4_GROUP) {
+  if constexpr (FMT == FMT_FP4) {
+    const uint32_t sw[4] = {sc.x, sc.y, sc.z, sc.w};
+    __half2 s0[2], s1[2];  // K: scales of tokens g and g+8 for the chunk's four steps
+    fp4_scales(sc.x, s0[0], s0[1]);
+    fp4_scales(sc.y, s1[0], s1[1]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int w = 4 * c + i;  // 16-channel step
+      uint32_t a[4];
+      if (!isv) {  // tokens g, g+8; channels 16w + 4j .. +3
+        const __half2 x = s0[i & 1], y = s1[i & 1];
+        fp4_k_frag(wv[i], i & 2 ? __high2half2(x) : __low2half2(x),
+                   i & 2 ? __high2half2(y) : __low2half2(y), a);
+        *reinterpret_cast<uint2*>(kh + sw128_offset(16 * s + g, 16 * w + 4 * j, kTcStep)) =
+            make_uint2(a[0], a[2]);
+        *reinterpret_cast<uint2*>(kh + sw128_offset(16 * s + g + 8, 16 * w + 4 * j, kTcStep)) =
+            make_uint2(a[1], a[3]);
+      } else {  // channels 16w + g, +8; tokens 2j, 2j+1 | 2j+8, 2j+9
+        __half2 lo, hi;
+        fp4_scales(sw[i], lo, hi);
+        fp4_v_frag(wv[i], lo, hi, a);
+        const int d0 = 16 * w + g;
+        *reinterpret_cast<uint32_t*>(vt + sw128_offset(d0, 16 * s + 2 * j, D)) = a[0] & m0;
+        *reinterpret_cast<uint32_t*>(vt + sw128_offset(d0, 16 * s + 2 * j + 8, D)) = a[2] & m1;
+        *reinterpret_cast<uint32_t*>(vt + sw128_offset(d0 + 8, 16 * s + 2 * j, D)) = a[1] & m0;
+        *reinterpret_cast<uint32_t*>(vt + sw128_offset(d0 + 8, 16 * s + 2 * j + 8, D)) = a[3] & m1;
+      }
+    }
+  } else if constexpr (FMT == FMT_INT4_GROUP) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int w = 4 * c + i;  // 16-channel step
@@ -151,6 +180,16 @@ __device__ __forceinline__ void tc_convert_chunk(uint4 raw, int L, int c, bool i
       }
     }
   }
+}
+
+// 4-bit floats: the scales of chunk c of lane L of a K (V) sub-tile, whose sub-tile's
+// scales are at `sc` (K: tokens g and g + 8 in x and y; V: a word per 16-channel step).
+template <int D>
+__device__ __forceinline__ uint4 tc_chunk_scales(const char* sc, int L, int c, bool isv) {
+  constexpr int NG = D / 16;
+  if (isv) return *reinterpret_cast<const uint4*>(sc + (L & 3) * 4 * NG + 16 * c);
+  const char* k = sc + (L >> 2) * 2 * NG + 4 * c;
+  return make_uint4(*reinterpret_cast<const uint32_t*>(k), *reinterpret_cast<const uint32_t*>(k + NG), 0, 0);
 }
 
 // Bounded wait that gives up early once another role has set *abort; a wait
@@ -228,7 +267,7 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
   constexpr bool CH = T::channel;
   using PL = TcPlan<D, NT, CH>;
   constexpr int ES = FMT == FMT_FP16 ? 2 : 1;
-  constexpr int SUB_BYTES = FMT == FMT_INT4_GROUP ? 8 * D : 16 * D * ES;
+  constexpr int SUB_BYTES = fmt_4bit(FMT) ? 8 * D : 16 * D * ES;
   constexpr int CPS = SUB_BYTES / 16;                 // 16-byte chunks per K (or V) sub-tile
   constexpr int NCH = (CPS + kTcConv - 1) / kTcConv;  // chunks per converter thread and sub-tile
   const float kNegInf = __int_as_float(0xff800000u);
@@ -368,6 +407,7 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
     const int npg = kTcStep / bs;
     // raw codes of one step: [sub-tile][K|V][chunk] for this thread's chunks
     uint4 rv[4][2][NCH];
+    uint4 rs[FMT == FMT_FP4 ? 4 : 1][2][NCH];  // and their scales (4-bit floats)
     float sk = 0.f, sv = 0.f;  // this thread's token scales (cid < 64)
     bool tok_ok = false;       // and whether that token is present
     int tphys[4];              // block ids of the step being loaded
@@ -399,6 +439,12 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
                                ? *reinterpret_cast<const uint4*>(base + (kv ? pool.code_bytes : 0) +
                                                                  (ch >> 5) * 512 + (ch & 31) * 16)
                                : make_uint4(0, 0, 0, 0);
+            if constexpr (FMT == FMT_FP4)
+              rs[s][kv][i] = (ok && ch < CPS)
+                                 ? tc_chunk_scales<D>(page_of(ph[pg]) + 2 * pool.code_bytes +
+                                                          kv * bs * (D / 16) + sub * D,
+                                                      ch & 31, ch >> 5, kv == 1)
+                                 : make_uint4(0, 0, 0, 0);
           }
       }
       if (cid < kTcStep) {
@@ -445,7 +491,8 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
           for (int i = 0; i < NCH; ++i) {
             const int ch = cid + i * kTcConv;
             if (ch < CPS) tc_convert_chunk<FMT, D>(rv[s][kv][i], ch & 31, ch >> 5, kv == 1, s,
-                                                   nvalid, khb, vtb);
+                                                   nvalid, khb, vtb,
+                                                   rs[FMT == FMT_FP4 ? s : 0][kv][i]);
           }
       }
       if (cid < kTcStep) {

@@ -82,7 +82,7 @@ template <int FMT, int D>
 __global__ void __launch_bounds__(128) kvq_prefill_stage_kernel(const StageParams p) {
   using T = FmtTraits<FMT>;
   using R = StepRec<D>;
-  constexpr int SUB_BYTES = FMT == FMT_INT4_GROUP ? 8 * D : 16 * D * (FMT == FMT_FP16 ? 2 : 1);
+  constexpr int SUB_BYTES = fmt_4bit(FMT) ? 8 * D : 16 * D * (FMT == FMT_FP16 ? 2 : 1);
   constexpr int CPS = SUB_BYTES / 16;
   const PoolView& pool = p.pool;
   const int bs = pool.bs;
@@ -110,11 +110,14 @@ __global__ void __launch_bounds__(128) kvq_prefill_stage_kernel(const StageParam
     int off;
     const char* page = page_of(t0 + 16 * s4, off);
     const int nvalid = page ? min(max(ctx - (t0 + 16 * s4), 0), 16) : 0;
-    uint4 rv = make_uint4(0, 0, 0, 0);
+    uint4 rv = make_uint4(0, 0, 0, 0), rs = make_uint4(0, 0, 0, 0);
+    if (FMT == FMT_FP4 && nvalid > 0)
+      rs = tc_chunk_scales<D>(page + 2 * pool.code_bytes + (isv ? bs * (D / 16) : 0) + (off >> 4) * D,
+                              ch & 31, ch >> 5, isv);
     if (nvalid > 0)
       rv = *reinterpret_cast<const uint4*>(page + (isv ? pool.code_bytes : 0) + (off >> 4) * SUB_BYTES +
                                            (ch >> 5) * 512 + (ch & 31) * 16);
-    tc_convert_chunk<FMT, D>(rv, ch & 31, ch >> 5, isv, s4, nvalid, rec + R::kh, rec + R::vt);
+    tc_convert_chunk<FMT, D>(rv, ch & 31, ch >> 5, isv, s4, nvalid, rec + R::kh, rec + R::vt, rs);
   }
   // per-token scales, the valid-token mask, the largest V scale
   if (tid < kTcStep) {

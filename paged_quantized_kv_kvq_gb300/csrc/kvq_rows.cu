@@ -97,6 +97,7 @@ cudaError_t launch_rows(const RowsArgs& a, const RowsPlan& plan, cudaStream_t st
     case FMT_FP8_E5M2: return run_rows_d<FMT_FP8_E5M2>(l);
     case FMT_INT8_BLOCK: return run_rows_d<FMT_INT8_BLOCK>(l);
     case FMT_FP8_BLOCK: return run_rows_d<FMT_FP8_BLOCK>(l);
+    case FMT_FP4: return run_rows_d<FMT_FP4>(l);
   }
   return cudaErrorInvalidValue;
 }

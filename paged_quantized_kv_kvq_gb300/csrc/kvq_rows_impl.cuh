@@ -265,7 +265,10 @@ __global__ void __launch_bounds__(kRowsThreads) kvq_rows_kernel(const RowsParams
       float z[2][4];
       {
         uint32_t kw[NU32];
-        load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, kw);
+        if constexpr (FMT == FMT_FP4)
+          fp4_load_k<D>(stage + sub * pool.sub_bytes, stage + 2 * pool.code_bytes + sub * D, lane, kw);
+        else
+          load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, kw);
         constexpr int SUB = KPG >= 2 ? 2 : 1;  // independent accumulators per group
         float acc[2][NG * SUB][4];
 #pragma unroll
@@ -373,7 +376,11 @@ __global__ void __launch_bounds__(kRowsThreads) kvq_rows_kernel(const RowsParams
       // ---- P.V: lane word w of the V sub-tile is the B fragment of channels 8w..8w+7
       {
         uint32_t vw[NU32];
-        load_lane_words<FMT, D>(stage + pool.code_bytes + sub * pool.sub_bytes, lane, vw);
+        if constexpr (FMT == FMT_FP4)
+          fp4_load_v<D>(stage + pool.code_bytes + sub * pool.sub_bytes,
+                        stage + 2 * pool.code_bytes + bs * (D / 16) + sub * D, lane, nvalid, vw);
+        else
+          load_lane_words<FMT, D>(stage + pool.code_bytes + sub * pool.sub_bytes, lane, vw);
         if constexpr (T::maybe_nan) {
           if (nvalid < 16) {
             // zero the V of tokens that no row of this warp attends (they may

@@ -38,6 +38,7 @@ cudaError_t launch_weights(const WeightsArgs& a, cudaStream_t st) {
     case FMT_FP8_E5M2: return run_weights_d<FMT_FP8_E5M2>(l);
     case FMT_INT8_BLOCK: return run_weights_d<FMT_INT8_BLOCK>(l);
     case FMT_FP8_BLOCK: return run_weights_d<FMT_FP8_BLOCK>(l);
+    case FMT_FP4: return run_weights_d<FMT_FP4>(l);
   }
   return cudaErrorInvalidValue;
 }

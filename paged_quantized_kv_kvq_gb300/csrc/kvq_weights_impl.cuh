@@ -46,7 +46,7 @@ struct WeightsParams {
   float* scores;
   int64_t stride;
   float decay;
-  int scale_bytes;  // K scales of a page copied behind its codes (per token, per group)
+  int scale_bytes;  // K scales of a page copied behind its codes (per token, per group, 4-bit floats)
   int slot_bytes;   // room of a page in a stage
   int nstage;
 };
@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(kWeightsWarps * 32, kWeightsCtas)
   constexpr int NU32 = lane_words<FMT, D>(), NC = NU32 / 4;  // 32-bit words, 16-byte chunks per lane
   constexpr int NS = T::group_scales ? NG : 1;
   constexpr bool kCopied = T::group_scales || T::token_scales;  // scales come with the codes
+  constexpr bool kFp4 = FMT == FMT_FP4;                         // (so do these, in bytes)
   const float kInf = __int_as_float(0x7f800000u);
   extern __shared__ __align__(128) char smem[];
   const PoolView& pool = p.d.pool;
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kWeightsWarps * 32, kWeightsCtas)
         bulk_g2s(dst, page, pool.code_bytes, &bars[st]);
         if constexpr (T::token_scales)
           bulk_g2s(dst + pool.code_bytes, pool.tok_scales + (int64_t)now.entry * 2 * bs, p.scale_bytes, &bars[st]);
-        else if constexpr (T::group_scales)
+        else if constexpr (T::group_scales || kFp4)
           bulk_g2s(dst + pool.code_bytes, page + 2 * pool.code_bytes, p.scale_bytes, &bars[st]);
       }
     }
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kWeightsWarps * 32, kWeightsCtas)
     const int k = 16 * x >> bl, sub = (16 * x & (bs - 1)) >> 4;
     lo_at[x] = k * p.slot_bytes + sub * pool.sub_bytes + lane * 16;
     hi_at[x] = bs == 8 ? lo_at[x] + p.slot_bytes - NC / 2 * 512 : lo_at[x];
-    lo_sc[x] = k * p.slot_bytes + pool.code_bytes + (16 * sub + g) * NS * 4;
+    lo_sc[x] = k * p.slot_bytes + pool.code_bytes + (kFp4 ? sub * D : (16 * sub + g) * NS * 4);
     hi_sc[x] = lo_sc[x] + (bs == 8 ? p.slot_bytes : 8 * NS * 4);
   }
   int st = 0;
@@ -292,8 +293,10 @@ __global__ void __launch_bounds__(kWeightsWarps * 32, kWeightsCtas)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int more = (o >> 4) * pool.sub_bytes;  // (blocks of 64 tokens: the second pair)
+        if constexpr (kFp4)
+          fp4_load_k<D>(stage + lo_at[x] - lane * 16 + more, stage + lo_sc[x] + o * (D / 16), lane, kw[x]);
 #pragma unroll
-        for (int q = 0; q < NC; ++q) {
+        for (int q = 0; q < (kFp4 ? 0 : NC); ++q) {
           // chunks of the first half hold tokens 0..7, of the second 8..15 (INT4
           // words hold both; 8-token pages a half each)
           const bool second = FMT != FMT_INT4_GROUP && q >= NC / 2;
@@ -396,7 +399,8 @@ cudaError_t run_weights(const WeightsLaunch& l) {
   WeightsParams p = l.p;
   const PoolView& pool = p.d.pool;
   using T = FmtTraits<FMT>;
-  p.scale_bytes = T::group_scales ? pool.bs * NG * 4 : T::token_scales ? pool.bs * 4 : 0;
+  p.scale_bytes = T::group_scales ? pool.bs * NG * 4 : T::token_scales ? pool.bs * 4
+                  : FMT == FMT_FP4 ? pool.bs * (D / 16) : 0;
   p.slot_bytes = (pool.code_bytes + p.scale_bytes + 127) / 128 * 128;
   // stages: what kWeightsCtas CTAs leave each of their warps of an SM's 228 KB
   const int span = pool.bs < 32 ? 32 : pool.bs;
