@@ -597,6 +597,114 @@ kvq_status kvq_evict_blocks(const kvq_pool* pool, const float* scores, int64_t s
                             int32_t* lens_out, int32_t* kept, float* scores_out,
                             int64_t out_stride, cudaStream_t stream);
 
+/* ---- Differential attention: two softmax maps over one set of values, one taken from
+ * the other with a learned weight.  The pages do not describe it; it reads the same
+ * pools.  A kv head's keys are two keys of head_dim/2 channels side by side, its values
+ * head_dim channels; a query head is two queries side by side:
+ *   y   = softmax(q1 . k1 * sm_scale) v - lambda softmax(q2 . k2 * sm_scale) v
+ *   out = fp16(out_scale * y / sqrt(mean(y^2) + eps) * norm_weight)
+ * with q1, k1 the first head_dim/2 channels of q and k, q2, k2 the others.  (kvq_rope
+ * takes such rows as [T][2 heads][head_dim/2] where head_dim is 128.)
+ * The arithmetic is that of kvq_paged_decode (kvq_prefill_ex), the difference and the
+ * norm in fp32, rounded once to fp16 (beyond 65504 to an infinity). */
+
+/* Scratch bytes of kvq_diff_decode for these sizes.  Host only. */
+size_t kvq_diff_decode_workspace_bytes(const kvq_pool* pool, int num_seqs, int num_heads,
+                                       int max_context_len);
+
+/* Single tokens.
+ *   q           : fp16 [num_seqs][num_heads][head_dim]; num_heads is a multiple of
+ *                 kv_heads; head h reads kv head h / (num_heads/kv_heads)
+ *   sm_scale    : of both maps (usually 1/sqrt(head_dim/2))
+ *   lambda      : fp32 [num_heads]
+ *   norm_weight : fp32 [head_dim], or NULL: no norm, out = fp16(out_scale * y)
+ *   eps         : >= 0 (a row of zeros stays zero with 0, too)
+ *   out_scale   : finite (the part of a normed head that its initial lambda leaves)
+ *   out         : fp16 [num_seqs][num_heads][head_dim]; zeros for a sequence of length 0
+ * The other arguments, the workspace's alignment and the errors are those of
+ * kvq_paged_decode. */
+kvq_status kvq_diff_decode(const kvq_pool* pool, const kvq_half* q, int num_seqs, int num_heads,
+                           const int32_t* block_table, int max_blocks_per_seq,
+                           const int32_t* context_lens, int max_context_len, float sm_scale,
+                           const float* lambda, const float* norm_weight, float eps,
+                           float out_scale, kvq_half* out, void* workspace, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/* Scratch bytes of kvq_diff_prefill for these sizes (0 for refused ones).  Host only. */
+size_t kvq_diff_prefill_workspace_bytes(const kvq_pool* pool, int num_seqs, int64_t num_tokens,
+                                        int num_heads, int max_context_len);
+
+/* Prompts and chunks of them.
+ *   q, out     : fp16 [num_tokens][num_heads][head_dim]; rows from q_start[num_seqs] on
+ *                are not read, and left as they were
+ *   num_tokens : rows of q and out, >= q_start[num_seqs]
+ *   workspace  : >= kvq_diff_prefill_workspace_bytes(..) bytes, 256-byte aligned
+ * lambda, norm_weight, eps and out_scale are those of kvq_diff_decode, the other
+ * arguments and the errors those of kvq_prefill_ex; WORKSPACE when the workspace is
+ * missing or too small, UNSUPPORTED for pools of 8-token blocks. */
+kvq_status kvq_diff_prefill(const kvq_pool* pool, const kvq_half* q, int64_t num_tokens, int num_seqs,
+                            int num_heads, const int32_t* q_start, int max_q_len,
+                            const int32_t* block_table, int max_blocks_per_seq,
+                            const int32_t* context_lens, int max_context_len, float sm_scale,
+                            const float* lambda, const float* norm_weight, float eps,
+                            float out_scale, kvq_half* out, void* workspace, size_t ws_bytes,
+                            cudaStream_t stream);
+
+/* ---- A step's bookkeeping on the device: block tables, slot map and positions from the
+ * requests' lengths ([KVC] §2.2: blocks are allocated as a sequence grows).  Free blocks
+ * are a list of ids and a count, both in device memory and the caller's; the blocks at
+ * its end are taken first.  One block table serves the pools of all layers. */
+
+/* Blocks for the step's new tokens, and where those go.
+ *   pool         : only its block size, number of blocks and error word are used
+ *   new_tokens   : int32 [num_seqs] tokens that each sequence gets in this step
+ *   block_table  : int32 [num_seqs][max_blocks_per_seq]; entries of new blocks are
+ *                  written, the others stay
+ *   context_lens : int32 [num_seqs] tokens cached so far
+ *   free_list    : int32 [free_capacity]; entry free_count - 1 - k goes to the k-th new
+ *                  block, sequence by sequence; the list itself is not changed
+ *   free_count   : int32 [1], 0 .. free_capacity
+ *   lens_out     : int32 [num_seqs] lengths with the new tokens; may be context_lens
+ *   count_out    : int32 [1] free blocks left; may be free_count
+ *   q_start      : int32 [num_seqs + 1]: sequence s's new tokens are rows q_start[s] ..
+ *                  q_start[s+1]-1 (as kvq_prefill takes them)
+ *   slot_mapping : int64 [max_tokens]: the slot of each row (as kvq_append takes them)
+ *   positions    : int64 [max_tokens]: its position (as kvq_rope takes them)
+ *   max_tokens   : rows of the last two; those behind the last sequence get slot -1 and
+ *                  position 0 (the padding of a captured step)
+ * A sequence is served whole or not at all.  Not served are: one with a negative length
+ * or count; one whose tokens do not fit its table row, or whose rows pass max_tokens;
+ * and those from which on the sum of new blocks over the sequences so far (each counted
+ * that fits its row) is more than free_count, but for sequences that need none.  Such a
+ * sequence keeps its length, its row of the table and its rows q_start[s] .. (as far as
+ * max_tokens goes), whose slots are -1, and OUT_OF_RANGE is set, as it is for a count
+ * outside the list (clamped) and for an id outside the pool (which the table gets, and
+ * whose tokens get slot -1).  UNSUPPORTED beyond 16384 sequences and from 2^31 - 1 rows or
+ * free entries on. */
+kvq_status kvq_extend_tables(const kvq_pool* pool, const int32_t* new_tokens, int num_seqs,
+                             int32_t* block_table, int max_blocks_per_seq,
+                             const int32_t* context_lens, const int32_t* free_list,
+                             int free_capacity, const int32_t* free_count, int32_t* lens_out,
+                             int32_t* count_out, int32_t* q_start, int64_t* slot_mapping,
+                             int64_t* positions, int max_tokens, cudaStream_t stream);
+
+/* Blocks that sequences no longer need go to the end of the free list, sequence by
+ * sequence and in the order of its row: those of old_lens[s] tokens but for those of
+ * new_lens[s] (0: the sequence has ended; kvq_evict_blocks leaves the evicted blocks
+ * behind the kept ones, so its context_lens and lens_out are an old and a new length).
+ *   shared_blocks : the first blocks of every row that other sequences hold too; they
+ *                   are not given back
+ *   count_out     : int32 [1]; may be free_count
+ * A block must not be given back twice, nor while another sequence holds it.  Neither the
+ * table nor lengths are changed.  Device errors: a negative length (taken as 0), one
+ * beyond the row (clamped), a count outside the list (clamped), an id outside the pool
+ * (not given back) and a full list (blocks beyond it are not given back) set
+ * OUT_OF_RANGE.  UNSUPPORTED beyond 16384 sequences and from 2^31 - 1 table entries on. */
+kvq_status kvq_release_blocks(const kvq_pool* pool, const int32_t* block_table, int max_blocks_per_seq,
+                              const int32_t* old_lens, const int32_t* new_lens, int num_seqs,
+                              int shared_blocks, int32_t* free_list, int free_capacity,
+                              const int32_t* free_count, int32_t* count_out, cudaStream_t stream);
+
 /* The cached K and V of n slots as fp16 values, code * scale in fp32 rounded
  * once: k_out, v_out [n][kv_heads][head_dim], 16-byte aligned.  A negative slot
  * leaves its rows as they were; a slot outside the pool does too and sets

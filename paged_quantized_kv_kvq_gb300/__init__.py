@@ -165,6 +165,13 @@ def _declare(L):
         "kvq_paged_decode_lse": (i32, [P, P, i32, i32, P, i32, P, i32, f32, P, P, P, sz, i32, P]),
         "kvq_attention_weights": (i32, [P, P, i32, i32, P, i32, P, i32, f32, P, f32, P, P, i64, P]),
         "kvq_evict_blocks": (i32, [P, P, i64, i32, P, i32, P, i32, i32, i32, i32, P, P, P, P, i64, P]),
+        "kvq_diff_decode_workspace_bytes": (sz, [P, i32, i32, i32]),
+        "kvq_diff_decode": (i32, [P, P, i32, i32, P, i32, P, i32, f32, P, P, f32, f32, P, P, sz, P]),
+        "kvq_diff_prefill_workspace_bytes": (sz, [P, i32, i64, i32, i32]),
+        "kvq_diff_prefill": (i32, [P, P, i64, i32, i32, P, i32, P, i32, P, i32, f32, P, P, f32, f32, P, P,
+                                   sz, P]),
+        "kvq_extend_tables": (i32, [P, P, i32, P, i32, P, P, i32, P, P, P, P, P, P, i32, P]),
+        "kvq_release_blocks": (i32, [P, P, i32, P, P, i32, i32, P, i32, P, P, P]),
         "kvq_read_values": (i32, [P, P, i64, P, P, P]),
         "kvq_read_slots": (i32, [P, P, i64, P, P, P]),
         "kvq_get_error": (i32, [P, P]),
@@ -593,6 +600,118 @@ def kvq_evict_blocks(pool, scores, block_table, context_lens, max_context_len, b
         0 if scores_out is None else scores_out.shape[2], _stream(stream)), "kvq_evict_blocks")
 
 
+def _diff(q, lam, out, norm_weight, dev):
+    """Pointers of lambda, the norm's weight and out, held against q [rows, heads, head_dim]."""
+    torch = _th()
+    _, H, D = q.shape
+    if lam.numel() != H:
+        raise ValueError("lam must be [num_heads]")
+    if out.numel() != q.numel():
+        raise ValueError("out must have the size of q")
+    if norm_weight is not None and norm_weight.numel() != D:
+        raise ValueError("norm_weight must be [head_dim]")
+    return (_at(lam, torch.float32, "lam", dev), _weight(norm_weight, D, "norm_weight", dev),
+            _at(out, torch.float16, "out", dev))
+
+
+def kvq_diff_decode_workspace_bytes(pool, num_seqs, num_heads, max_context_len) -> int:
+    return int(lib().kvq_diff_decode_workspace_bytes(pool, num_seqs, num_heads, max_context_len))
+
+
+def kvq_diff_decode(pool, q, block_table, context_lens, max_context_len, sm_scale, lam, out,
+                    workspace=None, norm_weight=None, eps=1e-5, out_scale=1.0, stream=None) -> None:
+    """Differential attention of single tokens, q [S, H, D] -> out fp16 [S, H, D]
+    (kvq_diff_decode in include/kvq.h); lam [H] and norm_weight [D] fp32."""
+    torch = _th()
+    S, H, max_blocks = _seqs(pool, q, block_table, context_lens)
+    dev = _device()
+    lp, wp, op = _diff(q, lam, out, norm_weight, dev)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().kvq_diff_decode(
+        pool, _at(q, torch.float16, "q", dev), S, H, _at(block_table, torch.int32, "block_table", dev),
+        max_blocks, _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len),
+        float(sm_scale), lp, wp, float(eps), float(out_scale), op,
+        None if workspace is None else _at(workspace, workspace.dtype, "workspace", dev), ws_bytes,
+        _stream(stream)), "kvq_diff_decode")
+
+
+def kvq_diff_prefill_workspace_bytes(pool, num_seqs, num_tokens, num_heads, max_context_len) -> int:
+    return int(lib().kvq_diff_prefill_workspace_bytes(pool, num_seqs, num_tokens, num_heads,
+                                                      max_context_len))
+
+
+def kvq_diff_prefill(pool, q, q_start, max_q_len, block_table, context_lens, max_context_len, sm_scale,
+                     lam, out, workspace, norm_weight=None, eps=1e-5, out_scale=1.0, stream=None) -> None:
+    """Differential attention of prompts, q [T, H, D] -> out fp16 [T, H, D]
+    (kvq_diff_prefill in include/kvq.h); q_start [S + 1] int32."""
+    torch = _th()
+    S, table = context_lens.numel(), block_table.shape
+    if q.dim() != 3 or q_start.numel() != S + 1:
+        raise ValueError("q must be [tokens, heads, head_dim] and q_start [num_seqs + 1]")
+    if len(table) != 2 or table[0] != S:
+        raise ValueError("block_table must be [num_seqs, max_blocks_per_seq]")
+    T, H, D = q.shape
+    rows = _pool_rows(pool)
+    if rows is not None and (D != rows[1] or H % rows[0] != 0):
+        raise ValueError("q must have the pool's head_dim of %d and a multiple of its %d kv heads"
+                         % (rows[1], rows[0]))
+    dev = _device()
+    lp, wp, op = _diff(q, lam, out, norm_weight, dev)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib().kvq_diff_prefill(
+        pool, _at(q, torch.float16, "q", dev), T, S, H, _at(q_start, torch.int32, "q_start", dev),
+        int(max_q_len), _at(block_table, torch.int32, "block_table", dev), table[1],
+        _at(context_lens, torch.int32, "context_lens", dev), int(max_context_len), float(sm_scale), lp,
+        wp, float(eps), float(out_scale), op,
+        None if workspace is None else _at(workspace, workspace.dtype, "workspace", dev), ws_bytes,
+        _stream(stream)), "kvq_diff_prefill")
+
+
+def _count(t, name, dev):
+    if t.numel() != 1:
+        raise ValueError("%s must be one int32" % name)
+    return _at(t, _th().int32, name, dev)
+
+
+def kvq_extend_tables(pool, new_tokens, block_table, context_lens, free_list, free_count, lens_out,
+                      count_out, q_start, slot_mapping, positions, stream=None) -> None:
+    """Blocks from the free list for each sequence's new tokens, into the block table, with
+    the rows' slots and positions (kvq_extend_tables in include/kvq.h).  lens_out may be
+    context_lens itself, count_out free_count."""
+    torch = _th()
+    S, T, table = context_lens.numel(), slot_mapping.numel(), block_table.shape
+    if len(table) != 2 or table[0] != S:
+        raise ValueError("block_table must be [num_seqs, blocks]")
+    if new_tokens.numel() != S or lens_out.numel() != S or q_start.numel() != S + 1:
+        raise ValueError("new_tokens, context_lens and lens_out must be [num_seqs], q_start [num_seqs + 1]")
+    if positions.numel() != T:
+        raise ValueError("slot_mapping and positions must have the same size")
+    dev, i32, i64 = _device(), torch.int32, torch.int64
+    _check(lib().kvq_extend_tables(
+        pool, _at(new_tokens, i32, "new_tokens", dev), S, _at(block_table, i32, "block_table", dev), table[1],
+        _at(context_lens, i32, "context_lens", dev), _at(free_list, i32, "free_list", dev), free_list.numel(),
+        _count(free_count, "free_count", dev), _at(lens_out, i32, "lens_out", dev),
+        _count(count_out, "count_out", dev), _at(q_start, i32, "q_start", dev),
+        _at(slot_mapping, i64, "slot_mapping", dev), _at(positions, i64, "positions", dev), T,
+        _stream(stream)), "kvq_extend_tables")
+
+
+def kvq_release_blocks(pool, block_table, old_lens, new_lens, free_list, free_count, count_out,
+                       shared_blocks=0, stream=None) -> None:
+    """Blocks of old_lens tokens that new_lens tokens do not need go back to the free list
+    (kvq_release_blocks in include/kvq.h).  count_out may be free_count itself."""
+    torch = _th()
+    S, table = old_lens.numel(), block_table.shape
+    if len(table) != 2 or table[0] != S or new_lens.numel() != S:
+        raise ValueError("block_table must be [num_seqs, blocks], old_lens and new_lens [num_seqs]")
+    dev, i32 = _device(), torch.int32
+    _check(lib().kvq_release_blocks(
+        pool, _at(block_table, i32, "block_table", dev), table[1], _at(old_lens, i32, "old_lens", dev),
+        _at(new_lens, i32, "new_lens", dev), S, int(shared_blocks), _at(free_list, i32, "free_list", dev),
+        free_list.numel(), _count(free_count, "free_count", dev), _count(count_out, "count_out", dev),
+        _stream(stream)), "kvq_release_blocks")
+
+
 def kvq_decode_step(pool, k_new, v_new, q, block_table, context_lens, max_context_len, sm_scale,
                     out, workspace=None, stream=None) -> None:
     """Append each sequence's new token at position context_lens[s]-1, then
@@ -865,6 +984,53 @@ class KVPool:
         kvq_evict_blocks(self.handle, scores, block_table, context_lens, max_context_len,
                          budget_blocks, sink_blocks, recent_blocks, table, lens, kept, out, stream)
         return table, lens, kept, out
+
+    def diff_decode(self, q, block_table, context_lens, max_context_len, lam, norm_weight=None, eps=1e-5,
+                    out_scale=1.0, sm_scale=None, stream=None):
+        """Differential attention of single tokens, fp16 [S, H, D]."""
+        torch = _th()
+        S, H, D = q.shape
+        nws = kvq_diff_decode_workspace_bytes(self.handle, S, H, max_context_len)
+        with _on(stream):
+            out = torch.empty((S, H, D), dtype=torch.float16, device=q.device)
+            ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
+        kvq_diff_decode(self.handle, q, block_table, context_lens, max_context_len,
+                        (D // 2) ** -0.5 if sm_scale is None else sm_scale, lam, out, ws, norm_weight, eps,
+                        out_scale, stream)
+        return out
+
+    def diff_prefill(self, q, q_start, max_q_len, block_table, context_lens, max_context_len, lam,
+                     norm_weight=None, eps=1e-5, out_scale=1.0, sm_scale=None, stream=None):
+        """Differential attention of prompts, fp16 [T, H, D]; rows behind the last sequence are zeros."""
+        torch = _th()
+        T, H, D = q.shape
+        nws = kvq_diff_prefill_workspace_bytes(self.handle, context_lens.numel(), T, H, max_context_len)
+        with _on(stream):
+            out = torch.zeros((T, H, D), dtype=torch.float16, device=q.device)
+            ws = torch.empty(nws, dtype=torch.uint8, device=q.device) if nws else None
+        kvq_diff_prefill(self.handle, q, q_start, max_q_len, block_table, context_lens, max_context_len,
+                         (D // 2) ** -0.5 if sm_scale is None else sm_scale, lam, out, ws, norm_weight, eps,
+                         out_scale, stream)
+        return out
+
+    def extend_tables(self, new_tokens, block_table, context_lens, free_list, free_count, max_tokens,
+                      stream=None):
+        """(q_start, slot_mapping, positions) of a step; block_table, context_lens and
+        free_count are updated in place."""
+        torch = _th()
+        with _on(stream):
+            q_start = torch.empty(context_lens.numel() + 1, dtype=torch.int32, device=context_lens.device)
+            slots = torch.empty(max_tokens, dtype=torch.int64, device=context_lens.device)
+            positions = torch.empty_like(slots)
+        kvq_extend_tables(self.handle, new_tokens, block_table, context_lens, free_list, free_count,
+                          context_lens, free_count, q_start, slots, positions, stream)
+        return q_start, slots, positions
+
+    def release_blocks(self, block_table, old_lens, new_lens, free_list, free_count, shared_blocks=0,
+                       stream=None):
+        """Blocks beyond new_lens go back to the free list, whose count is updated in place."""
+        kvq_release_blocks(self.handle, block_table, old_lens, new_lens, free_list, free_count, free_count,
+                           shared_blocks, stream)
 
     def cascade_decode(self, q, block_table, context_lens, max_context_len, prefix_blocks,
                        sm_scale=None, out=None, stream=None):

@@ -752,6 +752,156 @@ kvq_status kvq_prefill_ex(const kvq_pool* pool, const kvq_half* q, int num_seqs,
   return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
 }
 
+}  // extern "C"
+
+// Checks of what the differential calls add; fills *d.
+static bool diff_args_ok(const float* lambda, const float* norm_weight, float eps, float out_scale,
+                         kvq_half* out, kvq::DiffOut* d) {
+  if (lambda == nullptr || out == nullptr || !(eps >= 0.f) || !std::isfinite(out_scale)) return false;
+  d->lambda = lambda;
+  d->weight = norm_weight;
+  d->eps = eps;
+  d->out_scale = out_scale;
+  d->out = reinterpret_cast<__half*>(out);
+  return true;
+}
+
+constexpr int kMaxDiffHeads = 1 << 20;
+
+extern "C" {
+
+size_t kvq_diff_decode_workspace_bytes(const kvq_pool* pool, int num_seqs, int num_heads,
+                                       int max_context_len) {
+  if (num_heads < 1 || num_heads > kMaxDiffHeads || pool == nullptr || num_heads % pool->view.Hkv != 0) return 0;
+  return kvq_decode_workspace_bytes_ex(pool, num_seqs, 2 * num_heads, max_context_len, 0);
+}
+
+kvq_status kvq_diff_decode(const kvq_pool* pool, const kvq_half* q, int num_seqs, int num_heads,
+                           const int32_t* block_table, int max_blocks_per_seq,
+                           const int32_t* context_lens, int max_context_len, float sm_scale,
+                           const float* lambda, const float* norm_weight, float eps,
+                           float out_scale, kvq_half* out, void* workspace, size_t ws_bytes,
+                           cudaStream_t stream) {
+  if (pool == nullptr || num_heads < 1 || num_heads % pool->view.Hkv != 0) return KVQ_ERR_INVALID_ARG;
+  if (num_heads > kMaxDiffHeads) return KVQ_ERR_UNSUPPORTED;
+  kvq::DecodeArgs a;
+  kvq::DecodePlan plan;
+  const kvq_status st = prepare_decode(pool, q, num_seqs, 2 * num_heads, block_table, max_blocks_per_seq,
+                                       context_lens, max_context_len, sm_scale,
+                                       reinterpret_cast<float*>(out), workspace, ws_bytes, 0, &a, &plan);
+  if (st != KVQ_OK || num_seqs == 0) return st;
+  if (!diff_args_ok(lambda, norm_weight, eps, out_scale, out, &a.diff)) return KVQ_ERR_INVALID_ARG;
+  a.q_stride = (int64_t)num_heads * pool->view.D;
+  return from_cuda(kvq::launch_decode(a, plan, stream));
+}
+
+size_t kvq_diff_prefill_workspace_bytes(const kvq_pool* pool, int num_seqs, int64_t num_tokens,
+                                        int num_heads, int max_context_len) {
+  if (pool == nullptr || num_seqs < 1 || num_tokens < 1 || num_tokens > 0x7fffffffLL || num_heads < 1 ||
+      num_heads > kMaxDiffHeads || num_heads % pool->view.Hkv != 0 || max_context_len < 1 ||
+      pool->view.bs == 8)
+    return 0;
+  return kvq::diff_prefill_ws_bytes(pool->view, num_tokens, num_seqs, num_heads, max_context_len);
+}
+
+kvq_status kvq_diff_prefill(const kvq_pool* pool, const kvq_half* q, int64_t num_tokens, int num_seqs,
+                            int num_heads, const int32_t* q_start, int max_q_len,
+                            const int32_t* block_table, int max_blocks_per_seq,
+                            const int32_t* context_lens, int max_context_len, float sm_scale,
+                            const float* lambda, const float* norm_weight, float eps,
+                            float out_scale, kvq_half* out, void* workspace, size_t ws_bytes,
+                            cudaStream_t stream) {
+  if (pool == nullptr || num_tokens < 0 || num_seqs < 0 || num_heads < 1 || max_q_len < 0 ||
+      max_blocks_per_seq < 1 || max_context_len < 0 || num_heads % pool->view.Hkv != 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (pool->view.bs == 8 || num_heads > kMaxDiffHeads || num_tokens > 0x7fffffffLL) return KVQ_ERR_UNSUPPORTED;
+  if ((int64_t)max_context_len > (int64_t)max_blocks_per_seq * pool->view.bs) return KVQ_ERR_INVALID_ARG;
+  if (!(sm_scale == sm_scale)) return KVQ_ERR_INVALID_ARG;
+  if (num_seqs == 0 || max_q_len == 0 || num_tokens == 0) return KVQ_OK;
+  kvq::DiffOut d;
+  if (q == nullptr || q_start == nullptr || block_table == nullptr || context_lens == nullptr ||
+      !diff_args_ok(lambda, norm_weight, eps, out_scale, out, &d))
+    return KVQ_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(q) & 15) return KVQ_ERR_INVALID_ARG;
+  if (max_context_len == 0) return KVQ_ERR_INVALID_ARG;
+  const size_t need = kvq_diff_prefill_workspace_bytes(pool, num_seqs, num_tokens, num_heads, max_context_len);
+  if (workspace == nullptr || ws_bytes < need) return KVQ_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255) return KVQ_ERR_INVALID_ARG;
+  const cudaError_t e = kvq::launch_diff_prefill(
+      pool->view, reinterpret_cast<const __half*>(q), num_tokens, num_seqs, num_heads, q_start, max_q_len,
+      block_table, max_blocks_per_seq, context_lens, max_context_len, sm_scale, d, workspace, stream);
+  return e == cudaErrorInvalidValue ? KVQ_ERR_UNSUPPORTED : from_cuda(e);
+}
+
+constexpr int kMaxPlanSeqs = 16384;  // (their prefix sums lie in shared memory)
+
+kvq_status kvq_extend_tables(const kvq_pool* pool, const int32_t* new_tokens, int num_seqs,
+                             int32_t* block_table, int max_blocks_per_seq,
+                             const int32_t* context_lens, const int32_t* free_list,
+                             int free_capacity, const int32_t* free_count, int32_t* lens_out,
+                             int32_t* count_out, int32_t* q_start, int64_t* slot_mapping,
+                             int64_t* positions, int max_tokens, cudaStream_t stream) {
+  if (pool == nullptr || num_seqs < 0 || max_blocks_per_seq < 1 || free_capacity < 0 || max_tokens < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (free_count == nullptr || count_out == nullptr || q_start == nullptr ||
+      (free_capacity > 0 && free_list == nullptr))
+    return KVQ_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (new_tokens == nullptr || block_table == nullptr || context_lens == nullptr ||
+                       lens_out == nullptr))
+    return KVQ_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (slot_mapping == nullptr || positions == nullptr)) return KVQ_ERR_INVALID_ARG;
+  if (num_seqs > kMaxPlanSeqs || free_capacity == 0x7fffffff || max_tokens == 0x7fffffff)
+    return KVQ_ERR_UNSUPPORTED;
+  kvq::ExtendArgs a;
+  a.n = new_tokens;
+  a.lens = context_lens;
+  a.table = block_table;
+  a.free_list = free_list;
+  a.count = free_count;
+  a.lens_out = lens_out;
+  a.count_out = count_out;
+  a.q_start = q_start;
+  a.slots = slot_mapping;
+  a.positions = positions;
+  a.err = pool->view.err;
+  a.num_blocks = pool->view.num_blocks;
+  a.S = num_seqs;
+  a.max_blocks = max_blocks_per_seq;
+  a.capacity = free_capacity;
+  a.max_tokens = max_tokens;
+  a.bs = pool->view.bs;
+  return from_cuda(kvq::launch_extend(a, stream));
+}
+
+kvq_status kvq_release_blocks(const kvq_pool* pool, const int32_t* block_table, int max_blocks_per_seq,
+                              const int32_t* old_lens, const int32_t* new_lens, int num_seqs,
+                              int shared_blocks, int32_t* free_list, int free_capacity,
+                              const int32_t* free_count, int32_t* count_out, cudaStream_t stream) {
+  if (pool == nullptr || num_seqs < 0 || max_blocks_per_seq < 1 || shared_blocks < 0 || free_capacity < 0)
+    return KVQ_ERR_INVALID_ARG;
+  if (free_count == nullptr || count_out == nullptr || (free_capacity > 0 && free_list == nullptr))
+    return KVQ_ERR_INVALID_ARG;
+  if (num_seqs > 0 && (block_table == nullptr || old_lens == nullptr || new_lens == nullptr))
+    return KVQ_ERR_INVALID_ARG;
+  if (num_seqs > kMaxPlanSeqs || (int64_t)num_seqs * max_blocks_per_seq >= 0x7fffffffLL)
+    return KVQ_ERR_UNSUPPORTED;
+  kvq::ReleaseArgs a;
+  a.table = block_table;
+  a.old_lens = old_lens;
+  a.new_lens = new_lens;
+  a.free_list = free_list;
+  a.count = free_count;
+  a.count_out = count_out;
+  a.err = pool->view.err;
+  a.num_blocks = pool->view.num_blocks;
+  a.S = num_seqs;
+  a.max_blocks = max_blocks_per_seq;
+  a.capacity = free_capacity;
+  a.shared = shared_blocks;
+  a.bs = pool->view.bs;
+  return from_cuda(kvq::launch_release(a, stream));
+}
+
 kvq_status kvq_paged_decode(const kvq_pool* pool, const kvq_half* q, int num_seqs, int num_q_heads,
                             const int32_t* block_table, int max_blocks_per_seq,
                             const int32_t* context_lens, int max_context_len, float sm_scale,

@@ -1,0 +1,286 @@
+// kvq_blocks.cu -- a step's block tables, slot map and positions from the requests'
+// lengths, and the blocks of requests that shrank or ended back on the free list, so
+// that a serving step (a captured one, too) needs no host to plan it.
+//
+//   need_s = ceil((L_s + n_s) / bs) - ceil(L_s / bs)     blocks sequence s takes
+//   q_s    = n_0 + .. + n_{s-1}                          its first row
+//   b_s    = need_0 + .. + need_{s-1}                    blocks taken before it
+//   row q_s + i: position L_s + i, in block (L_s + i) / bs of its table row, which
+//   is an older entry or free_list[count - 1 - (b_s + .. )]
+//
+// Two prefix sums over the sequences, then one independent lookup per row and per new
+// table entry.  Bound: latency -- a launch, a chain of loads (lengths, then free-list
+// entries) and the scan's barriers; the bytes are 16 a row.  One thread-block cluster
+// does it all: every CTA makes the whole scan for itself (8 bytes a sequence, from L2)
+// and keeps it in shared memory, the rows and entries are shared out among the CTAs, and
+// one cluster barrier stands between the last read of the lengths and the count and the
+// first write to them, so that both may be updated in place.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "kvq_context.h"
+#include "kvq_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace kvq {
+
+namespace {
+
+constexpr int kPlanThreads = 512;
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr uint32_t kPlanCap = 0x7fffffffu;  // prefix sums stop here
+
+// a + b of two sums that are at most the cap, at most the cap (associative).
+__device__ __forceinline__ uint32_t cap_add(uint32_t a, uint32_t b) { return min(a + b, kPlanCap); }
+
+// Sums (capped) of two values over the threads before this one and over all of them.
+struct PairScan {
+  uint2* part;  // [kPlanWarps]
+
+  __device__ __forceinline__ uint2 before(uint2 v, uint2* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint2 x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
+      if (lane >= o) x = make_uint2(cap_add(x.x, a), cap_add(x.y, b));
+    }
+    uint2 e = make_uint2(__shfl_up_sync(0xffffffffu, x.x, 1), __shfl_up_sync(0xffffffffu, x.y, 1));
+    if (lane == 0) e = make_uint2(0, 0);
+    __syncthreads();  // (the sums of the call before have been read)
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    uint2 w = make_uint2(0, 0), all = make_uint2(0, 0);
+#pragma unroll
+    for (int i = 0; i < kPlanWarps; ++i) {
+      const uint2 p = part[i];
+      if (i < warp) w = make_uint2(cap_add(w.x, p.x), cap_add(w.y, p.y));
+      all = make_uint2(cap_add(all.x, p.x), cap_add(all.y, p.y));
+    }
+    *total = all;
+    return make_uint2(cap_add(w.x, e.x), cap_add(w.y, e.y));
+  }
+};
+
+// Last index s in [0, n) with first[s] <= x (first[0] = 0 <= x).
+__device__ __forceinline__ int last_at_most(const uint32_t* first, int n, uint32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kvq_extend_kernel(const __grid_constant__ ExtendArgs p,
+                                                                 int bs_log2) {
+  extern __shared__ uint32_t smem[];
+  const int S = p.S, tid = threadIdx.x;
+  PairScan scan{reinterpret_cast<uint2*>(smem)};  // [kPlanWarps]
+  uint32_t* rows = smem + 2 * kPlanWarps;         // [S + 1] rows before each sequence
+  uint32_t* taken = rows + S + 1;                 // [S + 1] blocks before it
+  int* len = reinterpret_cast<int*>(taken + S + 1);  // [S] its length, or ~length where it is not served
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
+  const int bs = 1 << bs_log2;
+
+  int count = *p.count;
+  if (count < 0 || count > p.capacity) {
+    if (rank == 0 && tid == 0) set_error(p.err, ERR_RANGE);
+    count = min(max(count, 0), p.capacity);
+  }
+  // ---- prefix sums; who is served
+  uint2 carry = make_uint2(0, 0);
+  uint32_t served = 0;  // blocks that served sequences take
+  for (int base = 0; base < S; base += kPlanThreads) {
+    const int s = base + tid;
+    int L = 0, n = 0;
+    if (s < S) {
+      L = p.lens[s];
+      n = p.n[s];
+    }
+    const bool ok = n >= 0 && L >= 0 && (int64_t)L + n <= (int64_t)p.max_blocks << bs_log2;
+    const uint32_t need = ok ? static_cast<uint32_t>((((int64_t)L + n + bs - 1) >> bs_log2) - (((int64_t)L + bs - 1) >> bs_log2)) : 0;
+    uint2 all;
+    const uint2 own = make_uint2(max(n, 0), need);
+    uint2 at = scan.before(own, &all);
+    at = make_uint2(cap_add(carry.x, at.x), cap_add(carry.y, at.y));
+    const uint2 end = make_uint2(cap_add(at.x, own.x), cap_add(at.y, own.y));
+    carry = make_uint2(cap_add(carry.x, all.x), cap_add(carry.y, all.y));
+    // (a sum at the cap is more than any call has of either)
+    const bool serve = ok && end.x <= static_cast<uint32_t>(p.max_tokens) &&
+                       (need == 0 || end.y <= static_cast<uint32_t>(count));
+    if (s < S) {
+      rows[s] = min(at.x, static_cast<uint32_t>(p.max_tokens));
+      taken[s] = at.y;
+      len[s] = serve ? L : ~max(L, 0);
+      if (serve && need > 0) served = end.y;  // (they take the first blocks: the last one's end is their sum)
+      if (!serve && rank == 0) set_error(p.err, ERR_RANGE);
+    }
+  }
+  if (tid == 0) {
+    rows[S] = min(carry.x, static_cast<uint32_t>(p.max_tokens));
+    taken[S] = carry.y;
+  }
+  served = __reduce_max_sync(0xffffffffu, served);
+  __syncthreads();  // rows, taken, len; the scan's sums have been read
+  if ((tid & 31) == 0) smem[tid >> 5] = served;
+  __syncthreads();
+  served = __reduce_max_sync(0xffffffffu, smem[tid & (kPlanWarps - 1)]);
+
+  // every CTA has read the lengths and the count
+  if (ranks > 1) cluster.sync();
+  const int step = ranks * kPlanThreads, me = rank * kPlanThreads + tid;
+  if (me == 0) *p.count_out = count - static_cast<int>(served);
+  for (int s = me; s <= S; s += step) {
+    p.q_start[s] = static_cast<int>(rows[s]);
+    if (s == S) break;
+    const int L = len[s];
+    if (L >= 0) p.lens_out[s] = L + static_cast<int>(rows[s + 1] - rows[s]);
+    else if (p.lens_out != p.lens) p.lens_out[s] = p.lens[s];
+  }
+  auto pool_block = [&](int id) { return id >= 0 && (int64_t)id < p.num_blocks; };
+  // ---- new table entries
+  for (uint32_t k = me; k < served; k += step) {
+    const int s = last_at_most(taken, S, k);
+    const int64_t j = (((int64_t)len[s] + bs - 1) >> bs_log2) + (k - taken[s]);
+    const int id = p.free_list[count - 1 - static_cast<int>(k)];
+    if (!pool_block(id)) set_error(p.err, ERR_RANGE);
+    p.table[(int64_t)s * p.max_blocks + j] = id;
+  }
+  // ---- rows
+  for (int64_t r = me; r < p.max_tokens; r += step) {
+    int64_t slot = -1, pos = 0;
+    if (r < rows[S]) {
+      const int s = last_at_most(rows, S, static_cast<uint32_t>(r));
+      const int L = len[s];
+      pos = (L >= 0 ? L : ~L) + (r - rows[s]);
+      if (L >= 0) {
+        const int64_t held = ((int64_t)L + bs - 1) >> bs_log2, j = pos >> bs_log2;
+        const int id = j < held ? p.table[(int64_t)s * p.max_blocks + j]
+                                : p.free_list[count - 1 - static_cast<int>(taken[s] + (j - held))];
+        if (pool_block(id)) slot = ((int64_t)id << bs_log2) + (pos & (bs - 1));
+        else set_error(p.err, ERR_RANGE);
+      }
+    }
+    p.slots[r] = slot;
+    p.positions[r] = pos;
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kvq_release_kernel(const __grid_constant__ ReleaseArgs p,
+                                                                  int bs_log2) {
+  extern __shared__ uint32_t smem[];
+  const int S = p.S, tid = threadIdx.x;
+  PairScan scan{reinterpret_cast<uint2*>(smem)};  // [kPlanWarps]
+  uint32_t* here = smem + 2 * kPlanWarps;         // blocks of the pool among this CTA's entries
+  uint32_t* gone = here + 1;                      // [S] entries before each sequence
+  int* first = reinterpret_cast<int*>(gone + S);  // [S] its first entry that goes
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
+  const int bs = 1 << bs_log2;
+
+  int count = *p.count;
+  if (count < 0 || count > p.capacity) {
+    if (rank == 0 && tid == 0) set_error(p.err, ERR_RANGE);
+    count = min(max(count, 0), p.capacity);
+  }
+  uint2 carry = make_uint2(0, 0);
+  for (int base = 0; base < S; base += kPlanThreads) {
+    const int s = base + tid;
+    int64_t from = 0, to = 0;
+    if (s < S) {
+      const int a = p.old_lens[s], b = p.new_lens[s];
+      to = ((int64_t)max(a, 0) + bs - 1) >> bs_log2;
+      from = max(((int64_t)max(b, 0) + bs - 1) >> bs_log2, (int64_t)p.shared);
+      if (a < 0 || b < 0 || to > p.max_blocks) {
+        if (rank == 0) set_error(p.err, ERR_RANGE);
+        to = min(to, (int64_t)p.max_blocks);
+      }
+    }
+    uint2 all;
+    const uint2 at = scan.before(make_uint2(from < to ? static_cast<uint32_t>(to - from) : 0, 0), &all);
+    if (s < S) {
+      gone[s] = cap_add(carry.x, at.x);
+      first[s] = static_cast<int>(min(from, (int64_t)p.max_blocks));
+    }
+    carry.x = cap_add(carry.x, all.x);
+  }
+  const uint32_t total = carry.x;
+  if (tid == 0) *here = 0;
+  __syncthreads();
+
+  // ---- this CTA's entries: how many are blocks of the pool, then each to its place
+  const uint32_t per = (total + ranks - 1) / ranks;
+  const uint32_t e0 = static_cast<uint32_t>(min((uint64_t)rank * per, (uint64_t)total));
+  const uint32_t e1 = static_cast<uint32_t>(min((uint64_t)e0 + per, (uint64_t)total));
+  auto entry = [&](uint32_t e) {
+    const int s = last_at_most(gone, S, e);
+    const int id = p.table[(int64_t)s * p.max_blocks + first[s] + (e - gone[s])];
+    return id >= 0 && (int64_t)id < p.num_blocks ? id : -1;
+  };
+  uint32_t mine = 0;
+  if (ranks > 1) {
+    for (uint32_t e = e0 + tid; e < e1; e += kPlanThreads) mine += entry(e) >= 0;
+    mine = __reduce_add_sync(0xffffffffu, mine);
+    if ((tid & 31) == 0 && mine > 0) atomicAdd(here, mine);
+    cluster.sync();  // (and every CTA has read the count)
+  }
+  uint32_t at = 0;
+  for (int q = 0; q < rank; ++q) at += *cluster.map_shared_rank(here, q);
+  for (uint32_t base = e0; base < e1; base += kPlanThreads) {
+    const uint32_t e = base + tid;
+    const int id = e < e1 ? entry(e) : -1;
+    if (e < e1 && id < 0) set_error(p.err, ERR_RANGE);
+    uint2 all;
+    const uint32_t k = at + scan.before(make_uint2(id >= 0, 0), &all).x;
+    if (id >= 0) {
+      if ((int64_t)count + k < p.capacity) p.free_list[count + k] = id;
+      else set_error(p.err, ERR_RANGE);
+    }
+    at += all.x;
+  }
+  // the last CTA has counted them all
+  if (rank == ranks - 1 && tid == 0)
+    *p.count_out = static_cast<int>(min((int64_t)count + at, (int64_t)p.capacity));
+  if (ranks > 1) cluster.sync();  // no CTA leaves while its count may be read
+}
+
+template <class Args>
+cudaError_t launch_plan(void (*kernel)(const Args, int), const Args& a, int bs, int ctas, size_t smem,
+                        cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int log2 = 0;
+  while ((1 << log2) < bs) ++log2;
+  return phase_mark(st, cudaLaunchKernelEx(&cfg, kernel, a, log2));
+}
+
+}  // namespace
+
+cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
+  const size_t smem = (2 * kPlanWarps + 3 * (size_t)a.S + 2) * 4;
+  const cudaError_t e = allow_big_smem<kvq_extend_kernel>();
+  if (e != cudaSuccess) return e;
+  return launch_plan(kvq_extend_kernel, a, a.bs, a.max_tokens > 2048 ? 8 : 1, smem, st);
+}
+
+cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t st) {
+  const size_t smem = (2 * kPlanWarps + 1 + 2 * (size_t)a.S) * 4;
+  const cudaError_t e = allow_big_smem<kvq_release_kernel>();
+  if (e != cudaSuccess) return e;
+  return launch_plan(kvq_release_kernel, a, a.bs, (int64_t)a.S * a.max_blocks > 16384 ? 8 : 1, smem, st);
+}
+
+}  // namespace kvq

@@ -119,6 +119,7 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
   p.skip = a.skip;
   p.pre = a.pre;
   p.lse = a.lse;
+  p.diff = a.diff;
   p.wait_tries = a.wait_tries;
   p.fault_issue = a.fault_issue;
   l.grid = dim3(static_cast<unsigned>(plan.grid));
@@ -128,6 +129,7 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
   l.st = st;
   l.dependent = dependent;
   l.two_ctas = plan.two_ctas;
+  if (a.diff.lambda != nullptr) return launch_decode_diff(l);
   if (fmt_block(a.pool.fmt)) return launch_decode_block(l);
   if (a.pool.bs == 8)
     return a.pool.fmt == FMT_INT8_GROUP ? launch_decode_bs8_group(l) : launch_decode_bs8_misc(l);

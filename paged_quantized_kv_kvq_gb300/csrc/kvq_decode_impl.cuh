@@ -45,6 +45,7 @@
 #include "kvq_common.cuh"
 #include "kvq_context.h"
 #include "kvq_fp4.cuh"
+#include "kvq_internal.h"
 
 namespace kvq {
 
@@ -54,6 +55,14 @@ constexpr int kDecodeCtasPerSm = 3;  // resident CTAs per SM the grid is sized f
 constexpr int kDecodeThreads = kDecodeWarps * 32;
 constexpr int kPartRows = 8;       // partial rows per (warp, slot): one per Q head of a tile
 constexpr int kMergeThreads = 256;
+
+// Factor of a row whose squares sum to ss (a row of zeros stays one).
+template <int D>
+__device__ __forceinline__ float diff_factor(const DiffOut& o, float ss) {
+  if (o.weight == nullptr) return o.out_scale;
+  const float v = fmaf(ss, 1.f / D, o.eps);
+  return v > 0.f ? o.out_scale * rsqrtf(v) : 0.f;
+}
 
 struct DecodeParams {
   PoolView pool;
@@ -71,6 +80,7 @@ struct DecodeParams {
   const float* pre;
   int skip;
   float* lse;          // [S][Hq] natural log of each row's softmax denominator, or null
+  DiffOut diff;        // differential attention (DIFF kernels)
   int S, Hq, G, n_ht, max_blocks, max_ctx;
   int ppw_fixed;       // pages per warp; 0 = balance the pages over all warps
   int nstage;          // shared-memory stages per warp
@@ -636,8 +646,9 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
 // Q fragments of a unit: head n = g of the tile, channels 16kk + 4j .. +3.
 // Per-channel pools fold the K channel scale into q (fp32), scale the result by
 // 2^eq so that max|q'| lies in [2^13, 2^14), and split it into fp16 hi + lo;
-// csc then carries 2^-eq.
-template <int FMT, int D>
+// csc then carries 2^-eq.  DIFF: row g of the tile is a map of a head, the other map's
+// channels zero.
+template <int FMT, int D, bool DIFF = false>
 __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, int ht, int lane,
                                        uint32_t (&qb)[D / 16][2],
                                        uint32_t (&ql)[FmtTraits<FMT>::channel ? D / 16 : 1][2],
@@ -647,12 +658,13 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, int 
   const int Gt = min(8, p.G - 8 * ht);
   const bool hv = g < Gt;
   const int hq = h * p.G + 8 * ht + (hv ? g : 0);
-  const __half* qp = p.q + (int64_t)s * p.q_stride + (int64_t)hq * D;
+  const __half* qp = p.q + (int64_t)s * p.q_stride + (int64_t)(DIFF ? hq >> 1 : hq) * D;
+  auto has = [&](int kk) { return hv && (!DIFF || (kk >= KS / 2) == ((hq & 1) != 0)); };
   csc = p.sm_scale_log2;
   if constexpr (!FmtTraits<FMT>::channel) {
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
-      uint2 v = hv ? *reinterpret_cast<const uint2*>(qp + 16 * kk + 4 * j) : make_uint2(0, 0);
+      uint2 v = has(kk) ? *reinterpret_cast<const uint2*>(qp + 16 * kk + 4 * j) : make_uint2(0, 0);
       qb[kk][0] = v.x;
       qb[kk][1] = v.y;
     }
@@ -662,7 +674,7 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, int 
     float amax = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
-      uint2 v = hv ? *reinterpret_cast<const uint2*>(qp + 16 * kk + 4 * j) : make_uint2(0, 0);
+      uint2 v = has(kk) ? *reinterpret_cast<const uint2*>(qp + 16 * kk + 4 * j) : make_uint2(0, 0);
       __half2 a = *reinterpret_cast<__half2*>(&v.x), b = *reinterpret_cast<__half2*>(&v.y);
       const int d0 = 16 * kk + 4 * j;
       qf[kk][0] = __low2float(a) * ksc[d0 + 0];
@@ -685,7 +697,7 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, int s, int h, int 
   }
 }
 
-template <int FMT, int D, int NG, bool BS8, int CTAS>
+template <int FMT, int D, int NG, bool BS8, int CTAS, bool DIFF>
 __global__ void __launch_bounds__(kDecodeThreads, CTAS)
     kvq_decode_kernel(const DecodeParams p) {
   using T = FmtTraits<FMT>;
@@ -772,6 +784,11 @@ __global__ void __launch_bounds__(kDecodeThreads, CTAS)
     // the normalised prefix result
     for (int s = gw; s < p.S; s += nwarps) {
       if (PS[s + 1] != PS[s]) continue;
+      if constexpr (DIFF) {
+        __half* o = p.diff.out + (int64_t)s * (p.Hq / 2) * D;
+        for (int i = lane; i < p.Hq / 2 * D; i += 32) o[i] = __ushort_as_half(0);
+        continue;
+      }
       float* o = p.out + (int64_t)s * p.out_stride;
       if (p.lse != nullptr)
         for (int i = lane; i < p.Hq; i += 32) p.lse[(int64_t)s * p.Hq + i] = kNegInf;
@@ -975,7 +992,7 @@ __global__ void __launch_bounds__(kDecodeThreads, CTAS)
   int L = 0;                  // context length of the current unit's sequence
   auto start_unit = [&]() {
     L = min(p.lens[cc.s], p.max_ctx) - p.skip * bs;  // tokens after the skipped prefix
-    load_q<FMT, D>(p, cc.s, cc.lu / p.n_ht, cc.lu % p.n_ht, lane, qb, ql, csc);
+    load_q<FMT, D, DIFF>(p, cc.s, cc.lu / p.n_ht, cc.lu % p.n_ht, lane, qb, ql, csc);
     m[0] = m[1] = kNegInf;
     l[0] = l[1] = 0.f;
     E = T::row_scales && !tile_scale<FMT, BS8>() ? 100 : 14;
@@ -994,6 +1011,33 @@ __global__ void __launch_bounds__(kDecodeThreads, CTAS)
     const float* vch = T::channel ? pool.chan_scales + ((int64_t)pool.Hkv + h) * D : nullptr;
     const int64_t row0 = (int64_t)u.s * p.Hq + h * p.G + 8 * ht;  // (prefix partials, lse)
     float* obase = p.out + (int64_t)u.s * p.out_stride + (int64_t)(h * p.G + 8 * ht) * D;
+    if (DIFF && seg_pi0 == 0 && seg_end == u.Ps) {  // both maps of a head are this lane's
+      const float f0 = lt0 > 0.f ? inv2E / lt0 : 0.f, f1 = lt1 > 0.f ? inv2E / lt1 : 0.f;
+      const int head = h * (p.G / 2) + 4 * ht + j;
+      const bool there = 2 * j < Gt;
+      const float f1l = there ? f1 * p.diff.lambda[head] : 0.f;
+      float ss = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        const int d0 = 16 * mt + g;
+        const float c0 = T::channel ? vch[d0] : 1.f, c8 = T::channel ? vch[d0 + 8] : 1.f;
+        o[mt][0] = (o[mt][0] * f0 - o[mt][1] * f1l) * c0;
+        o[mt][2] = (o[mt][2] * f0 - o[mt][3] * f1l) * c8;
+        ss = fmaf(o[mt][0], o[mt][0], fmaf(o[mt][2], o[mt][2], ss));
+      }
+      const float f = diff_factor<D>(p.diff, warp_sum_over_rows(ss));
+      if (!there) return;
+      __half* dst = p.diff.out + ((int64_t)u.s * (p.Hq / 2) + head) * D;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        const int d0 = 16 * mt + g;
+        const float w0 = p.diff.weight != nullptr ? f * p.diff.weight[d0] : f;
+        const float w8 = p.diff.weight != nullptr ? f * p.diff.weight[d0 + 8] : f;
+        dst[d0] = __float2half_rn(o[mt][0] * w0);
+        dst[d0 + 8] = __float2half_rn(o[mt][2] * w8);
+      }
+      return;
+    }
     if (seg_pi0 == 0 && seg_end == u.Ps) {
       if (p.lse != nullptr && g == 0) {
         if (2 * j < Gt) p.lse[row0 + 2 * j] = row_lse(m[0], lt0);
@@ -1241,6 +1285,57 @@ __global__ void __launch_bounds__(kDecodeThreads, CTAS)
   }
 }
 
+// Row rr of the pieces of a unit (warps wf .. wf + n_u - 1, first page U0) into the running
+// maximum M, sum Lsum and unnormalised output acc (elements lane + 32 i).
+template <int D, int CH>
+__device__ __forceinline__ void merge_pieces(const DecodeParams& p, int wf, int n_u, int U0, int ppw,
+                                             int rr, int lane, float& M, float& Lsum,
+                                             float (&acc)[D / 32]) {
+  constexpr int NE = D / 32;
+  const float kNegInf = __int_as_float(0xff800000u);
+  for (int k0 = 0; k0 < n_u; k0 += CH) {
+    float mk[CH], lk[CH], ok[CH][NE];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int k = k0 + c;
+      if (k < n_u) {
+        const int w = wf + k;
+        const int sl = (k == 0 && (int64_t)w * ppw < U0) ? 1 : 0;
+        const float* pr = p.part + (((int64_t)w * 2 + sl) * kPartRows + rr) * (D + 2);
+        mk[c] = __ldcg(pr);
+        lk[c] = __ldcg(pr + 1);
+#pragma unroll
+        for (int i = 0; i < NE; ++i) ok[c][i] = __ldcg(pr + 2 + lane + 32 * i);
+      } else {
+        mk[c] = kNegInf;
+        lk[c] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i) ok[c][i] = 0.f;
+      }
+    }
+    float cm = M;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) cm = fmaxf(cm, mk[c]);
+    if (cm == kNegInf) {  // no token yet, or NaN scores alone: sums of 0 or NaN
+#pragma unroll
+      for (int c = 0; c < CH; ++c) Lsum += lk[c];
+      continue;
+    }
+    const float fo = M == kNegInf ? 0.f : fast_exp2(M - cm);
+    Lsum *= fo;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) acc[i] *= fo;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const float wgt = mk[c] == kNegInf ? 0.f : fast_exp2(mk[c] - cm);
+      Lsum = fmaf(wgt, lk[c], Lsum);
+#pragma unroll
+      for (int i = 0; i < NE; ++i) acc[i] = fmaf(wgt, ok[c][i], acc[i]);
+    }
+    M = cm;
+  }
+}
+
 // Log-sum-exp merge of the units that the decode kernel's warp ranges cut:
 // unit u's pieces are the partials of warps wf..wl (slot 1 of wf when its range
 // started before the unit, slot 0 otherwise).  Launched as a programmatic
@@ -1295,51 +1390,70 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const DecodePa
 #pragma unroll
       for (int i = 0; i < NE; ++i) acc[i] = pr[2 + lane + 32 * i];
     }
-    for (int k0 = 0; k0 < n_u; k0 += CH) {
-      float mk[CH], lk[CH], ok[CH][NE];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const int k = k0 + c;
-        if (k < n_u) {
-          const int w = wf + k;
-          const int sl = (k == 0 && (int64_t)w * ppw < U0) ? 1 : 0;
-          const float* pr = p.part + (((int64_t)w * 2 + sl) * kPartRows + rr) * (D + 2);
-          mk[c] = __ldcg(pr);
-          lk[c] = __ldcg(pr + 1);
-#pragma unroll
-          for (int i = 0; i < NE; ++i) ok[c][i] = __ldcg(pr + 2 + lane + 32 * i);
-        } else {
-          mk[c] = kNegInf;
-          lk[c] = 0.f;
-#pragma unroll
-          for (int i = 0; i < NE; ++i) ok[c][i] = 0.f;
-        }
-      }
-      float cm = M;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) cm = fmaxf(cm, mk[c]);
-      if (cm == kNegInf) {  // no token yet, or NaN scores alone: sums of 0 or NaN
-#pragma unroll
-        for (int c = 0; c < CH; ++c) Lsum += lk[c];
-        continue;
-      }
-      const float fo = M == kNegInf ? 0.f : fast_exp2(M - cm);
-      Lsum *= fo;
-#pragma unroll
-      for (int i = 0; i < NE; ++i) acc[i] *= fo;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const float wgt = mk[c] == kNegInf ? 0.f : fast_exp2(mk[c] - cm);
-        Lsum = fmaf(wgt, lk[c], Lsum);
-#pragma unroll
-        for (int i = 0; i < NE; ++i) acc[i] = fmaf(wgt, ok[c][i], acc[i]);
-      }
-      M = cm;
-    }
+    merge_pieces<D, CH>(p, wf, n_u, U0, ppw, rr, lane, M, Lsum, acc);
     if (p.lse != nullptr && lane == 0) p.lse[orow] = row_lse(M, Lsum);
     float* dst = p.out + (int64_t)s * p.out_stride + (int64_t)(h * p.G + 8 * ht + rr) * D;
 #pragma unroll
     for (int i = 0; i < NE; ++i) dst[lane + 32 * i] = Lsum > 0.f ? acc[i] / Lsum : 0.f;
+  }
+}
+
+// The same for differential attention: a warp takes both rows of a head and writes its
+// normed difference.
+template <int D, int CH>
+__global__ void __launch_bounds__(kMergeThreads) kvq_diff_merge_kernel(const DecodeParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float kNegInf = __int_as_float(0xff800000u);
+  constexpr int NW = kMergeThreads / 32;
+  constexpr int NE = D / 32;   // output elements per lane
+  const int lane = threadIdx.x & 31;
+  const int U = p.pool.Hkv * p.n_ht;
+  const int* PS = p.ps;
+  const int Ttot = __ldcg(PS + p.S);
+  const int nwarps = p.grid * kDecodeWarps;
+  const int ppw = p.ppw_fixed > 0 ? p.ppw_fixed : (Ttot + nwarps - 1) / nwarps;
+  if (ppw <= 0) return;
+  const int hpu = min(kPartRows, p.G) / 2;  // heads of a tile
+  const int64_t ntasks = (int64_t)p.S * U * hpu;
+  for (int64_t task = (int64_t)blockIdx.x * NW + (threadIdx.x >> 5); task < ntasks;
+       task += (int64_t)gridDim.x * NW) {
+    const int64_t u = task / hpu;
+    const int i = (int)(task % hpu);
+    const int s = (int)(u / U), lu = (int)(u % U);
+    const int ht = lu % p.n_ht;
+    if (2 * i >= min(8, p.G - 8 * ht)) continue;
+    const int ps0 = __ldcg(PS + s), ps1 = __ldcg(PS + s + 1);
+    const int Ps = (ps1 - ps0) / U;
+    if (Ps == 0) continue;
+    const int U0 = ps0 + lu * Ps;
+    const int wf = U0 / ppw, wl = (U0 + Ps - 1) / ppw;
+    if (wf == wl) continue;  // written directly by its warp
+    const int head = lu / p.n_ht * (p.G / 2) + 4 * ht + i;
+    float y[NE];
+    const float lam = p.diff.lambda[head];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float M = kNegInf, Lsum = 0.f, acc[NE];
+#pragma unroll
+      for (int e = 0; e < NE; ++e) acc[e] = 0.f;
+      merge_pieces<D, CH>(p, wf, wl - wf + 1, U0, ppw, 2 * i + r, lane, M, Lsum, acc);
+      const float f = Lsum > 0.f ? (r == 0 ? 1.f : -lam) / Lsum : 0.f;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) y[e] = r == 0 ? acc[e] * f : fmaf(acc[e], f, y[e]);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float f = diff_factor<D>(p.diff, ss);
+    __half* dst = p.diff.out + ((int64_t)s * (p.Hq / 2) + head) * D;
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      const int d = lane + 32 * e;
+      dst[d] = __float2half_rn(y[e] * (p.diff.weight != nullptr ? f * p.diff.weight[d] : f));
+    }
   }
 }
 
@@ -1354,10 +1468,32 @@ struct DecodeLaunch {
   bool two_ctas = false;  // planned for two CTAs per SM (per-block formats)
 };
 
+// The merge of a decode's pieces, as its programmatic dependent.
+template <int D, bool DIFF>
+cudaError_t run_merge(const DecodeLaunch& l) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(l.merge_grid);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  cfg.stream = l.st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if constexpr (DIFF)
+    return phase_mark(l.st, l.merge_chunk == 16
+                                ? cudaLaunchKernelEx(&cfg, kvq_diff_merge_kernel<D, 16>, l.p)
+                                : cudaLaunchKernelEx(&cfg, kvq_diff_merge_kernel<D, 8>, l.p));
+  return phase_mark(l.st, l.merge_chunk == 16
+                              ? cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, 16>, l.p)
+                              : cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, 8>, l.p));
+}
+
 // CTAS: resident CTAs per SM the kernel is compiled for.
-template <int FMT, int D, int NG, bool BS8 = false, int CTAS = kDecodeCtasPerSm>
+template <int FMT, int D, int NG, bool BS8 = false, int CTAS = kDecodeCtasPerSm, bool DIFF = false>
 cudaError_t run_decode(const DecodeLaunch& l) {
-  cudaError_t e = allow_big_smem<kvq_decode_kernel<FMT, D, NG, BS8, CTAS>>();
+  cudaError_t e = allow_big_smem<kvq_decode_kernel<FMT, D, NG, BS8, CTAS, DIFF>>();
   if (e != cudaSuccess) return e;
   {
     cudaLaunchConfig_t dc = {};
@@ -1370,49 +1506,37 @@ cudaError_t run_decode(const DecodeLaunch& l) {
     da[0].val.programmaticStreamSerializationAllowed = 1;
     dc.attrs = da;
     dc.numAttrs = l.dependent ? 1 : 0;
-    e = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode_kernel<FMT, D, NG, BS8, CTAS>, l.p));
+    e = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode_kernel<FMT, D, NG, BS8, CTAS, DIFF>, l.p));
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(l.merge_grid);
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = l.st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return phase_mark(l.st, l.merge_chunk == 16
-                              ? cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, 16>, l.p)
-                              : cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, 8>, l.p));
+  return run_merge<D, DIFF>(l);
 }
 
-template <int FMT, bool BS8 = false>
+template <int FMT, bool BS8 = false, bool DIFF = false>
 cudaError_t run_decode_d(const DecodeLaunch& l) {
   switch (l.p.pool.D) {
-    case 64: return run_decode<FMT, 64, 1, BS8>(l);
-    case 128: return run_decode<FMT, 128, 1, BS8>(l);
+    case 64: return run_decode<FMT, 64, 1, BS8, kDecodeCtasPerSm, DIFF>(l);
+    case 128: return run_decode<FMT, 128, 1, BS8, kDecodeCtasPerSm, DIFF>(l);
     default: return cudaErrorInvalidValue;
   }
 }
 
 // Per-group formats: NG = head_dim / group scale groups per head.
-template <int FMT, bool BS8 = false>
+template <int FMT, bool BS8 = false, bool DIFF = false>
 cudaError_t run_decode_group(const DecodeLaunch& l) {
   const int D = l.p.pool.D, ng = l.p.pool.ng;
   if (D == 64) {
     switch (ng) {
-      case 1: return run_decode<FMT, 64, 1, BS8>(l);
-      case 2: return run_decode<FMT, 64, 2, BS8>(l);
-      case 4: return run_decode<FMT, 64, 4, BS8>(l);
+      case 1: return run_decode<FMT, 64, 1, BS8, kDecodeCtasPerSm, DIFF>(l);
+      case 2: return run_decode<FMT, 64, 2, BS8, kDecodeCtasPerSm, DIFF>(l);
+      case 4: return run_decode<FMT, 64, 4, BS8, kDecodeCtasPerSm, DIFF>(l);
     }
   } else if (D == 128) {
     switch (ng) {
-      case 1: return run_decode<FMT, 128, 1, BS8>(l);
-      case 2: return run_decode<FMT, 128, 2, BS8>(l);
-      case 4: return run_decode<FMT, 128, 4, BS8>(l);
-      case 8: return run_decode<FMT, 128, 8, BS8>(l);
+      case 1: return run_decode<FMT, 128, 1, BS8, kDecodeCtasPerSm, DIFF>(l);
+      case 2: return run_decode<FMT, 128, 2, BS8, kDecodeCtasPerSm, DIFF>(l);
+      case 4: return run_decode<FMT, 128, 4, BS8, kDecodeCtasPerSm, DIFF>(l);
+      case 8: return run_decode<FMT, 128, 8, BS8, kDecodeCtasPerSm, DIFF>(l);
     }
   }
   return cudaErrorInvalidValue;

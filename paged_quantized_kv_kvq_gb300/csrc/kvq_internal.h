@@ -136,6 +136,19 @@ struct DecodePlan {
 bool plan_decode(const PoolView& pool, int S, int Hq, int max_ctx, int split_blocks, int sms,
                  DecodePlan* plan);
 
+// Differential attention: the two halves of a head's channels are two maps over one V,
+//   y = softmax(s q1.k1) V - lambda softmax(s q2.k2) V,
+//   out = out_scale * y / sqrt(mean(y^2) + eps) * weight  (no norm without a weight).
+// To the kernels a head is two Q rows, 2i and 2i + 1 of its group, each q with the other
+// half zero: what the heads of a group share -- the page, its conversion, the products'
+// n dimension -- the maps share too.
+struct DiffOut {
+  const float* lambda = nullptr;  // [heads]
+  const float* weight = nullptr;  // [D] or null
+  __half* out = nullptr;          // [rows][heads][D]
+  float eps = 0.f, out_scale = 1.f;
+};
+
 struct DecodeArgs {
   PoolView pool;
   const __half* q;
@@ -151,6 +164,7 @@ struct DecodeArgs {
   const float* pre = nullptr;
   int64_t q_stride = 0, out_stride = 0;  // elements between sequences' rows; 0 = Hq * D
   float* lse = nullptr;  // [S][Hq] log of the softmax denominators; null = not wanted
+  DiffOut diff;          // differential attention (Hq counts both maps) if diff.lambda is set
   int wait_tries = kWaitTries;  // bound of each pipeline wait, in ~1 ms tries
   int fault_issue = -1;   // self-test only: withhold warp 0's copy of this index
 };
@@ -204,6 +218,43 @@ cudaError_t launch_prefill_ws(const PoolView& pool, const __half* q, int S, int 
                               const int* lens, int max_ctx, float sm_scale, float* out, void* ws,
                               cudaStream_t st);
 
+// Differential attention of prompts (kvq_diff.cu); T rows of q and out, H heads.
+size_t diff_prefill_ws_bytes(const PoolView& pool, int64_t T, int S, int H, int max_ctx);
+cudaError_t launch_diff_prefill(const PoolView& pool, const __half* q, int64_t T, int S, int H,
+                                const int* q_start, int max_q_len, const int* table, int max_blocks,
+                                const int* lens, int max_ctx, float sm_scale, const DiffOut& diff,
+                                void* ws, cudaStream_t st);
+
+// Block tables, slot map and positions of a step (kvq_blocks.cu).
+struct ExtendArgs {
+  const int* n;     // [S] new tokens
+  const int* lens;  // [S]
+  int* table;       // [S][max_blocks]
+  const int* free_list;
+  const int* count;
+  int* lens_out;
+  int* count_out;
+  int* q_start;        // [S + 1]
+  int64_t* slots;      // [max_tokens]
+  int64_t* positions;  // [max_tokens]
+  int* err;
+  int64_t num_blocks;
+  int S, max_blocks, capacity, max_tokens, bs;
+};
+cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st);
+struct ReleaseArgs {
+  const int* table;
+  const int* old_lens;
+  const int* new_lens;
+  int* free_list;
+  const int* count;
+  int* count_out;
+  int* err;
+  int64_t num_blocks;
+  int S, max_blocks, capacity, shared, bs;
+};
+cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t st);
+
 // Per-format kernel launchers (one translation unit each, compiled in parallel).
 struct DecodeLaunch;
 cudaError_t launch_decode_int8_group(const DecodeLaunch& l);
@@ -215,6 +266,7 @@ cudaError_t launch_decode_e5m2(const DecodeLaunch& l);
 cudaError_t launch_decode_bs8_group(const DecodeLaunch& l);  // block size 8, INT8 per-group
 cudaError_t launch_decode_bs8_misc(const DecodeLaunch& l);   // block size 8, the other formats
 cudaError_t launch_decode_fp4(const DecodeLaunch& l);
+cudaError_t launch_decode_diff(const DecodeLaunch& l);  // differential, every format
 cudaError_t launch_decode_block(const DecodeLaunch& l);      // one scale per block, every block size
 
 }  // namespace kvq
