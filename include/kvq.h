@@ -360,7 +360,8 @@ kvq_status kvq_paged_decode(const kvq_pool* pool, const kvq_half* q, int num_seq
 
 /* As kvq_paged_decode, with an explicit split of each sequence's blocks across
  * thread blocks: split_blocks > 0 forces that many blocks per split (split-K
- * over the context, merged by log-sum-exp); 0 picks automatically. */
+ * over the context, merged by log-sum-exp; rounded up to 64 tokens for
+ * KVQ_FP4_E2M1); 0 picks automatically. */
 size_t kvq_decode_workspace_bytes_ex(const kvq_pool* pool, int num_seqs, int num_q_heads,
                                      int max_context_len, int split_blocks);
 kvq_status kvq_paged_decode_ex(const kvq_pool* pool, const kvq_half* q, int num_seqs,

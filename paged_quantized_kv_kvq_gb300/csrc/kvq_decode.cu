@@ -3,7 +3,7 @@
 // dispatch.
 #include <algorithm>
 
-#include "kvq_decode_impl.cuh"
+#include "kvq_decode4_impl.cuh"
 #include "kvq_internal.h"
 
 namespace kvq {
@@ -18,11 +18,17 @@ size_t round_up_sz(size_t x, size_t m) { return (x + m - 1) / m * m; }
 bool plan_decode(const PoolView& pool, int S, int Hq, int max_ctx, int split_blocks, int sms,
                  DecodePlan* plan) {
   constexpr int W = kDecodeWarps;
+  // Pools of 4-bit floats: stages of kDecode4Span tokens take the place of pages in all
+  // that follows (two of 9 KB a warp at head_dim 128 keep 220 KB in flight on an SM).
+  const bool fp4 = pool.fmt == FMT_FP4;
+  const int span = fp4 ? kDecode4Span : pool.bs;
+  if (fp4) split_blocks = static_cast<int>(((int64_t)split_blocks * pool.bs + span - 1) / span);
   const bool tok = pool.fmt == FMT_INT8_TOKEN || pool.fmt == FMT_FP8_TOKEN;
   // Block size 8: a stage holds a pair of pages (two page slots) completing
   // on one barrier.
   const int sps = pool.bs == 8 ? 2 : 1;
-  const int stage_bytes = sps * round_up(pool.page_bytes + (tok ? 2 * pool.bs * 4 : 0), 128);
+  const int stage_bytes = fp4 ? span / pool.bs * pool.page_bytes
+                              : sps * round_up(pool.page_bytes + (tok ? 2 * pool.bs * 4 : 0), 128);
   // Pages in flight per SM = CTAs per SM x W x stages; 3 CTAs x 4 warps x 4
   // stages keeps ~200 KB of copies in flight, above what HBM latency needs.
   // Block size 8 consumes up to four pages (three pairs) per update, so keeps
@@ -53,7 +59,7 @@ bool plan_decode(const PoolView& pool, int S, int Hq, int max_ctx, int split_blo
   const int n_ht = (G + 7) / 8;
   const int ctas_per_sm = std::max(1, std::min(kDecodeCtasPerSm, (228 * 1024) / (smem + 1024)));
   const int64_t units = (int64_t)S * pool.Hkv * n_ht;
-  const int64_t max_pages = (std::max(max_ctx, 0) + pool.bs - 1) / pool.bs;
+  const int64_t max_pages = ((int64_t)std::max(max_ctx, 0) + span - 1) / span;
   const int64_t tmax = std::max<int64_t>(units * max_pages, 1);
   int64_t grid;
   int ppw_fixed = 0;

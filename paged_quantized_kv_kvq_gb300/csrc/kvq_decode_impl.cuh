@@ -264,7 +264,6 @@ struct PairRegs {
   float ks[2][2][NS];  // [tile][row g | g+8][group]
   float vs[2][2][NS];
   const char* vtile[2];  // V codes in shared memory
-  const char* vsc[2];    // 4-bit floats: their scales
   const char* vtile_b[2];  // block size 8: V codes of the tile's second page (or null)
   int rows[2];
 };
@@ -276,13 +275,7 @@ __device__ __forceinline__ void load_tile(PairRegs<FMT, D, NG>& r, int t, const 
   using T = FmtTraits<FMT>;
   constexpr int NS = PairRegs<FMT, D, NG>::NS;
   const int g = lane >> 2;
-  if constexpr (FMT == FMT_FP4) {
-    const char* sc = stage + 2 * pool.code_bytes + sub * D;
-    fp4_load_k<D>(stage + sub * pool.sub_bytes, sc, lane, r.kw[t]);
-    r.vsc[t] = sc + pool.bs * (D / 16);
-  } else {
-    load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, r.kw[t]);
-  }
+  load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, r.kw[t]);
   r.vtile[t] = stage + pool.code_bytes + sub * pool.sub_bytes;
   if constexpr (T::block_scales) {
     const float2 sc = *reinterpret_cast<const float2*>(stage + 2 * pool.code_bytes);
@@ -558,8 +551,6 @@ __device__ __forceinline__ void compute_pair(PairRegs<FMT, D, NG>& r, int lane,
     for (int t = 0; t < 2; ++t) {
       if constexpr (BS8)
         load_v8<FMT, D>(r.vtile[t], r.vtile_b[t], lane, vwp[t]);
-      else if constexpr (FMT == FMT_FP4)
-        fp4_load_v<D>(r.vtile[t], r.vsc[t], lane, r.rows[t], vwp[t]);
       else
         load_lane_words<FMT, D>(r.vtile[t], lane, vwp[t]);
     }

@@ -62,10 +62,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 cudaError_t launch_diff_block(const DecodeLaunch& l);  // kvq_diff_decode.cu
 cudaError_t launch_diff_misc(const DecodeLaunch& l);
 cudaError_t launch_diff_group(const DecodeLaunch& l);  // kvq_diff_decode_group.cu
+cudaError_t launch_diff_fp4(const DecodeLaunch& l);    // kvq_decode_fp4.cu
 
 cudaError_t launch_decode_diff(const DecodeLaunch& l) {
   const int f = l.p.pool.fmt;
   if (fmt_block(f)) return launch_diff_block(l);
+  if (f == FMT_FP4) return launch_diff_fp4(l);
   return f == FMT_INT8_GROUP || f == FMT_INT4_GROUP ? launch_diff_group(l) : launch_diff_misc(l);
 }
 

@@ -33,7 +33,6 @@ cudaError_t launch_diff_misc(const DecodeLaunch& l) {
     case FMT_FP8_TOKEN: return run_any<FMT_FP8_TOKEN>(l);
     case FMT_INT8_CHANNEL: return run_any<FMT_INT8_CHANNEL>(l);
     case FMT_FP8_E5M2: return run_any<FMT_FP8_E5M2>(l);
-    case FMT_FP4: return run_decode_d<FMT_FP4, false, true>(l);
   }
   return cudaErrorInvalidValue;
 }

@@ -448,3 +448,27 @@ def test_blocks_beyond_four_gigabytes():
     from cache_ops_ref import attention
     _near(out.cpu().numpy(), attention(lambda s: np.stack([kv, vv], 1)[:61], q, [61])[0])
     pool.close()
+
+
+@pytest.mark.parametrize("hq", [4, 8])
+def test_long_range_in_one_warp_does_not_drift(hq):
+    """24000 tokens summed by one warp: the sum stays in fp32 adds."""
+    pool, ref, table, lens, rng = _filled(16, 1, 128, [24000], seed=5)
+    q = rng.standard_normal((1, hq, 128)).astype(np.float16)
+    out = pool.decode(_t(q), _t(table), _t(lens), 24000, split_blocks=1500)
+    _near(out.cpu().numpy(), ref.decode(q, table, lens))
+    pool.close()
+
+
+def test_a_wait_that_runs_out():
+    """A page copy that never comes: flagged, the next decode is right."""
+    pool, ref, table, lens, rng = _filled(16, 2, 128, [300, 70], seed=7)
+    q = rng.standard_normal((2, 8, 128)).astype(np.float16)
+    ws = torch.empty(kvq.kvq_decode_workspace_bytes(pool.handle, 2, 8, 300), dtype=torch.uint8, device=DEV)
+    out = torch.empty((2, 8, 128), device=DEV)
+    kvq.kvq_selftest_decode_timeout(pool.handle, _t(q), _t(table), _t(lens), 300, out, ws, wait_tries=5)
+    assert pool.error() == kvq.KVQ_ERR_TIMEOUT
+    kvq.kvq_paged_decode(pool.handle, _t(q), _t(table), _t(lens), 300, 128 ** -0.5, out, ws)
+    assert pool.error() == kvq.KVQ_OK
+    _near(out.cpu().numpy(), ref.decode(q, table, lens))
+    pool.close()
