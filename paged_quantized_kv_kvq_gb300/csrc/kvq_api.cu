@@ -107,6 +107,7 @@ kvq_status layout_for(int64_t num_blocks, int bs, int Hkv, int D, int dtype, int
     view->sub_bytes = sub_bytes;
     view->code_bytes = static_cast<int>(code_bytes);
     view->page_bytes = static_cast<int>(page_bytes);
+    view->v_off = static_cast<int>(dtype == KVQ_FP4_E2M1 ? page_bytes / 2 : code_bytes);
   }
   if (off_pages) *off_pages = op;
   if (off_tok) *off_tok = ot;

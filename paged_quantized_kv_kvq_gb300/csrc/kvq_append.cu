@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kAppendThreads) kvq_append_kernel(const Append
     const bool act = c < per;
     const int h = act ? c / D : 0, d0 = act ? c - h * D : 0;
     char* page = pool.pages + (blk * Hkv + h) * pool.page_bytes;
-    char* tile = page + (kv == 0 ? 0 : pool.code_bytes) + sub * pool.sub_bytes;
+    char* tile = page + (kv == 0 ? 0 : pool.v_off) + sub * pool.sub_bytes;
     uint4 raw = base == 0 ? raw0 : act ? *reinterpret_cast<const uint4*>(x + c) : make_uint4(0, 0, 0, 0);
     const __half2(&xv)[4] = *reinterpret_cast<const __half2(*)[4]>(&raw);
     float f[8];
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kAppendThreads) kvq_append_kernel(const Append
       if (!act) continue;
       if ((d0 & 15) == 0) {
         const int gi = d0 >> 4, ng = pool.ng;
-        page[2 * pool.code_bytes + kv * pool.bs * ng + sub * 16 * ng +
+        page[(kv == 0 ? 0 : pool.v_off) + pool.code_bytes + sub * D +
              (kv == 0 ? fp4_k_scale(tt, gi, ng) : fp4_v_scale(tt, gi, ng))] = static_cast<char>(sc);
       }
       store_fp4x8<false>(tile, kv, tt, d0, codes);
@@ -264,7 +264,7 @@ __global__ void kvq_read_slots_kernel(PoolView pool, const int64_t* slots, int64
   for (int c = threadIdx.x; c < per; c += blockDim.x) {
     const int h = c / D, d = c - h * D;
     const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
-    const char* tile = page + (kv == 0 ? 0 : pool.code_bytes) + sub * pool.sub_bytes;
+    const char* tile = page + (kv == 0 ? 0 : pool.v_off) + sub * pool.sub_bytes;
     const int64_t dst = (i * 2 + kv) * per + c;
     if (pool.fmt == FMT_INT4_GROUP) {  // biased nibble -> signed code
       int sh;
@@ -304,7 +304,7 @@ __global__ void kvq_read_slots_kernel(PoolView pool, const int64_t* slots, int64
       const int h = c / ng, gi = c - h * ng;
       const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
       scales_out[(i * 2 + kv) * ns + c] = fp4_scale_value(static_cast<uint8_t>(
-          page[2 * pool.code_bytes + kv * pool.bs * ng + sub * 16 * ng +
+          page[(kv == 0 ? 0 : pool.v_off) + pool.code_bytes + sub * D +
                (kv == 0 ? fp4_k_scale(tt, gi, ng) : fp4_v_scale(tt, gi, ng))]));
     }
   } else if (fmt_block(pool.fmt)) {  // the scale of the slot's block, per head

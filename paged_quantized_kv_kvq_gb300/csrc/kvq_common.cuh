@@ -18,8 +18,8 @@
 //                   K scales: [block_size][D/group] fp32   (per-group only)
 //                   V scales: [block_size][D/group] fp32   (per-group only)
 //                   K scale, V scale fp32, 8 B padding     (per-block only)
-//                   K scales: [block_size][D/16] bytes     (4-bit floats only)
-//                   V scales: [block_size][D/16] bytes     (4-bit floats only)
+//                   (4-bit floats: K codes, [block_size][D/16] scale bytes, V codes,
+//                   as many scale bytes)
 //   token scales: [num_blocks][2][block_size] fp32         (per-token only)
 //   chan scales : [2][kv_heads][D] fp32                    (per-channel only)
 //
@@ -154,6 +154,7 @@ struct PoolView {
   int sub_bytes;    // bytes of one 16-token sub-tile: 16 * D * esize (4-bit codes: 8 * D)
   int code_bytes;   // bytes of K (or V) codes in one page = bs * sub_bytes / 16
                     // (block size 8: half a sub-tile)
+  int v_off;        // where the V codes of a page begin: code_bytes (4-bit floats: page_bytes / 2)
   int page_bytes;   // 2*code_bytes + (per-group) 2*bs*ng*4, (per-block) 16 or (4-bit floats) 2*bs*ng
 };
 

@@ -57,6 +57,7 @@ bool plan_decode(const PoolView& pool, int S, int Hq, int max_ctx, int split_blo
   if (smem > 227 * 1024) return false;
   const int G = Hq / pool.Hkv;
   const int n_ht = (G + 7) / 8;
+  plan->part_rows = fp4 && decode4_dup(G) ? 4 : kPartRows;
   const int ctas_per_sm = std::max(1, std::min(kDecodeCtasPerSm, (228 * 1024) / (smem + 1024)));
   const int64_t units = (int64_t)S * pool.Hkv * n_ht;
   const int64_t max_pages = ((int64_t)std::max(max_ctx, 0) + span - 1) / span;
@@ -94,7 +95,7 @@ bool plan_decode(const PoolView& pool, int S, int Hq, int max_ctx, int split_blo
   const int64_t tok_per_warp = (int64_t)units * std::max(max_ctx, 0) / std::max<int64_t>(warps_total, 1);
   plan->merge_chunk = tok_per_warp >= 1024 ? 16 : 8;
   plan->ws_bytes = plan->ps_bytes +
-                   (size_t)grid * W * 2 * kPartRows * (pool.D + 2) * sizeof(float);
+                   (size_t)grid * W * 2 * plan->part_rows * (pool.D + 2) * sizeof(float);
   return true;
 }
 
@@ -120,6 +121,9 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
   p.ppw_fixed = plan.ppw_fixed;
   p.nstage = plan.nstage;
   p.stage_bytes = plan.stage_bytes;
+  p.part_rows = plan.part_rows;
+  p.span = a.pool.fmt == FMT_FP4 ? kDecode4Span : a.pool.bs;
+  p.inputs_early = dependent;
   p.grid = plan.grid;
   p.sm_scale_log2 = a.sm_scale * 1.4426950408889634f;
   p.skip = a.skip;

@@ -19,8 +19,8 @@
 //    take the same heads once more: their lanes carry the low parts of the weights
 //    (p - fp16(p)) where the others carry the high parts, so that one product does what
 //    two did.
-// The range of a warp, the partials and the merge are as in the general kernel with
-// steps in the place of pages, so that kernel's merge serves.
+// The range of a warp and the partials are as in the general kernel with
+// steps in the place of pages; kvq_join_kernel joins them.
 #pragma once
 #include "kvq_decode_impl.cuh"
 
@@ -28,7 +28,16 @@ namespace kvq {
 
 constexpr int kDecode4Span = 64;   // tokens of a step
 constexpr int kDecode4Ctas = 3;    // resident per SM
+// Rows of a head tile that fit 4 columns take the DUP kernel.
+constexpr bool decode4_dup(int G) { return G <= 4; }
 constexpr float kDecode4Exp = 14;  // weights are 2^14 p, so that their low parts stay normal fp16
+
+// fp16 pair of (a, b), or with less = -1 of what that pair leaves of them.
+__device__ __forceinline__ uint32_t part_h2(float a, float b, float less) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const __half2 r = __floats2half2_rn(fmaf(__low2float(h), less, a), fmaf(__high2float(h), less, b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 template <int D, bool DUP, bool DIFF>
 __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
@@ -45,11 +54,17 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
   const int sps = kDecode4Span >> bl;  // pages per step
   const int U = pool.Hkv * p.n_ht;     // units per sequence
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the merge waits for this grid)
-
   char* stages = smem + warp * nstage * p.stage_bytes;
   uint64_t* bars_base = reinterpret_cast<uint64_t*>(smem + kDecodeWarps * nstage * p.stage_bytes);
   uint64_t* bars = bars_base + warp * nstage;
+  if (lane < nstage) mbar_init(&bars[lane], 1);
+  fence_barrier_init();
+  // Launched while the kernel before it ends; only the decode step's append vouches for
+  // the lengths and the table.
+  if (!p.inputs_early) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The join may launch now: it waits for this grid, but reads the lengths before that.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   int* there_base = reinterpret_cast<int*>(bars_base + kDecodeWarps * nstage);
   int* there_at = there_base + warp * nstage;  // pages of each stage that are in the pool, a bit each
   int* wtot = there_base + kDecodeWarps * nstage;  // [kDecodeWarps]
@@ -150,38 +165,44 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
     c.Ps = c.s < p.S ? (PS[c.s + 1] - PS[c.s]) / U : 1;
   };
 
-  // ---- pages on their way: a lane looks after one page of each batch of 32, its table
-  // entry looked up a batch ahead
+  // ---- pages on their way: a lane looks after one page of each batch of 32.  Its table
+  // entry is asked for a batch ahead and looked at when the batch begins, so that no
+  // copy waits for it.
+  struct Entry {
+    int block, h;  // kv head; -1: behind the sequence
+    bool last;     // of the sequence's last step
+  };
   struct Page {
-    const char* at;  // null: behind the sequence, or outside the pool
-    bool last;       // of the sequence's last step
+    const char* at;  // null: nothing to copy
+    bool last;
   };
   const int batch = 32 / sps;  // steps of a batch
   auto look_up = [&](int n0) {
-    Page q{nullptr, false};
+    Entry q{0, -1, false};
     const int n = n0 + lane / sps;
     if (n < n_w) {
       const Cursor4 c = locate(a0 + n);
       const int pg = c.i * sps + lane % sps;
       q.last = c.i + 1 == c.Ps;
       if (pg << bl < tokens_of(c.s)) {
-        const int e = p.table[(int64_t)c.s * p.max_blocks + p.skip + pg];
-        if (e >= 0 && (int64_t)e < pool.num_blocks)
-          q.at = pool.pages + ((int64_t)e * pool.Hkv + c.lu / p.n_ht) * pool.page_bytes;
-        else
-          set_error(pool.err, ERR_RANGE);
+        q.block = p.table[(int64_t)c.s * p.max_blocks + p.skip + pg];
+        q.h = c.lu / p.n_ht;
       }
     }
     return q;
   };
-  if (lane < nstage) mbar_init(&bars[lane], 1);
-  fence_barrier_init();
-  __syncwarp();
-  Page now = look_up(0), next = look_up(batch);
+  auto page_of = [&](const Entry& q) {
+    const bool in = q.block >= 0 && (int64_t)q.block < pool.num_blocks;
+    if (q.h >= 0 && !in) set_error(pool.err, ERR_RANGE);
+    return Page{q.h >= 0 && in ? pool.pages + ((int64_t)q.block * pool.Hkv + q.h) * pool.page_bytes : nullptr,
+                q.last};
+  };
+  Page now = page_of(look_up(0));
+  Entry next = look_up(batch);
   int base = 0;  // first step of `now`'s batch
   auto issue = [&](int n, int st) {  // all lanes: step n of the range into stage st
     if (n - base == batch) {
-      now = next;
+      now = page_of(next);
       base = n;
       next = look_up(n + batch);
     }
@@ -218,12 +239,15 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
   for (int t = 0; t < 4; ++t) {
     const int k = 16 * t >> bl, sub = (16 * t & (pool.bs - 1)) >> 4;
     tile_at[t] = k * pool.page_bytes + sub * pool.sub_bytes;
-    scale_at[t] = k * pool.page_bytes + 2 * pool.code_bytes + sub * D;
+    scale_at[t] = k * pool.page_bytes + pool.code_bytes + sub * D;
   }
-  const int v_tile = pool.code_bytes, v_scale = pool.bs * NG;
+  const int v_off = pool.v_off;
 
-  // ---- the unit being attended: columns 2j, 2j+1 are this lane's
+  // ---- the unit being attended: columns 2j, 2j+1 are this lane's.  The scale is kept
+  // positive (its sign goes to q; zero is a zero q), so that it leaves the order of scores.
+  const float csc0 = p.sm_scale_log2, csc = csc0 == 0.f ? 1.f : fabsf(csc0);
   uint32_t qb[KS][2];
+  const float less = DUP && j >= 2 ? -1.f : 0.f;  // these lanes carry low parts
   float m[2], l[2], o[KS][4];
   Cursor4 cc = locate(a0);
   const Cursor4 first = cc;
@@ -237,10 +261,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
       // a map has its half of the channels
-      const bool has = row < Gt && (!DIFF || (kk >= KS / 2) == ((hq & 1) != 0));
+      const bool has = row < Gt && csc0 != 0.f && (!DIFF || (kk >= KS / 2) == ((hq & 1) != 0));
       const uint2 v = has ? *reinterpret_cast<const uint2*>(qp + 16 * kk) : make_uint2(0, 0);
-      qb[kk][0] = v.x;
-      qb[kk][1] = v.y;
+      qb[kk][0] = csc0 < 0.f ? v.x ^ 0x80008000u : v.x;
+      qb[kk][1] = csc0 < 0.f ? v.y ^ 0x80008000u : v.y;
     }
     m[0] = m[1] = kNegInf;
     l[0] = l[1] = 0.f;
@@ -323,7 +347,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
       return;
     }
     const int slot = (u.s == first.s && u.lu == first.lu) ? 0 : 1;
-    float* pbase = p.part + ((int64_t)gw * 2 + slot) * kPartRows * (D + 2);
+    float* pbase = p.part + ((int64_t)gw * 2 + slot) * p.part_rows * (D + 2);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       if (!(c ? v1 : v0)) continue;
@@ -341,7 +365,6 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
   };
 
   start_unit();
-  const float csc = p.sm_scale_log2;
   int st = 0;
   uint32_t phase = 0;
   bool failed = false;
@@ -396,7 +419,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
         }
       }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[t][e] = (acc[0][e] + acc[1][e]) * csc;
+      for (int e = 0; e < 4; ++e) z[t][e] = acc[0][e] + acc[1][e];
     }
     uint32_t keep[4][2];  // bits of the V scales that count: tokens 2j, 2j+1 | 2j+8, 2j+9
 #pragma unroll
@@ -422,7 +445,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
       for (int c = 0; c < 2; ++c) {
         float t = fmaxf(fmaxf(fmaxf(z[0][c], z[0][2 + c]), fmaxf(z[1][c], z[1][2 + c])),
                         fmaxf(fmaxf(z[2][c], z[2][2 + c]), fmaxf(z[3][c], z[3][2 + c])));
-        const float mn = fmaxf(m[c], warp_max_over_rows(t));
+        const float mn = fmaxf(m[c], warp_max_over_rows(t) * csc);
         const float ms = mn == kNegInf ? 0.f : mn;
         al[c] = fast_exp2(m[c] - ms);
         m[c] = mn;
@@ -432,16 +455,19 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[t][e] = fast_exp2(z[t][e] - mb[e & 1]);
+        for (int e = 0; e < 4; ++e) z[t][e] = fast_exp2(fmaf(z[t][e], csc, -mb[e & 1]));
         add[0] += z[t][0] + z[t][2];
         add[1] += z[t][1] + z[t][3];
-        uint32_t hA, lA, hB, lB;
-        split_h2(z[t][0], z[t][1], hA, lA);
-        split_h2(z[t][2], z[t][3], hB, lB);
         if constexpr (DUP) {
+          uint32_t hA, lA, hB, lB;
+          split_h2(z[t][0], z[t][1], hA, lA);
+          split_h2(z[t][2], z[t][3], hB, lB);
           pb[t][0][0] = movmatrix_t(j < 2 ? hA : lA);
           pb[t][0][1] = movmatrix_t(j < 2 ? hB : lB);
         } else {
+          uint32_t hA, lA, hB, lB;
+          split_h2(z[t][0], z[t][1], hA, lA);
+          split_h2(z[t][2], z[t][3], hB, lB);
           pb[t][0][0] = movmatrix_t(hA);
           pb[t][0][1] = movmatrix_t(hB);
           pb[t][NL - 1][0] = movmatrix_t(lA);
@@ -458,8 +484,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
       float acc[4][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint4 v = *reinterpret_cast<const uint4*>(stage + tile_at[t] + v_tile + lane * 16 + c * 512);
-        const uint4 q = *reinterpret_cast<const uint4*>(stage + scale_at[t] + v_scale + j * 4 * NG + 16 * c);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + tile_at[t] + v_off + lane * 16 + c * 512);
+        const uint4 q = *reinterpret_cast<const uint4*>(stage + scale_at[t] + v_off + j * 4 * NG + 16 * c);
         const uint32_t w[4] = {v.x, v.y, v.z, v.w}, sw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -493,8 +519,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
     // flag it, leave empty partials for the merge, wait (bounded again) for the copies
     // still in flight so that none lands after the CTA has exited
     if (lane == 0) set_error(pool.err, ERR_TIMEOUT);
-    if (lane < 2 * kPartRows) {
-      float* r = p.part + ((int64_t)gw * 2 * kPartRows + lane) * (D + 2);
+    if (lane < 2 * p.part_rows) {
+      float* r = p.part + ((int64_t)gw * 2 * p.part_rows + lane) * (D + 2);
       r[0] = kNegInf;
       r[1] = 0.f;
     }
@@ -522,14 +548,14 @@ cudaError_t run_decode4(const DecodeLaunch& l) {
   da[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   da[0].val.programmaticStreamSerializationAllowed = 1;
   dc.attrs = da;
-  dc.numAttrs = l.dependent ? 1 : 0;
+  dc.numAttrs = 1;
   const cudaError_t f = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode4_kernel<D, DUP, DIFF>, l.p));
-  return f != cudaSuccess ? f : run_merge<D, DIFF>(l);
+  return f != cudaSuccess ? f : run_join<D, DIFF>(l);
 }
 
 template <bool DIFF>
 cudaError_t run_decode4_any(const DecodeLaunch& l) {
-  const bool dup = l.p.G <= 4;
+  const bool dup = decode4_dup(l.p.G);
   if (l.p.pool.D == 64) return dup ? run_decode4<64, true, DIFF>(l) : run_decode4<64, false, DIFF>(l);
   return dup ? run_decode4<128, true, DIFF>(l) : run_decode4<128, false, DIFF>(l);
 }

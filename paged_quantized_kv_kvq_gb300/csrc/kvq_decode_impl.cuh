@@ -72,7 +72,10 @@ struct DecodeParams {
   float* out;          // [S][Hq][D], rows out_stride elements apart
   int64_t q_stride, out_stride;
   int* ps;             // [S + 1] page prefix over sequences (written by CTA 0 for the merge)
-  float* part;         // [warps][2][kPartRows][D + 2]: m, l, O of cut units
+  float* part;         // [warps][2][part_rows][D + 2]: m, l, O of cut units
+  int span;            // tokens that count as one page in ranges (4-bit floats: a step)
+  bool inputs_early;   // lengths and table may be read before griddepcontrol.wait
+  int part_rows;       // kPartRows, or fewer where the kernel holds fewer rows
   // Shared-prefix cascade: the first `skip` blocks of every sequence are the
   // shared prefix, already attended by the prefix kernel, whose partial rows
   // (m, l, O in true units) are in pre[S][Hq][D + 2]; skip = 0, pre = null
@@ -1292,7 +1295,7 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams& p, int wf, int 
       if (k < n_u) {
         const int w = wf + k;
         const int sl = (k == 0 && (int64_t)w * ppw < U0) ? 1 : 0;
-        const float* pr = p.part + (((int64_t)w * 2 + sl) * kPartRows + rr) * (D + 2);
+        const float* pr = p.part + (((int64_t)w * 2 + sl) * p.part_rows + rr) * (D + 2);
         mk[c] = __ldcg(pr);
         lk[c] = __ldcg(pr + 1);
 #pragma unroll
@@ -1389,61 +1392,133 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const DecodePa
   }
 }
 
-// The same for differential attention: a warp takes both rows of a head and writes its
-// normed difference.
-template <int D, int CH>
-__global__ void __launch_bounds__(kMergeThreads) kvq_diff_merge_kernel(const DecodeParams p) {
+// The merge of differential attention, and of pools of 4-bit floats: a warp takes a row,
+// or both rows of a differential head, whose normed difference it writes.  A merge is a
+// chain of round trips behind the last warp of the decode, so all that only takes
+// the lengths is done while the decode still runs: every CTA makes the prefix over the
+// sequences itself (up to kJoinSeqs; more are read from the workspace) and looks its first
+// unit up before griddepcontrol.wait; behind it one round trip brings the partials.
+constexpr int kJoinSeqs = 2048;
+
+template <int D, int CH, bool DIFF>
+__global__ void __launch_bounds__(kMergeThreads) kvq_join_kernel(const __grid_constant__ DecodeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float kNegInf = __int_as_float(0xff800000u);
   constexpr int NW = kMergeThreads / 32;
-  constexpr int NE = D / 32;   // output elements per lane
-  const int lane = threadIdx.x & 31;
+  constexpr int NE = D / 32;  // output elements per lane
+  constexpr int RPT = DIFF ? 2 : 1;
+  const float kNegInf = __int_as_float(0xff800000u);
+  extern __shared__ int join_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int U = p.pool.Hkv * p.n_ht;
+  const bool own = p.S <= kJoinSeqs;
   const int* PS = p.ps;
-  const int Ttot = __ldcg(PS + p.S);
+  if (own) {  // pages (steps) before each sequence, as the decode counts them
+    int* wtot = join_smem;  // [NW]
+    int* mine = join_smem + NW;
+    int carry = 0;
+    for (int base = 0; base < p.S; base += kMergeThreads) {
+      const int s = base + threadIdx.x;
+      int v = 0;
+      if (s < p.S) {
+        const int L = min(p.lens[s], p.max_ctx) - p.skip * p.pool.bs;
+        v = L > 0 ? (L + p.span - 1) / p.span * U : 0;
+      }
+      int x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) wtot[warp] = x;
+      __syncthreads();
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        before += w < warp ? wtot[w] : 0;
+        all += wtot[w];
+      }
+      if (s < p.S) mine[s + 1] = carry + before + x;
+      carry += all;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) mine[0] = 0;
+    __syncthreads();
+    PS = mine;
+  } else {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+  }
+  const int Ttot = PS[p.S];
   const int nwarps = p.grid * kDecodeWarps;
   const int ppw = p.ppw_fixed > 0 ? p.ppw_fixed : (Ttot + nwarps - 1) / nwarps;
-  if (ppw <= 0) return;
-  const int hpu = min(kPartRows, p.G) / 2;  // heads of a tile
-  const int64_t ntasks = (int64_t)p.S * U * hpu;
-  for (int64_t task = (int64_t)blockIdx.x * NW + (threadIdx.x >> 5); task < ntasks;
-       task += (int64_t)gridDim.x * NW) {
-    const int64_t u = task / hpu;
-    const int i = (int)(task % hpu);
-    const int s = (int)(u / U), lu = (int)(u % U);
-    const int ht = lu % p.n_ht;
-    if (2 * i >= min(8, p.G - 8 * ht)) continue;
-    const int ps0 = __ldcg(PS + s), ps1 = __ldcg(PS + s + 1);
-    const int Ps = (ps1 - ps0) / U;
-    if (Ps == 0) continue;
-    const int U0 = ps0 + lu * Ps;
-    const int wf = U0 / ppw, wl = (U0 + Ps - 1) / ppw;
-    if (wf == wl) continue;  // written directly by its warp
-    const int head = lu / p.n_ht * (p.G / 2) + 4 * ht + i;
-    float y[NE];
-    const float lam = p.diff.lambda[head];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
+  const int tpu = min(kPartRows, p.G) / RPT;  // tasks of a head tile
+  const int64_t ntasks = ppw > 0 ? (int64_t)p.S * U * tpu : 0;
+  struct Task {
+    int s, lu, i, U0, wf, n_u;  // n_u: pieces; 0: nothing to join
+  };
+  auto find = [&](int64_t task) {
+    Task t;
+    const int64_t u = task / tpu;
+    t.i = static_cast<int>(task - u * tpu);
+    t.s = static_cast<int>(u / U);
+    t.lu = static_cast<int>(u - (int64_t)t.s * U);
+    const int ps0 = PS[t.s], Ps = (PS[t.s + 1] - ps0) / U;
+    t.U0 = ps0 + t.lu * Ps;
+    t.wf = t.U0 / ppw;
+    t.n_u = (t.U0 + Ps - 1) / ppw - t.wf + 1;
+    // (a unit within one range was written by its warp; a ragged last tile has fewer rows)
+    if (Ps == 0 || t.n_u == 1 || RPT * t.i >= min(8, p.G - 8 * (t.lu % p.n_ht))) t.n_u = 0;
+    return t;
+  };
+  int64_t task = (int64_t)blockIdx.x * NW + warp;
+  const int64_t step = (int64_t)gridDim.x * NW;
+  Task t;
+  if (task < ntasks) t = find(task);
+  if (own) asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (; task < ntasks; task += step, t = task < ntasks ? find(task) : t) {
+    if (t.n_u == 0) continue;
+    const int ht = t.lu % p.n_ht, h = t.lu / p.n_ht;
+    if constexpr (!DIFF) {
+      const int64_t orow = (int64_t)t.s * p.Hq + h * p.G + 8 * ht + t.i;
       float M = kNegInf, Lsum = 0.f, acc[NE];
 #pragma unroll
       for (int e = 0; e < NE; ++e) acc[e] = 0.f;
-      merge_pieces<D, CH>(p, wf, wl - wf + 1, U0, ppw, 2 * i + r, lane, M, Lsum, acc);
-      const float f = Lsum > 0.f ? (r == 0 ? 1.f : -lam) / Lsum : 0.f;
+      if (p.pre != nullptr) {  // cascade: the prefix partial is one more piece
+        const float* pr = p.pre + orow * (D + 2);
+        M = pr[0];
+        Lsum = pr[1];
 #pragma unroll
-      for (int e = 0; e < NE; ++e) y[e] = r == 0 ? acc[e] * f : fmaf(acc[e], f, y[e]);
-    }
-    float ss = 0.f;
+        for (int e = 0; e < NE; ++e) acc[e] = pr[2 + lane + 32 * e];
+      }
+      merge_pieces<D, CH>(p, t.wf, t.n_u, t.U0, ppw, t.i, lane, M, Lsum, acc);
+      if (p.lse != nullptr && lane == 0) p.lse[orow] = row_lse(M, Lsum);
+      float* dst = p.out + (int64_t)t.s * p.out_stride + (int64_t)(h * p.G + 8 * ht + t.i) * D;
 #pragma unroll
-    for (int e = 0; e < NE; ++e) ss = fmaf(y[e], y[e], ss);
+      for (int e = 0; e < NE; ++e) dst[lane + 32 * e] = Lsum > 0.f ? acc[e] / Lsum : 0.f;
+    } else {
+      const int head = h * (p.G / 2) + 4 * ht + t.i;
+      const float lam = p.diff.lambda[head];
+      float y[NE], ss = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float f = diff_factor<D>(p.diff, ss);
-    __half* dst = p.diff.out + ((int64_t)s * (p.Hq / 2) + head) * D;
+      for (int r = 0; r < 2; ++r) {
+        float M = kNegInf, Lsum = 0.f, acc[NE];
 #pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int d = lane + 32 * e;
-      dst[d] = __float2half_rn(y[e] * (p.diff.weight != nullptr ? f * p.diff.weight[d] : f));
+        for (int e = 0; e < NE; ++e) acc[e] = 0.f;
+        merge_pieces<D, CH>(p, t.wf, t.n_u, t.U0, ppw, 2 * t.i + r, lane, M, Lsum, acc);
+        const float f = Lsum > 0.f ? (r == 0 ? 1.f : -lam) / Lsum : 0.f;
+#pragma unroll
+        for (int e = 0; e < NE; ++e) y[e] = r == 0 ? acc[e] * f : fmaf(acc[e], f, y[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < NE; ++e) ss = fmaf(y[e], y[e], ss);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float f = diff_factor<D>(p.diff, ss);
+      __half* dst = p.diff.out + ((int64_t)t.s * (p.Hq / 2) + head) * D;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        const int d = lane + 32 * e;
+        dst[d] = __float2half_rn(y[e] * (p.diff.weight != nullptr ? f * p.diff.weight[d] : f));
+      }
     }
   }
 }
@@ -1460,25 +1535,28 @@ struct DecodeLaunch {
 };
 
 // The merge of a decode's pieces, as its programmatic dependent.
-template <int D, bool DIFF>
-cudaError_t run_merge(const DecodeLaunch& l) {
+template <class Kernel>
+cudaError_t launch_merge(const DecodeLaunch& l, Kernel kernel, unsigned grid, int smem) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(l.merge_grid);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kMergeThreads);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = l.st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if constexpr (DIFF)
-    return phase_mark(l.st, l.merge_chunk == 16
-                                ? cudaLaunchKernelEx(&cfg, kvq_diff_merge_kernel<D, 16>, l.p)
-                                : cudaLaunchKernelEx(&cfg, kvq_diff_merge_kernel<D, 8>, l.p));
-  return phase_mark(l.st, l.merge_chunk == 16
-                              ? cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, 16>, l.p)
-                              : cudaLaunchKernelEx(&cfg, kvq_merge_kernel<D, 8>, l.p));
+  return phase_mark(l.st, cudaLaunchKernelEx(&cfg, kernel, l.p));
+}
+
+template <int D, bool DIFF>
+cudaError_t run_join(const DecodeLaunch& l) {
+  const int smem = l.p.S <= kJoinSeqs ? (kMergeThreads / 32 + l.p.S + 1) * 4 : 0;
+  // (a differential head is one task for two rows)
+  const unsigned grid = DIFF ? (l.merge_grid + 1) / 2 : l.merge_grid;
+  return l.merge_chunk == 16 ? launch_merge(l, kvq_join_kernel<D, 16, DIFF>, grid, smem)
+                             : launch_merge(l, kvq_join_kernel<D, 8, DIFF>, grid, smem);
 }
 
 // CTAS: resident CTAs per SM the kernel is compiled for.
@@ -1500,7 +1578,9 @@ cudaError_t run_decode(const DecodeLaunch& l) {
     e = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode_kernel<FMT, D, NG, BS8, CTAS, DIFF>, l.p));
     if (e != cudaSuccess) return e;
   }
-  return run_merge<D, DIFF>(l);
+  if constexpr (DIFF) return run_join<D, true>(l);
+  return l.merge_chunk == 16 ? launch_merge(l, kvq_merge_kernel<D, 16>, l.merge_grid, 0)
+                             : launch_merge(l, kvq_merge_kernel<D, 8>, l.merge_grid, 0);
 }
 
 template <int FMT, bool BS8 = false, bool DIFF = false>

@@ -17,7 +17,9 @@
 // channels 16kk + 4j .. +3 of tokens g and g + 8, V word mt tokens 2j, 2j+1, 2j+8, 2j+9
 // of channels 16mt + g and 16mt + g + 8.  Each byte is the pair of one fragment register.
 // The 16 * D/16 scale bytes of a sub-tile lie as the lanes want them: K's for
-// token row g, then g + 8, side by side; V's in words of the four tokens of a lane.
+// token row g, then g + 8, side by side; V's in words of the four tokens of a lane.  A
+// page is its K codes and their scales, then the same of V, so that either half is one
+// copy.
 #pragma once
 #include <cstdint>
 #include <cuda_fp16.h>

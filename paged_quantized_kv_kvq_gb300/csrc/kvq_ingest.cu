@@ -28,7 +28,7 @@ __device__ __forceinline__ void read_tile(const PoolView& pool, int64_t blk, int
   const int D = pool.D, d0 = 8 * ci;
   const int64_t row = (int64_t)pool.Hkv * D;
   const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
-  const char* tile = page + (kv == 0 ? 0 : pool.code_bytes) + (off >> 4) * pool.sub_bytes;
+  const char* tile = page + (kv == 0 ? 0 : pool.v_off) + (off >> 4) * pool.sub_bytes;
   const float* sc = reinterpret_cast<const float*>(page + 2 * pool.code_bytes);
   uint32_t w[8];  // K: token c's two words; V: a word per channel, a byte per token
   if (kv == 0) {
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
     const int64_t blk = slot >> bs_log2;
     const int off = static_cast<int>(slot & (pool.bs - 1)), t = off & 15;
     const char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
-    const char* tile = page + (kv == 0 ? 0 : pool.code_bytes) + (off >> 4) * pool.sub_bytes;
+    const char* tile = page + (kv == 0 ? 0 : pool.v_off) + (off >> 4) * pool.sub_bytes;
     const float* sc = reinterpret_cast<const float*>(page + 2 * pool.code_bytes);
     // the first of the thread's words: lane and word of (t, d0) in the sub-tile
     int lane, word;
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(256) kvq_read_values_kernel(PoolView pool, int
       s = sc[(kv * pool.bs + off) * pool.ng + d0 / pool.group];
     else if constexpr (FMT == FMT_FP4)
       s = fp4_scale_value(static_cast<uint8_t>(
-          page[2 * pool.code_bytes + kv * pool.bs * pool.ng + (off >> 4) * D +
+          page[(kv == 0 ? 0 : pool.v_off) + pool.code_bytes + (off >> 4) * D +
                (kv == 0 ? fp4_k_scale(t, ci >> 1, pool.ng) : fp4_v_scale(t, ci >> 1, pool.ng))]));
     else if constexpr (fmt_block(FMT))
       s = sc[kv];

@@ -106,7 +106,7 @@ template <int D>
 __device__ __forceinline__ void store_fp4_scale(char* page, int kv, int off, int gi, const PoolView& pool,
                                                 uint32_t code) {
   constexpr int NG = D / 16;
-  page[2 * pool.code_bytes + kv * pool.bs * NG + (off >> 4) * D +
+  page[(kv == 0 ? 0 : pool.v_off) + pool.code_bytes + (off >> 4) * D +
        (kv == 0 ? fp4_k_scale(off & 15, gi, NG) : fp4_v_scale(off & 15, gi, NG))] = static_cast<char>(code);
 }
 
@@ -216,7 +216,7 @@ __device__ __forceinline__ void ingest_token(const IngestParams& p, IngestShared
     const int h = hb + r0;
     const bool act = h < pool.Hkv;
     char* page = pool.pages + (blk * pool.Hkv + (act ? h : 0)) * pool.page_bytes;
-    char* codes = page + (kv == 0 ? 0 : pool.code_bytes);
+    char* codes = page + (kv == 0 ? 0 : pool.v_off);
     float* scales = reinterpret_cast<float*>(page + 2 * pool.code_bytes);
     float s = s_tok;
     if constexpr (kBlock) {
@@ -233,7 +233,7 @@ __device__ __forceinline__ void ingest_token(const IngestParams& p, IngestShared
       const int grown = sh.grown;
       for (int i = 0; i < grown; ++i) {
         uint4* tile = reinterpret_cast<uint4*>(pool.pages + (blk * pool.Hkv + sh.grown_head[i]) * pool.page_bytes +
-                                               (kv == 0 ? 0 : pool.code_bytes));
+                                               (kv == 0 ? 0 : pool.v_off));
         const float from = sh.grown_from[i], to = sh.grown_to[i], inv = quant_inverse(to);
         for (int u = tid; u < pool.code_bytes / 16; u += kIngestThreads) {
           uint4 v = tile[u];
@@ -379,7 +379,7 @@ __device__ __forceinline__ void ingest_run(const IngestParams& p, IngestShared& 
 
   for (int h = h0; h < h1; ++h) {
     char* page = pool.pages + (blk * pool.Hkv + h) * pool.page_bytes;
-    char* codes = page + (kv == 0 ? 0 : pool.code_bytes);
+    char* codes = page + (kv == 0 ? 0 : pool.v_off);
     float* scales = reinterpret_cast<float*>(page + 2 * pool.code_bytes);
     load_head(h);
     float s_block = 0.f;
@@ -645,7 +645,7 @@ __device__ __forceinline__ void ingest_whole(const IngestParams& p, IngestShared
         }
       }
       if (!last || !act) continue;
-      char* tile = page + (kv == 0 ? 0 : pool.code_bytes) + sub * pool.sub_bytes;
+      char* tile = page + (kv == 0 ? 0 : pool.v_off) + sub * pool.sub_bytes;
       if constexpr (FMT == FMT_FP16) {
         uint32_t o[4][4];
 #pragma unroll

@@ -122,6 +122,7 @@ struct DecodePlan {
   int ppw_fixed = 0;    // pages per warp when forced; 0 = balanced
   int n_ht = 0;         // head tiles of 8 Q heads per kv head
   int nstage = 0;  // pipeline stages per warp
+  int part_rows = 0;    // rows of a split partial
   int stage_bytes = 0;  // bytes of one stage
   int smem_bytes = 0;   // dynamic shared memory per CTA
   int merge_grid = 0;   // CTAs of the merge kernel

@@ -436,13 +436,13 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
           for (int i = 0; i < NCH; ++i) {
             const int ch = cid + i * kTcConv;
             rv[s][kv][i] = (ok && ch < CPS)
-                               ? *reinterpret_cast<const uint4*>(base + (kv ? pool.code_bytes : 0) +
+                               ? *reinterpret_cast<const uint4*>(base + (kv ? pool.v_off : 0) +
                                                                  (ch >> 5) * 512 + (ch & 31) * 16)
                                : make_uint4(0, 0, 0, 0);
             if constexpr (FMT == FMT_FP4)
               rs[s][kv][i] = (ok && ch < CPS)
-                                 ? tc_chunk_scales<D>(page_of(ph[pg]) + 2 * pool.code_bytes +
-                                                          kv * bs * (D / 16) + sub * D,
+                                 ? tc_chunk_scales<D>(page_of(ph[pg]) + (kv ? pool.v_off : 0) +
+                                                          pool.code_bytes + sub * D,
                                                       ch & 31, ch >> 5, kv == 1)
                                  : make_uint4(0, 0, 0, 0);
           }

@@ -112,10 +112,10 @@ __global__ void __launch_bounds__(128) kvq_prefill_stage_kernel(const StageParam
     const int nvalid = page ? min(max(ctx - (t0 + 16 * s4), 0), 16) : 0;
     uint4 rv = make_uint4(0, 0, 0, 0), rs = make_uint4(0, 0, 0, 0);
     if (FMT == FMT_FP4 && nvalid > 0)
-      rs = tc_chunk_scales<D>(page + 2 * pool.code_bytes + (isv ? bs * (D / 16) : 0) + (off >> 4) * D,
+      rs = tc_chunk_scales<D>(page + (isv ? pool.v_off : 0) + pool.code_bytes + (off >> 4) * D,
                               ch & 31, ch >> 5, isv);
     if (nvalid > 0)
-      rv = *reinterpret_cast<const uint4*>(page + (isv ? pool.code_bytes : 0) + (off >> 4) * SUB_BYTES +
+      rv = *reinterpret_cast<const uint4*>(page + (isv ? pool.v_off : 0) + (off >> 4) * SUB_BYTES +
                                            (ch >> 5) * 512 + (ch & 31) * 16);
     tc_convert_chunk<FMT, D>(rv, ch & 31, ch >> 5, isv, s4, nvalid, rec + R::kh, rec + R::vt, rs);
   }

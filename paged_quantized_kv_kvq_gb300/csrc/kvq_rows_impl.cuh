@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kRowsThreads) kvq_rows_kernel(const RowsParams
       {
         uint32_t kw[NU32];
         if constexpr (FMT == FMT_FP4)
-          fp4_load_k<D>(stage + sub * pool.sub_bytes, stage + 2 * pool.code_bytes + sub * D, lane, kw);
+          fp4_load_k<D>(stage + sub * pool.sub_bytes, stage + pool.code_bytes + sub * D, lane, kw);
         else
           load_lane_words<FMT, D>(stage + sub * pool.sub_bytes, lane, kw);
         constexpr int SUB = KPG >= 2 ? 2 : 1;  // independent accumulators per group
@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(kRowsThreads) kvq_rows_kernel(const RowsParams
       {
         uint32_t vw[NU32];
         if constexpr (FMT == FMT_FP4)
-          fp4_load_v<D>(stage + pool.code_bytes + sub * pool.sub_bytes,
-                        stage + 2 * pool.code_bytes + bs * (D / 16) + sub * D, lane, nvalid, vw);
+          fp4_load_v<D>(stage + pool.v_off + sub * pool.sub_bytes,
+                        stage + pool.v_off + pool.code_bytes + sub * D, lane, nvalid, vw);
         else
           load_lane_words<FMT, D>(stage + pool.code_bytes + sub * pool.sub_bytes, lane, vw);
         if constexpr (T::maybe_nan) {

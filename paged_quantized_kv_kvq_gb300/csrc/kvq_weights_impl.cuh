@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kWeightsWarps * 32, kWeightsCtas)
   constexpr int NU32 = lane_words<FMT, D>(), NC = NU32 / 4;  // 32-bit words, 16-byte chunks per lane
   constexpr int NS = T::group_scales ? NG : 1;
   constexpr bool kCopied = T::group_scales || T::token_scales;  // scales come with the codes
-  constexpr bool kFp4 = FMT == FMT_FP4;                         // (so do these, in bytes)
+  constexpr bool kFp4 = FMT == FMT_FP4;                         // (their scales follow the K codes)
   const float kInf = __int_as_float(0x7f800000u);
   extern __shared__ __align__(128) char smem[];
   const PoolView& pool = p.d.pool;
@@ -218,10 +218,10 @@ __global__ void __launch_bounds__(kWeightsWarps * 32, kWeightsCtas)
       if (now.entry >= 0) {
         char* dst = stages + st * stage_bytes + k * p.slot_bytes;
         const char* page = page_at(now);
-        bulk_g2s(dst, page, pool.code_bytes, &bars[st]);
+        bulk_g2s(dst, page, kFp4 ? page_tx : pool.code_bytes, &bars[st]);
         if constexpr (T::token_scales)
           bulk_g2s(dst + pool.code_bytes, pool.tok_scales + (int64_t)now.entry * 2 * bs, p.scale_bytes, &bars[st]);
-        else if constexpr (T::group_scales || kFp4)
+        else if constexpr (T::group_scales)
           bulk_g2s(dst + pool.code_bytes, page + 2 * pool.code_bytes, p.scale_bytes, &bars[st]);
       }
     }
