@@ -23,7 +23,7 @@ SOURCES = ["kvq_api.cu", "kvq_append.cu", "kvq_decode.cu", "kvq_decode_i8g.cu",
            "kvq_decode_misc.cu", "kvq_noalloc.cu", "kvq_rows.cu",
            "kvq_decode_i4g.cu", "kvq_prefill.cu", "kvq_decode_bs8.cu", "kvq_decode_bs8_misc.cu", "kvq_prefill_tc.cu",
            "kvq_decode_block.cu", "kvq_decode_fp4.cu", "kvq_diff.cu", "kvq_diff_decode.cu",
-           "kvq_diff_decode_group.cu", "kvq_blocks.cu", "kvq_rope.cu", "kvq_ingest.cu", "kvq_ingest_group.cu", "kvq_ingest_misc.cu",
+           "kvq_diff_decode_group.cu", "kvq_blocks.cu", "kvq_fp4_rows.cu", "kvq_rope.cu", "kvq_ingest.cu", "kvq_ingest_group.cu", "kvq_ingest_misc.cu",
            "kvq_weights.cu", "kvq_weights_group.cu", "kvq_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

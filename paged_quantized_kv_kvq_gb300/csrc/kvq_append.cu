@@ -24,6 +24,11 @@
 namespace kvq {
 
 constexpr int kAppendThreads = 128;
+// Tokens from which on 4-bit floats take kvq_fp4_rows.cu.  (8 heads of 128, this kernel and
+// that one: 256 tokens of whole blocks 3.8 and 3.1 us, single tokens 3.6 and 4.6; 512 tokens
+// 5.3 and 3.1, 4.3 and 4.9; 2048 tokens 12.9 and 4.6, 10.3 and 8.6; 16384 tokens 74 and 18,
+// 92 and 78.  2 heads of 64: 512 tokens 3.3 and 2.9, 3.1 and 3.8.)
+constexpr int kAppend4Tokens = 512;
 
 struct AppendParams {
   PoolView pool;
@@ -389,6 +394,8 @@ cudaError_t launch_step_append(const PoolView& pool, const __half* k, const __ha
   }
   AppendParams p{pool, k, v, slots, T, table, lens, max_blocks, max_ctx,
                  x_stride > 0 ? x_stride : (int64_t)pool.Hkv * pool.D};
+  if (pool.fmt == FMT_FP4 && slots != nullptr && T >= kAppend4Tokens)
+    return launch_append4(pool, k, v, p.x_stride, slots, T, st);
   dim3 grid(static_cast<unsigned>(T), 2);
   switch (pool.fmt) {
     case FMT_FP16: return launch_append_fmt<FMT_FP16>(p, grid, st, dependent);

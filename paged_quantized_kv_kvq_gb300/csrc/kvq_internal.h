@@ -81,6 +81,12 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st, bool beside = false)
 cudaError_t launch_read_values(const PoolView& pool, const int64_t* slots, int64_t n, __half* k,
                                __half* v, cudaStream_t st);
 
+// Long appends to pools of 4-bit floats, and their read-back (kvq_fp4_rows.cu).
+cudaError_t launch_append4(const PoolView& pool, const __half* k, const __half* v, int64_t stride,
+                           const int64_t* slots, int64_t T, cudaStream_t st);
+cudaError_t launch_read_values4(const PoolView& pool, const int64_t* slots, int64_t n, __half* k,
+                                __half* v, cudaStream_t st);
+
 // Attention weights of the cached tokens (kvq_weights_impl.cuh), from the
 // log-sum-exps of a decode of the same rows.
 struct WeightsArgs {

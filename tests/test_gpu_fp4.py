@@ -114,7 +114,8 @@ def test_append_is_bit_exact(way, bs, hkv, d):
 
 
 @pytest.mark.parametrize("way", ["append", "strided", "fused"])
-@pytest.mark.parametrize("bs,hkv,d,T", [(16, 2, 128, 5000), (64, 3, 64, 3001), (32, 1, 128, 1100), (16, 1, 64, 1025)])
+@pytest.mark.parametrize("bs,hkv,d,T", [(16, 2, 128, 5000), (64, 3, 64, 3001), (32, 1, 128, 1100), (16, 1, 64, 1025), (16, 9, 64, 511),
+                                        (16, 3, 128, 512), (32, 5, 64, 2049)])
 def test_append_of_many_tokens(way, bs, hkv, d, T):
     """Long calls: sequences that begin and end anywhere in their blocks, whose older
     tokens stay, single tokens and padding among them."""
@@ -150,6 +151,33 @@ def test_append_of_many_tokens(way, bs, hkv, d, T):
     assert pool.error() == kvq.KVQ_OK
     at = np.unique(np.concatenate([older, slots]))
     _check(pool, ref, at[at >= 0])
+    pool.close()
+
+
+def test_reads_of_many_slots():
+    """Long read-backs: runs, single slots in any order, the same slot twice, padding (whose
+    rows stay) and slots outside the pool (flagged)."""
+    rng = np.random.default_rng(3)
+    bs, hkv, d, nb = 32, 3, 64, 90
+    pool = kvq.KVPool(nb, bs, hkv, d, FMT, device=DEV)
+    ref = Fp4Cache(nb, bs, hkv, d)
+    at = np.arange(nb * bs)
+    k, v = _rows(rng, len(at), hkv, d), _rows(rng, len(at), hkv, d)
+    pool.append(_t(k), _t(v), _t(at))
+    ref.append(k, v, at)
+    ask = np.concatenate([at[5:1500], rng.integers(0, nb * bs, 300), [-1] * 5, at[100:117], at[200:190:-1], [7] * 20, at[1501:], [-3]])
+    for bad in (False, True):
+        if bad:
+            ask[[3, 700, 1600]] = nb * bs, 1 << 50, nb * bs + 9
+        ko, vo = (torch.full((len(ask), hkv, d), 7.0, dtype=torch.float16, device=DEV) for _ in range(2))
+        kvq.kvq_read_values(pool.handle, _t(ask), ko, vo)
+        assert pool.error() == (kvq.KVQ_ERR_OUT_OF_RANGE if bad else kvq.KVQ_OK)
+        real = (ask >= 0) & (ask < nb * bs)
+        want = ref.values(ask[real])
+        for got, x in ((ko, 0), (vo, 1)):
+            got = got.cpu().numpy()
+            np.testing.assert_array_equal(got[real], want[:, x].astype(np.float16))
+            assert (got[~real] == 7).all()
     pool.close()
 
 
