@@ -637,7 +637,7 @@ size_t kvq_diff_prefill_workspace_bytes(const kvq_pool* pool, int num_seqs, int6
 
 /* Prompts and chunks of them.
  *   q, out     : fp16 [num_tokens][num_heads][head_dim]; rows from q_start[num_seqs] on
- *                are not read, and left as they were
+ *                are not read, and left as they were; 16-byte aligned
  *   num_tokens : rows of q and out, >= q_start[num_seqs]
  *   workspace  : >= kvq_diff_prefill_workspace_bytes(..) bytes, 256-byte aligned
  * lambda, norm_weight, eps and out_scale are those of kvq_diff_decode, the other

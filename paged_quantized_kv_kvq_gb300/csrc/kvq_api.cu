@@ -823,7 +823,7 @@ kvq_status kvq_diff_prefill(const kvq_pool* pool, const kvq_half* q, int64_t num
   if (q == nullptr || q_start == nullptr || block_table == nullptr || context_lens == nullptr ||
       !diff_args_ok(lambda, norm_weight, eps, out_scale, out, &d))
     return KVQ_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(q) & 15) return KVQ_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) return KVQ_ERR_INVALID_ARG;
   if (max_context_len == 0) return KVQ_ERR_INVALID_ARG;
   const size_t need = kvq_diff_prefill_workspace_bytes(pool, num_seqs, num_tokens, num_heads, max_context_len);
   if (workspace == nullptr || ws_bytes < need) return KVQ_ERR_WORKSPACE;

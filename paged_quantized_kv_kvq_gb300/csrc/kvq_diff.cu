@@ -1,9 +1,11 @@
 // kvq_diff.cu -- differential attention over a paged pool: format dispatch of the decode
 // (kvq_decode_impl.cuh's DIFF kernels), and prompts.
 //
-// Prompts: every head becomes two Q rows, one per map with the other map's channels zero;
-// the prefill kernels attend them, and a last kernel takes the difference of the two
-// results of a head, norms it and rounds it.
+// Prompts go through the two-pass prefill, whose attention kernel has a form for two maps
+// (kvq_prefill_ws_impl.cuh).  Formats that it does not take (per-channel scales, several scale
+// groups per head): every head becomes two Q rows, one per map with the other map's
+// channels zero, the prefill kernels attend them, and a last kernel takes the
+// difference of the two results of a head, norms it and rounds it.
 #include <algorithm>
 
 #include "kvq_decode_impl.cuh"
@@ -55,6 +57,10 @@ __global__ void __launch_bounds__(kDiffThreads) kvq_diff_combine_kernel(const fl
     dst[e] = __float2half_rn(y[e] * (p.weight != nullptr ? f * p.weight[lane * NE + e] : f));
 }
 
+bool two_maps(const PoolView& pool) {
+  return prefill_tc_supported(pool) && pool.fmt != FMT_INT8_CHANNEL;
+}
+
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
@@ -72,6 +78,7 @@ cudaError_t launch_decode_diff(const DecodeLaunch& l) {
 }
 
 size_t diff_prefill_ws_bytes(const PoolView& pool, int64_t T, int S, int H, int max_ctx) {
+  if (two_maps(pool)) return prefill_ws_bytes(pool, S, max_ctx);
   const size_t rows = (size_t)T * 2 * H * pool.D;
   return up256(rows * sizeof(__half)) + up256(rows * sizeof(float)) + prefill_ws_bytes(pool, S, max_ctx);
 }
@@ -80,6 +87,9 @@ cudaError_t launch_diff_prefill(const PoolView& pool, const __half* q, int64_t T
                                 const int* q_start, int max_q_len, const int* table, int max_blocks,
                                 const int* lens, int max_ctx, float sm_scale, const DiffOut& diff,
                                 void* ws, cudaStream_t st) {
+  if (two_maps(pool))
+    return launch_prefill_ws(pool, q, S, H, q_start, max_q_len, table, max_blocks, lens, max_ctx, sm_scale,
+                             nullptr, ws, st, &diff);
   const int D = pool.D;
   const size_t rows = (size_t)T * 2 * H * D;
   __half* qx = static_cast<__half*>(ws);

@@ -11,6 +11,19 @@
 
 namespace kvq {
 
+// Differential attention: the two halves of a head's channels are two maps over one V,
+//   y = softmax(s q1.k1) V - lambda softmax(s q2.k2) V,
+//   out = out_scale * y / sqrt(mean(y^2) + eps) * weight  (no norm without a weight).
+// To the kernels a head is two Q rows, 2i and 2i + 1 of its group, each q with the other
+// half zero: what the heads of a group share -- the page, its conversion, the products'
+// n dimension -- the maps share too.
+struct DiffOut {
+  const float* lambda = nullptr;  // [heads]
+  const float* weight = nullptr;  // [D] or null
+  __half* out = nullptr;          // [rows][heads][D]
+  float eps = 0.f, out_scale = 1.f;
+};
+
 cudaError_t launch_append(const PoolView& pool, const __half* k, const __half* v,
                           const int64_t* slots, int64_t T, cudaStream_t st);
 // Append with slots from `slots`, or -- when slots is null -- the decode-step
@@ -143,19 +156,6 @@ struct DecodePlan {
 bool plan_decode(const PoolView& pool, int S, int Hq, int max_ctx, int split_blocks, int sms,
                  DecodePlan* plan);
 
-// Differential attention: the two halves of a head's channels are two maps over one V,
-//   y = softmax(s q1.k1) V - lambda softmax(s q2.k2) V,
-//   out = out_scale * y / sqrt(mean(y^2) + eps) * weight  (no norm without a weight).
-// To the kernels a head is two Q rows, 2i and 2i + 1 of its group, each q with the other
-// half zero: what the heads of a group share -- the page, its conversion, the products'
-// n dimension -- the maps share too.
-struct DiffOut {
-  const float* lambda = nullptr;  // [heads]
-  const float* weight = nullptr;  // [D] or null
-  __half* out = nullptr;          // [rows][heads][D]
-  float eps = 0.f, out_scale = 1.f;
-};
-
 struct DecodeArgs {
   PoolView pool;
   const __half* q;
@@ -223,7 +223,8 @@ size_t prefill_ws_bytes(const PoolView& pool, int S, int max_ctx);
 cudaError_t launch_prefill_ws(const PoolView& pool, const __half* q, int S, int Hq,
                               const int* q_start, int max_q_len, const int* table, int max_blocks,
                               const int* lens, int max_ctx, float sm_scale, float* out, void* ws,
-                              cudaStream_t st);
+                              cudaStream_t st, const DiffOut* diff = nullptr);
+// (diff: differential attention, Hq heads, rows to diff->out; not for per-channel pools.)
 
 // Differential attention of prompts (kvq_diff.cu); T rows of q and out, H heads.
 size_t diff_prefill_ws_bytes(const PoolView& pool, int64_t T, int S, int H, int max_ctx);

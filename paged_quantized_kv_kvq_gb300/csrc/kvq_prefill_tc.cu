@@ -80,16 +80,18 @@ size_t prefill_ws_bytes(const PoolView& pool, int S, int max_ctx) {
 namespace {
 
 template <int FMT, int D>
-cudaError_t run_ws(const StageParams& sp, const PrefillWsParams& ap, int64_t ntiles,
-                   cudaStream_t st) {
-  constexpr int NT = WsShape<FMT>::NT;
-  using PL = WsPlan<D, NT, FmtTraits<FMT>::channel>;
-  static_assert(PL::request <= 227 * 1024, "shared memory plan too large");
+cudaError_t run_stage(const StageParams& sp, cudaStream_t st) {
   const int64_t sgrid = (int64_t)sp.S * sp.max_steps * sp.pool.Hkv;
   if (sgrid > 0x7fffffffLL) return cudaErrorInvalidValue;
   kvq_prefill_stage_kernel<FMT, D><<<static_cast<unsigned>(sgrid), 128, 0, st>>>(sp);
-  cudaError_t e = phase_mark(st, cudaGetLastError());
-  if (e != cudaSuccess) return e;
+  return phase_mark(st, cudaGetLastError());
+}
+
+// NT: 128-row tiles of rows per item (DIFF: one, of two maps).
+template <int FMT, int D, int NT, bool DIFF>
+cudaError_t run_attend(const PrefillWsParams& ap, int64_t ntiles, cudaStream_t st) {
+  using PL = WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::channel>;
+  static_assert(PL::request <= 227 * 1024, "shared memory plan too large");
   PrefillWsParams a = ap;
   const int64_t ngroups = (ntiles + NT - 1) / NT;
   const int64_t items = ngroups * a.S * a.pool.Hkv;
@@ -102,18 +104,30 @@ cudaError_t run_ws(const StageParams& sp, const PrefillWsParams& ap, int64_t nti
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
     sms = 152;
   const int64_t grid = items < sms ? items : sms;
-  e = allow_big_smem<kvq_prefill_ws_kernel<FMT, D>>();
+  const cudaError_t e = allow_big_smem<kvq_prefill_ws_kernel<FMT, D, DIFF>>();
   if (e != cudaSuccess) return e;
-  kvq_prefill_ws_kernel<FMT, D><<<static_cast<unsigned>(grid), PL::threads, PL::request, st>>>(a);
+  kvq_prefill_ws_kernel<FMT, D, DIFF><<<static_cast<unsigned>(grid), PL::threads, PL::request, st>>>(a);
   return phase_mark(st, cudaGetLastError());
 }
 
+template <int FMT, int D>
+cudaError_t run_ws(const StageParams& sp, const PrefillWsParams& ap, int64_t ntiles, bool diff,
+                   cudaStream_t st) {
+  const cudaError_t e = run_stage<FMT, D>(sp, st);
+  if (e != cudaSuccess) return e;
+  if (!diff) return run_attend<FMT, D, WsShape<FMT>::NT, false>(ap, ntiles, st);
+  // a staged step looks the same whatever its codes were, with scales or without
+  if constexpr (FmtTraits<FMT>::channel) return cudaErrorInvalidValue;
+  else if constexpr (FmtTraits<FMT>::row_scales) return run_attend<FMT_INT8_BLOCK, D, 1, true>(ap, ntiles, st);
+  else return run_attend<FMT_FP16, D, 1, true>(ap, ntiles, st);
+}
+
 template <int FMT>
-cudaError_t run_ws_d(const StageParams& sp, const PrefillWsParams& ap, int64_t ntiles,
+cudaError_t run_ws_d(const StageParams& sp, const PrefillWsParams& ap, int64_t ntiles, bool diff,
                      cudaStream_t st) {
   switch (sp.pool.D) {
-    case 64: return run_ws<FMT, 64>(sp, ap, ntiles, st);
-    case 128: return run_ws<FMT, 128>(sp, ap, ntiles, st);
+    case 64: return run_ws<FMT, 64>(sp, ap, ntiles, diff, st);
+    case 128: return run_ws<FMT, 128>(sp, ap, ntiles, diff, st);
   }
   return cudaErrorInvalidValue;
 }
@@ -123,7 +137,7 @@ cudaError_t run_ws_d(const StageParams& sp, const PrefillWsParams& ap, int64_t n
 cudaError_t launch_prefill_ws(const PoolView& pool, const __half* q, int S, int Hq,
                               const int* q_start, int max_q_len, const int* table, int max_blocks,
                               const int* lens, int max_ctx, float sm_scale, float* out, void* ws,
-                              cudaStream_t st) {
+                              cudaStream_t st, const DiffOut* diff) {
   if (!prefill_tc_supported(pool)) return cudaErrorInvalidValue;
   const int G = Hq / pool.Hkv;
   const int64_t ntiles = ((int64_t)max_q_len * G + kTcRows - 1) / kTcRows;
@@ -143,17 +157,19 @@ cudaError_t launch_prefill_ws(const PoolView& pool, const __half* q, int S, int 
   ap.max_ctx = max_ctx;
   ap.max_steps = max_steps;
   ap.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  const bool d = diff != nullptr;
+  if (d) ap.diff = *diff;
   switch (pool.fmt) {
-    case FMT_FP16: return run_ws_d<FMT_FP16>(sp, ap, ntiles, st);
-    case FMT_INT8_TOKEN: return run_ws_d<FMT_INT8_TOKEN>(sp, ap, ntiles, st);
-    case FMT_INT8_CHANNEL: return run_ws_d<FMT_INT8_CHANNEL>(sp, ap, ntiles, st);
-    case FMT_INT8_GROUP: return run_ws_d<FMT_INT8_GROUP>(sp, ap, ntiles, st);
-    case FMT_FP8_TOKEN: return run_ws_d<FMT_FP8_TOKEN>(sp, ap, ntiles, st);
-    case FMT_INT4_GROUP: return run_ws_d<FMT_INT4_GROUP>(sp, ap, ntiles, st);
-    case FMT_FP8_E5M2: return run_ws_d<FMT_FP8_E5M2>(sp, ap, ntiles, st);
-    case FMT_INT8_BLOCK: return run_ws_d<FMT_INT8_BLOCK>(sp, ap, ntiles, st);
-    case FMT_FP8_BLOCK: return run_ws_d<FMT_FP8_BLOCK>(sp, ap, ntiles, st);
-    case FMT_FP4: return run_ws_d<FMT_FP4>(sp, ap, ntiles, st);
+    case FMT_FP16: return run_ws_d<FMT_FP16>(sp, ap, ntiles, d, st);
+    case FMT_INT8_TOKEN: return run_ws_d<FMT_INT8_TOKEN>(sp, ap, ntiles, d, st);
+    case FMT_INT8_CHANNEL: return run_ws_d<FMT_INT8_CHANNEL>(sp, ap, ntiles, d, st);
+    case FMT_INT8_GROUP: return run_ws_d<FMT_INT8_GROUP>(sp, ap, ntiles, d, st);
+    case FMT_FP8_TOKEN: return run_ws_d<FMT_FP8_TOKEN>(sp, ap, ntiles, d, st);
+    case FMT_INT4_GROUP: return run_ws_d<FMT_INT4_GROUP>(sp, ap, ntiles, d, st);
+    case FMT_FP8_E5M2: return run_ws_d<FMT_FP8_E5M2>(sp, ap, ntiles, d, st);
+    case FMT_INT8_BLOCK: return run_ws_d<FMT_INT8_BLOCK>(sp, ap, ntiles, d, st);
+    case FMT_FP8_BLOCK: return run_ws_d<FMT_FP8_BLOCK>(sp, ap, ntiles, d, st);
+    case FMT_FP4: return run_ws_d<FMT_FP4>(sp, ap, ntiles, d, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -165,6 +165,7 @@ struct PrefillWsParams {
   int S, Hq, G, max_ctx, max_steps;
   int ngroups;          // CTAs per (sequence, kv head): ceil(tiles / NT)
   float sm_scale_log2;
+  DiffOut diff;         // DIFF: where its rows go, in the place of `out`
 };
 
 constexpr int kWsStages = 4;  // record stages in shared memory
@@ -209,7 +210,7 @@ struct WsPlan {
   // misc: int abort; uint64 kv_full[S], kv_empty[S], s_full[NT], s_read[NT],
   // p_full[NT], pv_done[NT], o_full[NT], q_full[NT], drain; uint32 tslot
   static constexpr int abort = misc, bars = misc + 8;
-  static constexpr int nbars = 2 * kWsStages + 6 * NT + 1;
+  static constexpr int nbars = 2 * kWsStages + 6 * NT + 1 + 6;  // (the last six: DIFF)
   static constexpr int tslot = bars + 8 * nbars;
   // per softmax warp, a 32-row x 16-float block of its output rows on their
   // way to global memory (rows 64 bytes apart, 16-byte chunks swizzled)
@@ -235,7 +236,7 @@ struct WsItem {
   bool bad_ctx;
 };
 
-template <int NT>
+template <int NT>  // (DIFF: 1, its two tiles being two maps of the same rows)
 __device__ __forceinline__ WsItem ws_item(const PrefillWsParams& p, int i) {
   const int per = p.S * p.pool.Hkv;
   WsItem it;
@@ -259,12 +260,23 @@ __device__ __forceinline__ WsItem ws_item(const PrefillWsParams& p, int i) {
   return it;
 }
 
-template <int FMT, int D>
+// DIFF: differential attention.  The two tiles of an item are the two maps of the same 128
+// rows: tile X multiplies the X-th halves of the channels of Q and K alone (half the
+// products of a row padded with zeros), and both attend the same V.  When both are
+// done each tile's warps read the same rows of both O -- a warp may read the tensor-memory
+// lanes of its quarter whoever wrote them -- take the difference of their half of the
+// columns, swap the halves' sums of squares and write normed fp16 rows: no expanded Q,
+// no fp32 results in memory.  The tiles meet at three more pairs of mbarriers: O and the
+// row's factor there, sums there, O read (only then may the next item's first P.V, which
+// overwrites it, be asked for).
+template <int FMT, int D, bool DIFF = false>
 __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::channel>::threads, 1)
     kvq_prefill_ws_kernel(const PrefillWsParams p) {
   using T = FmtTraits<FMT>;
   constexpr bool CH = T::channel;
   constexpr int NT = WsShape<FMT>::NT;
+  static_assert(!DIFF || NT == 2, "two maps");
+  constexpr int IT = DIFF ? 1 : NT;  // 128-row tiles of rows per item
   constexpr int NS = kWsStages;
   using PL = WsPlan<D, NT, CH>;
   using R = StepRec<D>;
@@ -288,6 +300,9 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
   uint64_t* o_full = pv_done + NT;         // [NT]: the tile's final P.V of an item done
   uint64_t* q_full = o_full + NT;          // [NT]: the tile's Q rows of an item written
   uint64_t* drain = q_full + NT;           // clean-up
+  uint64_t* x_ready = drain + 1;           // DIFF [2]: the tile's O and factors are there
+  uint64_t* x_sum = x_ready + 2;           // DIFF [2]: its sums of squares are there
+  uint64_t* x_read = x_sum + 2;            // DIFF [2]: it has read both O
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + PL::tslot);
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -303,6 +318,8 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
       mbar_init(&q_full[x], kTcRows / 32);  // one arrival per warp
     }
     mbar_init(drain, NT);
+    if constexpr (DIFF)
+      for (int x = 0; x < 6; ++x) mbar_init(&x_ready[x], kTcRows / 32);
     *abort_f = 0;
     fence_barrier_init();
   }
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
     if (lane == 0) {
       int copied = 0;
       for (int item = blockIdx.x; item < n_items && !*abort_f; item += gridDim.x) {
-        const WsItem it = ws_item<NT>(p, item);
+        const WsItem it = ws_item<IT>(p, item);
         bool ok = true;
         for (int j = 0; j < it.nsteps; ++j) {
           if (copied >= NS &&
@@ -356,10 +373,11 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
       auto issue_s = [&](int g) {  // S = Q K^T of global step g
         const uint32_t kha = smem_u32(stage_of(g) + R::kh);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+        for (int k = 0; k < (DIFF ? D / 32 : D / 16); ++k) {
+          const int kk = DIFF ? C * (D / 32) + k : k;
           const uint32_t ko = (kk >> 2) * (kTcStep * 128) + (kk & 3) * 32;
           const uint32_t qo = (kk >> 2) * (kTcRows * 128) + (kk & 3) * 32;
-          tc_mma_f16(ts, sw128_desc(qa + qo), sw128_desc(kha + ko), id_s, kk > 0);
+          tc_mma_f16(ts, sw128_desc(qa + qo), sw128_desc(kha + ko), id_s, k > 0);
           if constexpr (CH) tc_mma_f16(ts, sw128_desc(qla + qo), sw128_desc(kha + ko), id_s, 1);
         }
         tc_commit(&s_full[C]);
@@ -376,7 +394,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
       };
       int gbase = 0, n_done = 0;  // global steps before the item, items with steps done
       for (int item = blockIdx.x; item < n_items && !*abort_f; item += gridDim.x) {
-        const WsItem it = ws_item<NT>(p, item);
+        const WsItem it = ws_item<IT>(p, item);
         if (it.nsteps <= 0) continue;
         // this item's Q rows are in shared memory
         if (!tc_wait(&q_full[C], n_done & 1, abort_f)) break;
@@ -427,11 +445,18 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
     // zeros for their rows here.
     auto next_item = [&](int from, WsItem& it) -> int {
       for (int i = from; i < n_items; i += gridDim.x) {
-        it = ws_item<NT>(p, i);
+        it = ws_item<IT>(p, i);
         if (it.nsteps < 0) continue;  // no rows in this item
         if (it.bad_ctx && it.row0 == 0 && it.h == 0 && tid == 0) set_error(pool.err, ERR_RANGE);
         if (it.nsteps > 0) return i;
-        const int rr = it.row0 + X * kTcRows + r;
+        const int rr = it.row0 + (DIFF ? 0 : X * kTcRows) + r;
+        if constexpr (DIFF) {
+          if (X == 0 && rr < it.rows_total) {
+            __half* o = p.diff.out + ((int64_t)(it.qbase + rr / p.G) * p.Hq + it.h * p.G + rr % p.G) * D;
+            for (int d = 0; d < D; ++d) o[d] = __ushort_as_half(0);
+          }
+          continue;
+        }
         if (rr < it.rows_total) {
           float* o = p.out + ((int64_t)(it.qbase + rr / p.G) * p.Hq + it.h * p.G + rr % p.G) * D;
           for (int d = 0; d < D; ++d) o[d] = 0.f;
@@ -443,7 +468,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
     // tile's q_full arrival; returns the row's score scale (per-channel pools
     // fold the K channel scale into the row and scale it by a power of two).
     auto load_q = [&](const WsItem& it) -> float {
-      const int rr = it.row0 + X * kTcRows + r;
+      const int rr = it.row0 + (DIFF ? 0 : X * kTcRows) + r;
       const __half* src =
           rr < it.rows_total
               ? p.q + ((int64_t)(it.qbase + rr / p.G) * p.Hq + it.h * p.G + rr % p.G) * D
@@ -454,8 +479,9 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         // whole rows (each row's source address comes from its owner lane);
         // a batch of loads is issued before any of its shared-memory stores,
         // which the compiler may not move loads past
-        constexpr int CPR = D / 8, RPI = 32 / CPR, NI = 32 / RPI, QBATCH = 8;
-        const int cj = lane % CPR, rj = lane / CPR;
+        // (a map's tile has half of the channels)
+        constexpr int CPR = (DIFF ? D / 2 : D) / 8, RPI = 32 / CPR, NI = 32 / RPI, QBATCH = NI < 8 ? NI : 8;
+        const int cj = lane % CPR + (DIFF ? X * CPR : 0), rj = lane / CPR;
 #pragma unroll
         for (int k0 = 0; k0 < NI; k0 += QBATCH) {
           uint4 v[QBATCH];
@@ -503,7 +529,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
     int item = next_item(blockIdx.x, it);
     float csc = item < n_items ? load_q(it) : 0.f;
     for (; item < n_items && !failed;) {
-      const int rr = it.row0 + X * kTcRows + r;
+      const int rr = it.row0 + (DIFF ? 0 : X * kTcRows) + r;
       const bool row_ok = rr < it.rows_total;
       const int lim = row_ok ? max(0, it.ctx - it.nq + rr / p.G + 1) : 0;
       const int64_t orow =
@@ -638,6 +664,16 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
           tc_st16(tP + 16 * hf, hv);
           tc_st16(tP + 32 + 16 * hf, lv);
         }
+        if constexpr (DIFF) {
+          // the other tile has read the last item's O, which the P.V to come overwrites
+          if (j == 0 && n_done > 0) {
+            if (!warp_wait(&x_read[X ^ 1], (n_done - 1) & 1, abort_f)) {
+              failed = true;
+              break;
+            }
+            tc_fence_after();
+          }
+        }
         tc_wait_st();
         tc_fence_before();
         warp_arrive(&p_full[X]);
@@ -655,7 +691,60 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         break;
       }
       tc_fence_after();
-      {
+      if constexpr (DIFF) {
+        float* facs = reinterpret_cast<float*>(sm + PL::oscr);  // [2][kTcRows] factors of the maps' rows
+        float* sums = facs + 2 * kTcRows;                       // [2][kTcRows] sums of squares
+        const int head = it.h * p.G + rr % p.G;
+        const float lam = row_ok ? p.diff.lambda[head] : 0.f;
+        const float f = l > 0.f ? pow2f(-E) / l : 0.f;
+        facs[X * kTcRows + r] = X == 0 ? f : -lam * f;
+        tc_fence_before();
+        warp_arrive(&x_ready[X]);
+        if (!warp_wait(&x_ready[X ^ 1], n_done & 1, abort_f)) {
+          failed = true;
+          break;
+        }
+        tc_fence_after();
+        const float f0 = facs[r], f1 = facs[kTcRows + r];
+        float y[D / 2], ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          float o0[32], o1[32];
+          tc_ld32(tmem + lane_base + X * (D / 2) + 32 * c, o0);
+          tc_ld32(tmem + 128 + lane_base + X * (D / 2) + 32 * c, o1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float v = fmaf(o1[i], f1, o0[i] * f0);
+            y[32 * c + i] = v;
+            ss = fmaf(v, v, ss);
+          }
+        }
+        tc_fence_before();
+        warp_arrive(&x_read[X]);
+        sums[X * kTcRows + r] = ss;
+        warp_arrive(&x_sum[X]);
+        if (!warp_wait(&x_sum[X ^ 1], n_done & 1, abort_f)) {
+          failed = true;
+          break;
+        }
+        const float g = diff_factor<D>(p.diff, sums[r] + sums[kTcRows + r]);
+        if (row_ok) {
+          const float* w = p.diff.weight;
+          uint4* dst = reinterpret_cast<uint4*>(p.diff.out + orow * D + X * (D / 2));
+#pragma unroll
+          for (int i = 0; i < D / 2; i += 8) {
+            __half2 hh[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int d = i + 2 * e;
+              const float w0 = w != nullptr ? g * w[X * (D / 2) + d] : g;
+              const float w1 = w != nullptr ? g * w[X * (D / 2) + d + 1] : g;
+              hh[e] = __floats2half2_rn(y[d] * w0, y[d + 1] * w1);
+            }
+            dst[i / 8] = *reinterpret_cast<const uint4*>(hh);
+          }
+        }
+      } else {
         const float f = l > 0.f ? pow2f(-E) / l : 0.f;
         const float* vch = CH ? pool.chan_scales + ((int64_t)pool.Hkv + it.h) * D : nullptr;
         // Each warp passes 16-column blocks of its 32 rows through shared

@@ -235,6 +235,9 @@ def test_refusals():
     g, qs = kvq.kvq_diff_prefill, _t(np.array([0, 1, 2], np.int32))
     assert status(g, pool.handle, q, qs, 1, T, L, 50, 0.1, lam, out, None) == kvq.KVQ_ERR_WORKSPACE
     assert status(g, pool.handle, q, qs, -1, T, L, 50, 0.1, lam, out, None) == bad
+    big = torch.empty(kvq.kvq_diff_prefill_workspace_bytes(pool.handle, 2, 2, 4, 50), dtype=torch.uint8, device=DEV)
+    odd = torch.empty(2 * 4 * 128 + 1, dtype=torch.float16, device=DEV)[1:].view(2, 4, 128)
+    assert status(g, pool.handle, q, qs, 1, T, L, 50, 0.1, lam, odd, big) == bad
     for name, x in (("lam", lam.double()), ("out", out.float()), ("q", q.float())):
         with pytest.raises(ValueError, match="must be"):
             f(pool.handle, **{**dict(q=q, block_table=T, context_lens=L, max_context_len=50, sm_scale=0.1, lam=lam, out=out, workspace=ws), name: x})
