@@ -210,11 +210,11 @@ struct WsPlan {
   // misc: int abort; uint64 kv_full[S], kv_empty[S], s_full[NT], s_read[NT],
   // p_full[NT], pv_done[NT], o_full[NT], q_full[NT], drain; uint32 tslot
   static constexpr int abort = misc, bars = misc + 8;
-  static constexpr int nbars = 2 * kWsStages + 6 * NT + 1 + 6;  // (the last six: DIFF)
+  static constexpr int nbars = 2 * kWsStages + 6 * NT + 1 + 10;  // (the last ten: DIFF)
   static constexpr int tslot = bars + 8 * nbars;
   // per softmax warp, a 32-row x 16-float block of its output rows on their
   // way to global memory (rows 64 bytes apart, 16-byte chunks swizzled)
-  static constexpr int oscr = misc + 256;
+  static constexpr int oscr = misc + 512;
   static constexpr int OSCR_WARP = 32 * 16 * 4;
   static constexpr int request = oscr + 4 * NT * OSCR_WARP + 1024;  // + alignment slack
   static_assert(tslot + 16 <= oscr, "mbarriers overlap the output blocks");
@@ -266,7 +266,12 @@ __device__ __forceinline__ WsItem ws_item(const PrefillWsParams& p, int i) {
 // done each tile's warps read the same rows of both O -- a warp may read the tensor-memory
 // lanes of its quarter whoever wrote them -- take the difference of their half of the
 // columns, swap the halves' sums of squares and write normed fp16 rows: no expanded Q,
-// no fp32 results in memory.  The tiles meet at three more pairs of mbarriers: O and the
+// no fp32 results in memory.  The results are rounded to fp16, so the weights enter P.V as one
+// fp16 number: each is within 2^-12 of itself, a result's sum of many such (independent)
+// errors within some 2^-12.8 of the map's own length, half of what the rounding of the
+// result itself adds.  That is half the P.V products, and the room of the low parts holds a
+// second P, so that a step's weights are written while the one before is still multiplied.
+// The tiles meet at three more pairs of mbarriers: O and the
 // row's factor there, sums there, O read (only then may the next item's first P.V, which
 // overwrites it, be asked for).
 template <int FMT, int D, bool DIFF = false>
@@ -303,6 +308,13 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
   uint64_t* x_ready = drain + 1;           // DIFF [2]: the tile's O and factors are there
   uint64_t* x_sum = x_ready + 2;           // DIFF [2]: its sums of squares are there
   uint64_t* x_read = x_sum + 2;            // DIFF [2]: it has read both O
+  uint64_t* pv_odd = x_read + 2;           // DIFF [2]: its last P.V of an odd global step done
+  uint64_t* p_odd = pv_odd + 2;            // DIFF [2]: its weights of an odd step are written
+  // (DIFF: pv_done and p_full are those of the even steps.  A warp may be a step ahead of
+  // another of its tile, whose arrival must not be taken for its own.)
+  auto p_bar = [&](int x, int g) { return DIFF && (g & 1) ? &p_odd[x] : &p_full[x]; };
+  auto pv_bar = [&](int x, int g) { return DIFF && (g & 1) ? &pv_odd[x] : &pv_done[x]; };
+  auto pv_par = [](int g) { return DIFF ? (g >> 1) & 1 : g & 1; };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + PL::tslot);
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -319,7 +331,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
     }
     mbar_init(drain, NT);
     if constexpr (DIFF)
-      for (int x = 0; x < 6; ++x) mbar_init(&x_ready[x], kTcRows / 32);
+      for (int x = 0; x < 10; ++x) mbar_init(&x_ready[x], x == 6 || x == 7 ? 1 : kTcRows / 32);
     *abort_f = 0;
     fence_barrier_init();
   }
@@ -384,13 +396,16 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
       };
       auto issue_pv = [&](int g, bool first) {  // O += P V of global step g (P in TMEM)
         const uint32_t vta = smem_u32(stage_of(g) + R::vt);
+        const uint32_t tpg = tp + (DIFF ? 32 * (g & 1) : 0);
 #pragma unroll
         for (int kk = 0; kk < kTcStep / 16; ++kk)
-          tc_mma_f16_ts(to, tp + 8 * kk, sw128_desc(vta + kk * 32), id_o, (!first || kk > 0) ? 1u : 0u);
+          tc_mma_f16_ts(to, tpg + 8 * kk, sw128_desc(vta + kk * 32), id_o, (!first || kk > 0) ? 1u : 0u);
+        if constexpr (!DIFF) {
 #pragma unroll
-        for (int kk = 0; kk < kTcStep / 16; ++kk)
-          tc_mma_f16_ts(to, tp + 32 + 8 * kk, sw128_desc(vta + kk * 32), id_o, 1u);
-        tc_commit(&pv_done[C]);
+          for (int kk = 0; kk < kTcStep / 16; ++kk)
+            tc_mma_f16_ts(to, tp + 32 + 8 * kk, sw128_desc(vta + kk * 32), id_o, 1u);
+        }
+        tc_commit(pv_bar(C, g));
       };
       int gbase = 0, n_done = 0;  // global steps before the item, items with steps done
       for (int item = blockIdx.x; item < n_items && !*abort_f; item += gridDim.x) {
@@ -412,7 +427,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
           }
           if (j > 0) {
             // P.V of step j-1, once the tile's weights are written
-            ok = tc_wait(&p_full[C], (g - 1) & 1, abort_f);
+            ok = tc_wait(p_bar(C, g - 1), pv_par(g - 1), abort_f);
             if (!ok) break;
             tc_fence_after();
             issue_pv(g - 1, j == 1);
@@ -622,15 +637,23 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         const float alpha = fast_exp2(m - ms);
         l = fmaf(l, alpha, (rsa + rsb) * pow2f(-E));
         m = mn;
-        if (g > 0) {
-          // the previous P.V must be done before P is overwritten (and, within
-          // an item, before O is rescaled)
-          if (!warp_wait(&pv_done[X], (g - 1) & 1, abort_f)) {
+        // the last P.V that read this P must be done before it is overwritten (DIFF has two),
+        // and, within an item, the last one before O is rescaled
+        const float f = alpha * pow2f(dE);
+        const bool rescale = j > 0 && (!DIFF || __any_sync(0xffffffffu, f != 1.f));
+        if (DIFF && g > 1) {
+          if (!warp_wait(pv_bar(X, g - 2), pv_par(g - 2), abort_f)) {
             failed = true;
             break;
           }
           tc_fence_after();
-          const float f = alpha * pow2f(dE);
+        }
+        if (DIFF ? rescale : g > 0) {
+          if (!warp_wait(pv_bar(X, g - 1), pv_par(g - 1), abort_f)) {
+            failed = true;
+            break;
+          }
+          tc_fence_after();
           if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -658,11 +681,21 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
               f2_unpack(f2_mul(f2_pack(w0, w1), f2_pack(v4.x, v4.y)), w0, w1);
               f2_unpack(f2_mul(f2_pack(w2, w3), f2_pack(v4.z, v4.w)), w2, w3);
             }
-            tc_split2(w0, w1, hv[c], lv[c]);
-            tc_split2(w2, w3, hv[c + 1], lv[c + 1]);
+            if constexpr (DIFF) {
+              const __half2 a = __floats2half2_rn(w0, w1), b = __floats2half2_rn(w2, w3);
+              hv[c] = *reinterpret_cast<const uint32_t*>(&a);
+              hv[c + 1] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+              tc_split2(w0, w1, hv[c], lv[c]);
+              tc_split2(w2, w3, hv[c + 1], lv[c + 1]);
+            }
           }
-          tc_st16(tP + 16 * hf, hv);
-          tc_st16(tP + 32 + 16 * hf, lv);
+          if constexpr (DIFF) {
+            tc_st16(tP + 32 * (g & 1) + 16 * hf, hv);
+          } else {
+            tc_st16(tP + 16 * hf, hv);
+            tc_st16(tP + 32 + 16 * hf, lv);
+          }
         }
         if constexpr (DIFF) {
           // the other tile has read the last item's O, which the P.V to come overwrites
@@ -676,7 +709,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         }
         tc_wait_st();
         tc_fence_before();
-        warp_arrive(&p_full[X]);
+        warp_arrive(p_bar(X, g));
       }
       if (failed) break;
       // ---- the next item's Q now (the S products of this item, the last
