@@ -28,21 +28,22 @@
 // thread, one TMEM lane each); a copier thread bulk-copies the step records
 // into four shared-memory stages the moment each is free, running ahead
 // across items, and one control thread per tile issues that tile's
-// tcgen05.mma.  Per tile, tensor memory holds the output accumulator O, the
-// step's scores S and the step's weights P:
+// tcgen05.mma.  Per tile, tensor memory holds the output accumulator O and two
+// buffers in which a step's scores S become its weights P:
 //   * the control thread issues S = Q.K^T (M 128, N 64, K D, A and B from
-//     shared memory) for every tile once the step's record has landed and the
-//     tile has read its previous S;
-//   * each softmax thread reads its row of S, signals that S may be
-//     overwritten, applies the K scales, the causal limit and the online
-//     softmax (base 2), and writes the weights p * s_V * 2^E as fp16 high and
-//     low parts into P with tcgen05.st; the row's exponent reference moves
-//     only when a score passes it by more than 2^8, and only then (or when E
-//     drops) is its row of O rescaled;
+//     shared memory) of a step behind the P.V of the step two before it, whose
+//     buffer it takes, once its record has landed;
+//   * each softmax thread reads its row of S, applies the K scales, the causal
+//     limit and the online softmax (base 2), and writes the weights p * s_V * 2^E
+//     as fp16 high and low parts over it with tcgen05.st; the row's exponent
+//     reference moves only when a score passes it by more than 2^8, and only then
+//     (or when E drops) does it wait for the last P.V and rescale its row of O;
 //   * the control thread then issues O += P_hi.V + P_lo.V (M 128, N D, K 64,
 //     A from tensor memory, V^T from shared memory).
-// So the next step's S is computed while the softmax of the current one runs,
-// and the two tiles' softmax and tensor work interleave.  The next item's Q
+// So a tile's next S is there before its softmax is done with this one, and no
+// softmax warp waits for a P.V.  (With one S and one P buffer it waited for the last
+// P.V before it could write the weights: 8 x 2048, 4-bit floats, 436 us.)  The two
+// tiles' softmax and tensor work interleave.  The next item's Q
 // rows are loaded before the current item's epilogue, whose output rows go
 // out through a per-warp shared-memory transpose.  The threads meet
 // only at mbarriers; every wait is bounded and gives up early once another
@@ -187,6 +188,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return ok;
 }
 
+// The same for two barriers, a lane each, in one loop.
+__device__ __forceinline__ bool warp_wait2(uint64_t* b0, uint32_t p0, uint64_t* b1, uint32_t p1,
+                                           volatile int* abort) {
+  const int lane = threadIdx.x & 31;
+  uint64_t* bar = lane == 0 ? b0 : b1;
+  const uint32_t parity = lane == 0 ? p0 : p1;
+  bool mine = lane > 1;
+  for (int i = 0; i < kSpinPolls; ++i) {
+    if (!mine) mine = mbar_test_wait(bar, parity);
+    if (__all_sync(0xffffffffu, mine)) {
+      __syncwarp();  // the other lanes' accesses come after each lane's acquire
+      return true;
+    }
+    if ((i & 255) == 255 && __any_sync(0xffffffffu, lane == 0 && *abort)) return false;
+  }
+  if (!mine) mine = tc_wait_suspend(bar, parity, abort);
+  mine = __all_sync(0xffffffffu, mine);
+  __syncwarp();
+  return mine;
+}
+
 // One arrival for the whole warp, after every lane's prior work (a warp-wide
 // arrive would be 32 atomic updates of the same word).  The lanes' shared
 // memory writes, tensor memory accesses (each lane fenced with
@@ -207,10 +229,10 @@ struct WsPlan {
   static constexpr int q = 0;
   static constexpr int stage = NT * QB * (CH ? 2 : 1);     // [kWsStages][R::bytes]
   static constexpr int misc = stage + kWsStages * R::bytes;
-  // misc: int abort; uint64 kv_full[S], kv_empty[S], s_full[NT], s_read[NT],
-  // p_full[NT], pv_done[NT], o_full[NT], q_full[NT], drain; uint32 tslot
+  // misc: int abort; uint64 kv_full[S], kv_empty[S], s_full[NT][2], p_full[NT][2],
+  // pv_done[NT][2], o_full[NT], q_full[NT], drain, DIFF's six; uint32 tslot
   static constexpr int abort = misc, bars = misc + 8;
-  static constexpr int nbars = 2 * kWsStages + 6 * NT + 1 + 10;  // (the last ten: DIFF)
+  static constexpr int nbars = 2 * kWsStages + 8 * NT + 1 + 6;
   static constexpr int tslot = bars + 8 * nbars;
   // per softmax warp, a 32-row x 16-float block of its output rows on their
   // way to global memory (rows 64 bytes apart, 16-byte chunks swizzled)
@@ -221,9 +243,9 @@ struct WsPlan {
   // the softmax warps, one control warp per tile (its lane 0 issues that
   // tile's MMAs) and a copier warp (its lane 0 issues the record copies)
   static constexpr int threads = kTcRows * NT + 32 * NT + 32;
-  // TMEM: per tile x, O at 128x (D columns), S at 256 + 128x (64), P at S + 64
-  // (32 columns of fp16 pairs for the high part, 32 for the low part); one
-  // tile: O 0, S 128, P 192
+  // TMEM: per tile x, O at 128x (D columns), the two buffers at 256 + 128x: S (64), then P
+  // over it (32 columns of fp16 pairs for the high part, 32 for the low part); one
+  // tile: O 0, buffers 128
   static constexpr int cols = NT == 2 ? 512 : 256;
   static constexpr int s_col(int x) { return NT == 2 ? 256 + 128 * x : 128; }
 };
@@ -269,9 +291,7 @@ __device__ __forceinline__ WsItem ws_item(const PrefillWsParams& p, int i) {
 // no fp32 results in memory.  The results are rounded to fp16, so the weights enter P.V as one
 // fp16 number: each is within 2^-12 of itself, a result's sum of many such (independent)
 // errors within some 2^-12.8 of the map's own length, half of what the rounding of the
-// result itself adds.  That is half the P.V products, and the room of the low parts holds a
-// second P, so that a step's weights are written while the one before is still multiplied.
-// The tiles meet at three more pairs of mbarriers: O and the
+// result itself adds.  That is half the P.V products.  The tiles meet at three more pairs of mbarriers: O and the
 // row's factor there, sums there, O read (only then may the next item's first P.V, which
 // overwrites it, be asked for).
 template <int FMT, int D, bool DIFF = false>
@@ -282,6 +302,9 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
   constexpr int NT = WsShape<FMT>::NT;
   static_assert(!DIFF || NT == 2, "two maps");
   constexpr int IT = DIFF ? 1 : NT;  // 128-row tiles of rows per item
+  // Two softmax warps share a scheduler, so a warp's own latencies count: fewer waits, one
+  // load of the scores, shorter chains.  (The other formats keep their order of sums.)
+  constexpr bool FAST = DIFF || FMT == FMT_FP4;
   constexpr int NS = kWsStages;
   using PL = WsPlan<D, NT, CH>;
   using R = StepRec<D>;
@@ -298,23 +321,21 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + PL::bars);
   uint64_t* kv_full = bars;                // [NS]: the step's record landed
   uint64_t* kv_empty = bars + NS;          // [NS]: every tile's MMAs of the step in that stage done
-  uint64_t* s_full = bars + 2 * NS;        // [NT]: S of the tile's current step
-  uint64_t* s_read = s_full + NT;          // [NT]: the tile's 4 warps have read S
-  uint64_t* p_full = s_read + NT;          // [NT]: the tile's 4 warps have written P
-  uint64_t* pv_done = p_full + NT;         // [NT]: the tile's last issued P.V done
-  uint64_t* o_full = pv_done + NT;         // [NT]: the tile's final P.V of an item done
+  uint64_t* s_full = bars + 2 * NS;        // [NT][2]: S of a step (by its parity)
+  uint64_t* p_full = s_full + 2 * NT;      // [NT][2]: the tile's 4 warps have written its P
+  uint64_t* pv_done = p_full + 2 * NT;     // [NT][2]: its P.V done
+  uint64_t* o_full = pv_done + 2 * NT;     // [NT]: the tile's final P.V of an item done
   uint64_t* q_full = o_full + NT;          // [NT]: the tile's Q rows of an item written
   uint64_t* drain = q_full + NT;           // clean-up
   uint64_t* x_ready = drain + 1;           // DIFF [2]: the tile's O and factors are there
   uint64_t* x_sum = x_ready + 2;           // DIFF [2]: its sums of squares are there
   uint64_t* x_read = x_sum + 2;            // DIFF [2]: it has read both O
-  uint64_t* pv_odd = x_read + 2;           // DIFF [2]: its last P.V of an odd global step done
-  uint64_t* p_odd = pv_odd + 2;            // DIFF [2]: its weights of an odd step are written
-  // (DIFF: pv_done and p_full are those of the even steps.  A warp may be a step ahead of
-  // another of its tile, whose arrival must not be taken for its own.)
-  auto p_bar = [&](int x, int g) { return DIFF && (g & 1) ? &p_odd[x] : &p_full[x]; };
-  auto pv_bar = [&](int x, int g) { return DIFF && (g & 1) ? &pv_odd[x] : &pv_done[x]; };
-  auto pv_par = [](int g) { return DIFF ? (g >> 1) & 1 : g & 1; };
+  // A warp may be a step ahead of another of its tile, so a step's barriers are those of its
+  // parity, whose phases count every other step.
+  auto s_bar = [&](int x, int g) { return &s_full[2 * x + (g & 1)]; };
+  auto p_bar = [&](int x, int g) { return &p_full[2 * x + (g & 1)]; };
+  auto pv_bar = [&](int x, int g) { return &pv_done[2 * x + (g & 1)]; };
+  auto par2 = [](int g) { return static_cast<uint32_t>(g >> 1) & 1u; };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + PL::tslot);
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -322,16 +343,17 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
       mbar_init(&kv_empty[i], NT);
     }
     for (int x = 0; x < NT; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&s_read[x], kTcRows / 32);  // one arrival per warp
-      mbar_init(&p_full[x], kTcRows / 32);  // one arrival per warp
-      mbar_init(&pv_done[x], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&s_full[2 * x + b], 1);
+        mbar_init(&p_full[2 * x + b], kTcRows / 32);  // one arrival per warp
+        mbar_init(&pv_done[2 * x + b], 1);
+      }
       mbar_init(&o_full[x], 1);
       mbar_init(&q_full[x], kTcRows / 32);  // one arrival per warp
     }
     mbar_init(drain, NT);
     if constexpr (DIFF)
-      for (int x = 0; x < 10; ++x) mbar_init(&x_ready[x], x == 6 || x == 7 ? 1 : kTcRows / 32);
+      for (int x = 0; x < 6; ++x) mbar_init(&x_ready[x], kTcRows / 32);
     *abort_f = 0;
     fence_barrier_init();
   }
@@ -379,10 +401,10 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
       constexpr uint32_t id_o = tc_idesc_f16(128, D);
       const uint32_t qa = smem_u32(sm + PL::q + C * PL::QB);
       const uint32_t qla = smem_u32(sm + PL::q + (NT + C) * PL::QB);
-      const uint32_t ts = tmem + PL::s_col(C);
-      const uint32_t tp = ts + 64;
+      const uint32_t tb = tmem + PL::s_col(C);
       const uint32_t to = tmem + C * 128;
       auto issue_s = [&](int g) {  // S = Q K^T of global step g
+        const uint32_t ts = tb + 64 * (g & 1);
         const uint32_t kha = smem_u32(stage_of(g) + R::kh);
 #pragma unroll
         for (int k = 0; k < (DIFF ? D / 32 : D / 16); ++k) {
@@ -392,14 +414,14 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
           tc_mma_f16(ts, sw128_desc(qa + qo), sw128_desc(kha + ko), id_s, k > 0);
           if constexpr (CH) tc_mma_f16(ts, sw128_desc(qla + qo), sw128_desc(kha + ko), id_s, 1);
         }
-        tc_commit(&s_full[C]);
+        tc_commit(s_bar(C, g));
       };
       auto issue_pv = [&](int g, bool first) {  // O += P V of global step g (P in TMEM)
         const uint32_t vta = smem_u32(stage_of(g) + R::vt);
-        const uint32_t tpg = tp + (DIFF ? 32 * (g & 1) : 0);
+        const uint32_t tp = tb + 64 * (g & 1);
 #pragma unroll
         for (int kk = 0; kk < kTcStep / 16; ++kk)
-          tc_mma_f16_ts(to, tpg + 8 * kk, sw128_desc(vta + kk * 32), id_o, (!first || kk > 0) ? 1u : 0u);
+          tc_mma_f16_ts(to, tp + 8 * kk, sw128_desc(vta + kk * 32), id_o, (!first || kk > 0) ? 1u : 0u);
         if constexpr (!DIFF) {
 #pragma unroll
           for (int kk = 0; kk < kTcStep / 16; ++kk)
@@ -413,27 +435,26 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         if (it.nsteps <= 0) continue;
         // this item's Q rows are in shared memory
         if (!tc_wait(&q_full[C], n_done & 1, abort_f)) break;
-        bool ok = true;
-        for (int j = 0; j <= it.nsteps && ok; ++j) {
+        // S of a step once its record has landed; its buffer's last reader, the P.V two steps
+        // before, has been issued by then (and runs before it)
+        auto next_s = [&](int j) {
           const int g = gbase + j;
-          if (j < it.nsteps) {
-            // S of step j, once its record has landed and the tile has read
-            // its previous S
-            ok = tc_wait(&kv_full[g % NS], (g / NS) & 1, abort_f) &&
-                 (g == 0 || tc_wait(&s_read[C], (g - 1) & 1, abort_f));
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(g);
-          }
-          if (j > 0) {
-            // P.V of step j-1, once the tile's weights are written
-            ok = tc_wait(p_bar(C, g - 1), pv_par(g - 1), abort_f);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(g - 1, j == 1);
-            if (j == it.nsteps) tc_commit(&o_full[C]);
-            tc_commit(&kv_empty[(g - 1) % NS]);  // this tile's MMAs reading that stage are issued
-          }
+          if (!tc_wait(&kv_full[g % NS], (g / NS) & 1, abort_f)) return false;
+          tc_fence_after();
+          issue_s(g);
+          return true;
+        };
+        bool ok = next_s(0) && (it.nsteps == 1 || next_s(1));
+        for (int j = 0; j < it.nsteps && ok; ++j) {
+          const int g = gbase + j;
+          // P.V once the tile's weights are written
+          ok = tc_wait(p_bar(C, g), par2(g), abort_f);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(g, j == 0);
+          if (j + 1 == it.nsteps) tc_commit(&o_full[C]);
+          tc_commit(&kv_empty[g % NS]);  // this tile's MMAs reading that stage are issued
+          if (j + 2 < it.nsteps) ok = next_s(j + 2);
         }
         if (!ok) break;
         gbase += it.nsteps;
@@ -450,8 +471,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
     const int r = (warp & 3) * 32 + lane;
     const uint32_t tO = tmem + X * 128;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tS = tmem + PL::s_col(X) + lane_base;
-    const uint32_t tP = tS + 64;
+    const uint32_t tB = tmem + PL::s_col(X) + lane_base;
     char* qx = sm + PL::q + X * PL::QB;
     char* ql = sm + PL::q + (NT + X) * PL::QB;
     bool failed = false;
@@ -555,15 +575,23 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         const int g = gbase + j;
         const char* st = stage_of(g);
         // S of this step (its record's scales and mask landed before it)
-        if (!warp_wait(&s_full[X], g & 1, abort_f) ||
-            !warp_wait(&kv_full[g % NS], (g / NS) & 1, abort_f)) {
+        if constexpr (FAST) {
+          if (!warp_wait2(s_bar(X, g), par2(g), &kv_full[g % NS], (g / NS) & 1, abort_f)) {
+            failed = true;
+            break;
+          }
+        } else if (!warp_wait(s_bar(X, g), par2(g), abort_f) ||
+                   !warp_wait(&kv_full[g % NS], (g / NS) & 1, abort_f)) {
           failed = true;
           break;
         }
         tc_fence_after();
+        const uint32_t tS = tB + 64 * (g & 1);  // S, and P over it
         const int t0 = j * kTcStep;
         float z[kTcStep];
-        {
+        if constexpr (FAST) {
+          tc_ld64(tS, z);
+        } else {
           float a[32];
           tc_ld32(tS, a);
 #pragma unroll
@@ -572,14 +600,15 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
 #pragma unroll
           for (int i = 0; i < 32; ++i) z[32 + i] = a[i];
         }
-        tc_fence_before();
-        warp_arrive(&s_read[X]);  // the next S may go into this buffer
         const float* ksb = reinterpret_cast<const float*>(st + R::ks);
         const float* vsb = reinterpret_cast<const float*>(st + R::vs);
         const uint32_t mk0 = reinterpret_cast<const uint32_t*>(st + R::mask)[0];
         const uint32_t mk1 = reinterpret_cast<const uint32_t*>(st + R::mask)[1];
         const int lr = lim - t0;  // tokens [0, lr) of this step are attended by this row
         float mx = kNegInf;
+        float mq[FAST ? 4 : 1];  // (FAST: four chains for the maximum, and for the sum)
+#pragma unroll
+        for (float& v : mq) v = kNegInf;
         if (lr >= kTcStep && (mk0 & mk1) == 0xffffffffu) {
 #pragma unroll
           for (int t = 0; t < kTcStep; t += 4) {
@@ -593,16 +622,20 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
             z[t + 1] = a1;
             z[t + 2] = a2;
             z[t + 3] = a3;
-            mx = fmax3(fmax3(mx, a0, a1), a2, a3);
+            float& mc = mq[FAST ? (t >> 2) & 3 : 0];
+            mc = fmax3(fmax3(mc, a0, a1), a2, a3);
           }
         } else {
 #pragma unroll
           for (int t = 0; t < kTcStep; ++t) {
             const bool okt = t < lr && (((t < 32 ? mk0 : mk1) >> (t & 31)) & 1u);
             z[t] = okt ? (T::row_scales ? z[t] * ksb[t] : z[t]) : kNegInf;
-            mx = fmaxf(mx, z[t]);
+            float& mc = mq[FAST ? t & 3 : 0];
+            mc = fmaxf(mc, z[t]);
           }
         }
+        mx = mq[0];
+        if constexpr (FAST) mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
         // scores in log2 units are z * csc (csc > 0); the reference maximum m
         // moves only when the step's maximum passes it by more than kTcSlack
         const float mxz = mx == kNegInf ? kNegInf : mx * csc;
@@ -620,7 +653,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         }
         // p' = 2^(z csc - ms + E), the weight before the V scale
         const float nbias = static_cast<float>(E) - ms;
-        uint64_t rs2 = f2_pack(0.f, 0.f);
+        uint64_t rs2 = f2_pack(0.f, 0.f), rsq[FAST ? 3 : 1] = {};
         {
           const uint64_t c2 = f2_pack(csc, csc), b2 = f2_pack(nbias, nbias);
 #pragma unroll
@@ -629,40 +662,32 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
             f2_unpack(f2_fma(f2_pack(z[t], z[t + 1]), c2, b2), a0, a1);
             z[t] = fast_exp2(a0);  // 0 for masked tokens
             z[t + 1] = fast_exp2(a1);
-            rs2 = f2_add(rs2, f2_pack(z[t], z[t + 1]));
+            const int q = FAST ? (t >> 1) & 3 : 0;
+            uint64_t& rc = q == 0 ? rs2 : rsq[q - (FAST ? 1 : 0)];
+            rc = f2_add(rc, f2_pack(z[t], z[t + 1]));
           }
         }
+        if constexpr (FAST) rs2 = f2_add(f2_add(rs2, rsq[0]), f2_add(rsq[1], rsq[2]));
         float rsa, rsb;
         f2_unpack(rs2, rsa, rsb);
         const float alpha = fast_exp2(m - ms);
         l = fmaf(l, alpha, (rsa + rsb) * pow2f(-E));
         m = mn;
-        // the last P.V that read this P must be done before it is overwritten (DIFF has two),
-        // and, within an item, the last one before O is rescaled
+        // within an item, O is rescaled once the last P.V is done
         const float f = alpha * pow2f(dE);
-        const bool rescale = j > 0 && (!DIFF || __any_sync(0xffffffffu, f != 1.f));
-        if (DIFF && g > 1) {
-          if (!warp_wait(pv_bar(X, g - 2), pv_par(g - 2), abort_f)) {
+        if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          if (!warp_wait(pv_bar(X, g - 1), par2(g - 1), abort_f)) {
             failed = true;
             break;
           }
           tc_fence_after();
-        }
-        if (DIFF ? rescale : g > 0) {
-          if (!warp_wait(pv_bar(X, g - 1), pv_par(g - 1), abort_f)) {
-            failed = true;
-            break;
-          }
-          tc_fence_after();
-          if (j > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float o[32];
-              tc_ld32(tO + lane_base + 32 * c, o);
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tc_ld32(tO + lane_base + 32 * c, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= f;
-              tc_st32(tO + lane_base + 32 * c, o);
-            }
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tc_st32(tO + lane_base + 32 * c, o);
           }
         }
         // the weights w = p' * s_V as fp16 hi + lo pairs into P (two halves of
@@ -691,10 +716,10 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
             }
           }
           if constexpr (DIFF) {
-            tc_st16(tP + 32 * (g & 1) + 16 * hf, hv);
+            tc_st16(tS + 16 * hf, hv);
           } else {
-            tc_st16(tP + 16 * hf, hv);
-            tc_st16(tP + 32 + 16 * hf, lv);
+            tc_st16(tS + 16 * hf, hv);
+            tc_st16(tS + 32 + 16 * hf, lv);
           }
         }
         if constexpr (DIFF) {
