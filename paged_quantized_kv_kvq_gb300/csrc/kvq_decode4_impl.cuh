@@ -32,13 +32,6 @@ constexpr int kDecode4Ctas = 3;    // resident per SM
 constexpr bool decode4_dup(int G) { return G <= 4; }
 constexpr float kDecode4Exp = 14;  // weights are 2^14 p, so that their low parts stay normal fp16
 
-// fp16 pair of (a, b), or with less = -1 of what that pair leaves of them.
-__device__ __forceinline__ uint32_t part_h2(float a, float b, float less) {
-  const __half2 h = __floats2half2_rn(a, b);
-  const __half2 r = __floats2half2_rn(fmaf(__low2float(h), less, a), fmaf(__high2float(h), less, b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 template <int D, bool DUP, bool DIFF>
 __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
     kvq_decode4_kernel(const __grid_constant__ DecodeParams p) {
@@ -247,7 +240,6 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
   // positive (its sign goes to q; zero is a zero q), so that it leaves the order of scores.
   const float csc0 = p.sm_scale_log2, csc = csc0 == 0.f ? 1.f : fabsf(csc0);
   uint32_t qb[KS][2];
-  const float less = DUP && j >= 2 ? -1.f : 0.f;  // these lanes carry low parts
   float m[2], l[2], o[KS][4];
   Cursor4 cc = locate(a0);
   const Cursor4 first = cc;

@@ -15,9 +15,9 @@
 // a run does not fill is merged into the page (V nibbles by atomics: other warps may
 // hold its other tokens).
 // Bound: HBM (4 bytes a channel in, 1.125 out, for K and V together) and close behind it
-// the instructions, some 450 for the 64 values of a lane.  Measured, 16384 tokens x 8 heads
-// of 128: whole blocks 18.0 us (86 MB, 0.70 of the copy rate), from inside a block 18.2,
-// single tokens 78; read back 17.5, 18.8 and 48.  (Sub-tile by sub-tile of the 16 tokens
+// the instructions, some 700 for the 64 values of a lane (counted: issue slots 60% busy,
+// DRAM 45%).  Measured, 16384 tokens x 8 heads of 128: whole blocks 16.9 us (86 MB, 0.75 of
+// the copy rate), from inside a block 17.1, single tokens 76; read back 17.2, 18.2 and 47.  (Sub-tile by sub-tile of the 16 tokens
 // instead of runs: 16.6 us for whole blocks, but 32 from inside a block and 235 for
 // single tokens.)
 #include "kvq_context.h"
@@ -57,6 +57,17 @@ __device__ __forceinline__ uint2 quant16_fp4(const uint4 (&raw)[2], float inv) {
                     prmt(prmt(b[4], b[5], 0x0040u), prmt(b[6], b[7], 0x0040u), 0x5410u));
 }
 
+// fp4_scale_code of an fp16 value without the division: the same argument with 6 for s and
+// the middle between two scales (5 bits) for the border holds amax / 6 off every middle
+// that it is not by 1/2047 of itself, so amax * (1/6) rounded to 14 mantissa bits is on the
+// same side of it or on it.  (Below 2^-14 middles are multiples of 2^-18, which that leaves
+// exact, too.)
+__device__ __forceinline__ uint32_t scale_code16(float amax) {
+  const uint32_t y = __float_as_uint(fminf(amax * 0.16666667f, 10240.f)), u = (y + 0x100u) & ~0x1FFu;
+  const uint32_t sub = __float2uint_rn(__uint_as_float(u) * 131072.f);  // steps of 2^-17
+  return u < 0x38800000u ? sub : ((u + 0x7FFFFu + (u >> 20 & 1u)) >> 20) - (112u << 3);
+}
+
 __device__ __forceinline__ float absmax16(const uint4 (&raw)[2]) {
   const uint32_t h[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
   __half2 m = __half2half2(__ushort_as_half(0));
@@ -89,17 +100,14 @@ struct Runs {
 
   __device__ __forceinline__ Runs(const int64_t* slots, int64_t i0, int64_t T, int64_t limit, int* err) {
     const int lane = threadIdx.x & 31;
-    auto get = [&](int64_t i) {
-      const int64_t s = i >= 0 && i < T ? slots[i] : -1;
-      return s < limit ? s : -1;
-    };
     slot = i0 + lane < T ? slots[i0 + lane] : -1;
+    const int64_t before = lane == 0 && i0 > 0 ? slots[i0 - 1] : -1;
     if (slot >= limit) {
       set_error(err, ERR_RANGE);
       slot = -1;
     }
     int64_t prev = __shfl_up_sync(0xffffffffu, slot, 1);
-    if (lane == 0) prev = get(i0 - 1);
+    if (lane == 0) prev = before < limit ? before : -1;
     const bool cont = slot >= 0 && slot == prev + 1 && (slot & 15) != 0;
     follows = __ballot_sync(0xffffffffu, cont);
     leaders = __ballot_sync(0xffffffffu, slot >= 0 && !cont) & 0xFFFFu;
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(kRows4Threads) kvq_append4_kernel(PoolView poo
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      sc[c] = fp4_scale_code(absmax16(raw[c]));
+      sc[c] = scale_code16(absmax16(raw[c]));
       const float s = fp4_scale_value(sc[c]);
       const uint2 q = quant16_fp4(raw[c], s != 0.f ? __fdividef(1.f, s) : 0.f);
       lo[c] = q.x;

@@ -229,6 +229,23 @@ def test_codes_at_the_borders(way, T):
     pool.close()
 
 
+@pytest.mark.parametrize("T", [496, 3968])
+def test_the_scale_of_every_absmax(T):
+    """Every finite fp16 value as a group's largest (all 31744, or the 3968 smallest), by the
+    long and the short form."""
+    x = np.random.default_rng(4).uniform(-1, 1, (T * 8, 16))
+    x[:, 5] = -1
+    x = x * np.arange(T * 8, dtype=np.uint16).view(np.float16).astype(np.float64)[:, None]
+    x = x.astype(np.float16).reshape(T, 1, 128)
+    slots = np.arange(T, dtype=np.int64)
+    pool = kvq.KVPool(T // 16, 16, 1, 128, FMT, device=DEV)
+    ref = Fp4Cache(T // 16, 16, 1, 128)
+    pool.append(_t(x), _t(x[:, :, ::-1]), _t(slots))
+    ref.append(x, x[:, :, ::-1], slots)
+    _check(pool, ref, slots)
+    pool.close()
+
+
 def test_values_beyond_fp16_saturate():
     """bf16 rows reach 3e38: the largest scale, the largest code."""
     x = torch.randn((32, 1, 64), device=DEV).bfloat16()
