@@ -30,6 +30,20 @@ namespace {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
+// CTAs of a cluster (of 8 instead: 32768 rows of 512 sequences 8.1 us where 16 take 6.0, 16384
+// freed entries 7.1 and 5.1; small calls alike).
+constexpr int kPlanCluster = 16;
+// Rows and table entries up to which one CTA does it alone, without the cluster's barriers.
+// Rows, alone and as a cluster: 64 3.0 and 4.1 us, 512 3.2 and 3.7, 1024 4.4 and 4.4, 2048
+// 5.6 and 4.4.  Entries (the host does not know how many go; a tenth): 2048 3.2 and 5.0,
+// 8192 3.2 and 4.9, 16384 4.4 and 5.0, 32768 5.5 and 5.2; all of 16384: 20 and 5.2.
+constexpr int kPlanAlone = 1024;
+constexpr int64_t kPlanAloneEntries = 16384;
+// Neighbouring entries a thread frees at a time (1, 2, 4: alone, 768 of 8192 4.1, 3.2 and 3.6
+// us), and rows a thread of a cluster's (alone 1: 64 rows take 3.0, 3.6 and 4.4 us).  Both
+// calls for 512 sequences, 64 ended and 64 begun with up to 1024 tokens, with 1, 2 and 4 of
+// each: 17.2, 12.6 and 14.5 us (1 with 8 CTAs).
+constexpr int kPlanEntries = 2, kPlanRows = 2;
 constexpr uint32_t kPlanCap = 0x7fffffffu;  // prefix sums stop here
 
 // a + b of two sums that are at most the cap, at most the cap (associative).
@@ -74,6 +88,7 @@ __device__ __forceinline__ int last_at_most(const uint32_t* first, int n, uint32
   return lo;
 }
 
+template <int R>
 __global__ void __launch_bounds__(kPlanThreads) kvq_extend_kernel(const __grid_constant__ ExtendArgs p,
                                                                  int bs_log2) {
   extern __shared__ uint32_t smem[];
@@ -86,21 +101,16 @@ __global__ void __launch_bounds__(kPlanThreads) kvq_extend_kernel(const __grid_c
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
   const int bs = 1 << bs_log2;
 
-  int count = *p.count;
-  if (count < 0 || count > p.capacity) {
-    if (rank == 0 && tid == 0) set_error(p.err, ERR_RANGE);
-    count = min(max(count, 0), p.capacity);
-  }
+  const int given = *p.count, count = min(max(given, 0), p.capacity);
   // ---- prefix sums; who is served
   uint2 carry = make_uint2(0, 0);
   uint32_t served = 0;  // blocks that served sequences take
+  int L_next = tid < S ? p.lens[tid] : 0, n_next = tid < S ? p.n[tid] : 0;
   for (int base = 0; base < S; base += kPlanThreads) {
-    const int s = base + tid;
-    int L = 0, n = 0;
-    if (s < S) {
-      L = p.lens[s];
-      n = p.n[s];
-    }
+    const int s = base + tid, L = L_next, n = n_next;
+    const bool more = s + kPlanThreads < S;  // (loaded while this turn's sums are made)
+    L_next = more ? p.lens[s + kPlanThreads] : 0;
+    n_next = more ? p.n[s + kPlanThreads] : 0;
     const bool ok = n >= 0 && L >= 0 && (int64_t)L + n <= (int64_t)p.max_blocks << bs_log2;
     const uint32_t need = ok ? static_cast<uint32_t>((((int64_t)L + n + bs - 1) >> bs_log2) - (((int64_t)L + bs - 1) >> bs_log2)) : 0;
     uint2 all;
@@ -133,7 +143,10 @@ __global__ void __launch_bounds__(kPlanThreads) kvq_extend_kernel(const __grid_c
   // every CTA has read the lengths and the count
   if (ranks > 1) cluster.sync();
   const int step = ranks * kPlanThreads, me = rank * kPlanThreads + tid;
-  if (me == 0) *p.count_out = count - static_cast<int>(served);
+  if (me == 0) {
+    if (given != count) set_error(p.err, ERR_RANGE);
+    *p.count_out = count - static_cast<int>(served);
+  }
   for (int s = me; s <= S; s += step) {
     p.q_start[s] = static_cast<int>(rows[s]);
     if (s == S) break;
@@ -150,28 +163,57 @@ __global__ void __launch_bounds__(kPlanThreads) kvq_extend_kernel(const __grid_c
     if (!pool_block(id)) set_error(p.err, ERR_RANGE);
     p.table[(int64_t)s * p.max_blocks + j] = id;
   }
-  // ---- rows
-  for (int64_t r = me; r < p.max_tokens; r += step) {
-    int64_t slot = -1, pos = 0;
-    if (r < rows[S]) {
-      const int s = last_at_most(rows, S, static_cast<uint32_t>(r));
+  // ---- rows, R neighbours at a time: one search, their lookups side by side
+  const int64_t last = rows[S];
+  for (int64_t r0 = (int64_t)me * R; r0 < p.max_tokens; r0 += (int64_t)step * R) {
+    int64_t slot[R], pos[R];
+    int id[R];
+    int s = r0 < last ? last_at_most(rows, S, static_cast<uint32_t>(r0)) : 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t r = r0 + i;
+      slot[i] = -1;
+      pos[i] = 0;
+      id[i] = 0;
+      if (r >= last) continue;
+      if (rows[s + 1] <= r) s = last_at_most(rows, S, static_cast<uint32_t>(r));
       const int L = len[s];
-      pos = (L >= 0 ? L : ~L) + (r - rows[s]);
-      if (L >= 0) {
-        const int64_t held = ((int64_t)L + bs - 1) >> bs_log2, j = pos >> bs_log2;
-        const int id = j < held ? p.table[(int64_t)s * p.max_blocks + j]
-                                : p.free_list[count - 1 - static_cast<int>(taken[s] + (j - held))];
-        if (pool_block(id)) slot = ((int64_t)id << bs_log2) + (pos & (bs - 1));
-        else set_error(p.err, ERR_RANGE);
+      pos[i] = (L >= 0 ? L : ~L) + (r - rows[s]);
+      if (L < 0) continue;
+      const int64_t held = ((int64_t)L + bs - 1) >> bs_log2, j = pos[i] >> bs_log2;
+      id[i] = j < held ? p.table[(int64_t)s * p.max_blocks + j]
+                       : p.free_list[count - 1 - static_cast<int>(taken[s] + (j - held))];
+      slot[i] = pos[i] & (bs - 1);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (slot[i] < 0) continue;
+      if (pool_block(id[i])) slot[i] += (int64_t)id[i] << bs_log2;
+      else {
+        slot[i] = -1;
+        set_error(p.err, ERR_RANGE);
       }
     }
-    p.slots[r] = slot;
-    p.positions[r] = pos;
+    if (R % 2 == 0 && p.wide && r0 + R <= p.max_tokens) {
+#pragma unroll
+      for (int i = 0; i + 1 < R; i += 2) {
+        *reinterpret_cast<longlong2*>(p.slots + r0 + i) = make_longlong2(slot[i], slot[i + 1]);
+        *reinterpret_cast<longlong2*>(p.positions + r0 + i) = make_longlong2(pos[i], pos[i + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (r0 + i >= p.max_tokens) break;
+        p.slots[r0 + i] = slot[i];
+        p.positions[r0 + i] = pos[i];
+      }
+    }
   }
 }
 
 __global__ void __launch_bounds__(kPlanThreads) kvq_release_kernel(const __grid_constant__ ReleaseArgs p,
                                                                   int bs_log2) {
+  constexpr int R = kPlanEntries;
   extern __shared__ uint32_t smem[];
   const int S = p.S, tid = threadIdx.x;
   PairScan scan{reinterpret_cast<uint2*>(smem)};  // [kPlanWarps]
@@ -182,17 +224,16 @@ __global__ void __launch_bounds__(kPlanThreads) kvq_release_kernel(const __grid_
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
   const int bs = 1 << bs_log2;
 
-  int count = *p.count;
-  if (count < 0 || count > p.capacity) {
-    if (rank == 0 && tid == 0) set_error(p.err, ERR_RANGE);
-    count = min(max(count, 0), p.capacity);
-  }
+  const int given = *p.count, count = min(max(given, 0), p.capacity);
   uint2 carry = make_uint2(0, 0);
+  int a_next = tid < S ? p.old_lens[tid] : 0, b_next = tid < S ? p.new_lens[tid] : 0;
   for (int base = 0; base < S; base += kPlanThreads) {
-    const int s = base + tid;
+    const int s = base + tid, a = a_next, b = b_next;
+    const bool more = s + kPlanThreads < S;  // (loaded while this turn's sums are made)
+    a_next = more ? p.old_lens[s + kPlanThreads] : 0;
+    b_next = more ? p.new_lens[s + kPlanThreads] : 0;
     int64_t from = 0, to = 0;
     if (s < S) {
-      const int a = p.old_lens[s], b = p.new_lens[s];
       to = ((int64_t)max(a, 0) + bs - 1) >> bs_log2;
       from = max(((int64_t)max(b, 0) + bs - 1) >> bs_log2, (int64_t)p.shared);
       if (a < 0 || b < 0 || to > p.max_blocks) {
@@ -216,41 +257,69 @@ __global__ void __launch_bounds__(kPlanThreads) kvq_release_kernel(const __grid_
   const uint32_t per = (total + ranks - 1) / ranks;
   const uint32_t e0 = static_cast<uint32_t>(min((uint64_t)rank * per, (uint64_t)total));
   const uint32_t e1 = static_cast<uint32_t>(min((uint64_t)e0 + per, (uint64_t)total));
-  auto entry = [&](uint32_t e) {
-    const int s = last_at_most(gone, S, e);
-    const int id = p.table[(int64_t)s * p.max_blocks + first[s] + (e - gone[s])];
-    return id >= 0 && (int64_t)id < p.num_blocks ? id : -1;
+  int ids[R];
+  auto entries = [&](uint32_t e) {  // R neighbours: one search, their loads side by side
+    int q = e < e1 ? last_at_most(gone, S, e) : 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i, ++e) {
+      ids[i] = -1;
+      if (e >= e1) continue;
+      if (q + 1 < S && gone[q + 1] <= e) q = last_at_most(gone, S, e);
+      ids[i] = p.table[(int64_t)q * p.max_blocks + first[q] + (e - gone[q])];
+    }
+    uint32_t n = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (!(ids[i] >= 0 && (int64_t)ids[i] < p.num_blocks)) ids[i] = -1;
+      n += ids[i] >= 0;
+    }
+    return n;
   };
+  const uint32_t round = kPlanThreads * R;
   uint32_t mine = 0;
   if (ranks > 1) {
-    for (uint32_t e = e0 + tid; e < e1; e += kPlanThreads) mine += entry(e) >= 0;
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    if ((tid & 31) == 0 && mine > 0) atomicAdd(here, mine);
+    for (uint32_t base = e0; base < e1; base += round) mine += entries(base + tid * R);
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
+    if ((tid & 31) == 0 && sum > 0) atomicAdd(here, sum);
     cluster.sync();  // (and every CTA has read the count)
   }
   uint32_t at = 0;
   for (int q = 0; q < rank; ++q) at += *cluster.map_shared_rank(here, q);
-  for (uint32_t base = e0; base < e1; base += kPlanThreads) {
-    const uint32_t e = base + tid;
-    const int id = e < e1 ? entry(e) : -1;
-    if (e < e1 && id < 0) set_error(p.err, ERR_RANGE);
+  for (uint32_t base = e0; base < e1; base += round) {
+    // (a single round's entries are the ones just counted)
+    if (ranks == 1 || e1 - e0 > round) mine = entries(base + tid * R);
+    uint32_t e = base + tid * R;
     uint2 all;
-    const uint32_t k = at + scan.before(make_uint2(id >= 0, 0), &all).x;
-    if (id >= 0) {
-      if ((int64_t)count + k < p.capacity) p.free_list[count + k] = id;
-      else set_error(p.err, ERR_RANGE);
+    uint32_t k = at + scan.before(make_uint2(mine, 0), &all).x;
+#pragma unroll
+    for (int i = 0; i < R; ++i, ++e) {
+      if (ids[i] >= 0) {
+        if ((int64_t)count + k < p.capacity) p.free_list[count + k] = ids[i];
+        else set_error(p.err, ERR_RANGE);
+        ++k;
+      } else if (e < e1) {
+        set_error(p.err, ERR_RANGE);
+      }
     }
     at += all.x;
   }
   // the last CTA has counted them all
-  if (rank == ranks - 1 && tid == 0)
+  if (rank == ranks - 1 && tid == 0) {
+    if (given != count) set_error(p.err, ERR_RANGE);
     *p.count_out = static_cast<int>(min((int64_t)count + at, (int64_t)p.capacity));
+  }
   if (ranks > 1) cluster.sync();  // no CTA leaves while its count may be read
 }
 
-template <class Args>
-cudaError_t launch_plan(void (*kernel)(const Args, int), const Args& a, int bs, int ctas, size_t smem,
-                        cudaStream_t st) {
+template <auto Kernel, class Args>
+cudaError_t launch_plan(const Args& a, int ctas, size_t smem, cudaStream_t st) {
+  static PerContext<char> done;
+  char v = 0;
+  const cudaError_t e = done.get(&v, [](char*) {
+    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    return e != cudaSuccess ? e : cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kPlanThreads);
@@ -263,24 +332,24 @@ cudaError_t launch_plan(void (*kernel)(const Args, int), const Args& a, int bs, 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int log2 = 0;
-  while ((1 << log2) < bs) ++log2;
-  return phase_mark(st, cudaLaunchKernelEx(&cfg, kernel, a, log2));
+  while ((1 << log2) < a.bs) ++log2;
+  return phase_mark(st, cudaLaunchKernelEx(&cfg, Kernel, a, log2));
 }
 
 }  // namespace
 
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
   const size_t smem = (2 * kPlanWarps + 3 * (size_t)a.S + 2) * 4;
-  const cudaError_t e = allow_big_smem<kvq_extend_kernel>();
-  if (e != cudaSuccess) return e;
-  return launch_plan(kvq_extend_kernel, a, a.bs, a.max_tokens > 2048 ? 8 : 1, smem, st);
+  ExtendArgs b = a;
+  b.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
+  if (a.max_tokens <= kPlanAlone) return launch_plan<kvq_extend_kernel<1>>(b, 1, smem, st);
+  return launch_plan<kvq_extend_kernel<kPlanRows>>(b, kPlanCluster, smem, st);
 }
 
 cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t st) {
   const size_t smem = (2 * kPlanWarps + 1 + 2 * (size_t)a.S) * 4;
-  const cudaError_t e = allow_big_smem<kvq_release_kernel>();
-  if (e != cudaSuccess) return e;
-  return launch_plan(kvq_release_kernel, a, a.bs, (int64_t)a.S * a.max_blocks > 16384 ? 8 : 1, smem, st);
+  if ((int64_t)a.S * a.max_blocks <= kPlanAloneEntries) return launch_plan<kvq_release_kernel>(a, 1, smem, st);
+  return launch_plan<kvq_release_kernel>(a, kPlanCluster, smem, st);
 }
 
 }  // namespace kvq

@@ -248,6 +248,7 @@ struct ExtendArgs {
   int* err;
   int64_t num_blocks;
   int S, max_blocks, capacity, max_tokens, bs;
+  bool wide;  // slots and positions lie at 16-byte boundaries (set by the launcher)
 };
 cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st);
 struct ReleaseArgs {
