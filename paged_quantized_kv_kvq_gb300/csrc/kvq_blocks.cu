@@ -31,8 +31,9 @@ namespace {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
 // CTAs of a cluster (of 8 instead: 32768 rows of 512 sequences 8.1 us where 16 take 6.0, 16384
-// freed entries 7.1 and 5.1; small calls alike).
-constexpr int kPlanCluster = 16;
+// freed entries 7.1 and 5.1; small calls alike).  A partition of a GPU whose processing
+// clusters have fewer SMs cannot place 16: it gets the 8 that every one places.
+constexpr int kPlanCluster = 16, kPlanClusterSmall = 8;
 // Rows and table entries up to which one CTA does it alone, without the cluster's barriers.
 // Rows, alone and as a cluster: 64 3.0 and 4.1 us, 512 3.2 and 3.7, 1024 4.4 and 4.4, 2048
 // 5.6 and 4.4.  Entries (the host does not know how many go; a tenth): 2048 3.2 and 5.0,
@@ -312,25 +313,35 @@ __global__ void __launch_bounds__(kPlanThreads) kvq_release_kernel(const __grid_
 }
 
 template <auto Kernel, class Args>
-cudaError_t launch_plan(const Args& a, int ctas, size_t smem, cudaStream_t st) {
-  static PerContext<char> done;
-  char v = 0;
-  const cudaError_t e = done.get(&v, [](char*) {
-    const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-    return e != cudaSuccess ? e : cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  });
-  if (e != cudaSuccess) return e;
+cudaError_t launch_plan(const Args& a, bool alone, size_t smem, cudaStream_t st) {
+  static PerContext<int> most;  // CTAs of a cluster that this context's device places
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(kPlanThreads);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  auto ctas_of = [&](int n) { cfg.gridDim = dim3(attr[0].val.clusterDim.x = static_cast<unsigned>(n)); };
+  int ctas = 0;
+  const cudaError_t e = most.get(&ctas, [&](int* n) {
+    const size_t big = cfg.dynamicSmemBytes = 227 * 1024;
+    cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(big));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    int fit = 0;
+    ctas_of(kPlanCluster);
+    if (cudaOccupancyMaxActiveClusters(&fit, Kernel, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      fit = 0;
+    }
+    *n = fit > 0 ? kPlanCluster : kPlanClusterSmall;
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
+  ctas_of(alone ? 1 : ctas);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
   int log2 = 0;
   while ((1 << log2) < a.bs) ++log2;
   return phase_mark(st, cudaLaunchKernelEx(&cfg, Kernel, a, log2));
@@ -342,14 +353,13 @@ cudaError_t launch_extend(const ExtendArgs& a, cudaStream_t st) {
   const size_t smem = (2 * kPlanWarps + 3 * (size_t)a.S + 2) * 4;
   ExtendArgs b = a;
   b.wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.positions)) & 15) == 0;
-  if (a.max_tokens <= kPlanAlone) return launch_plan<kvq_extend_kernel<1>>(b, 1, smem, st);
-  return launch_plan<kvq_extend_kernel<kPlanRows>>(b, kPlanCluster, smem, st);
+  if (a.max_tokens <= kPlanAlone) return launch_plan<kvq_extend_kernel<1>>(b, true, smem, st);
+  return launch_plan<kvq_extend_kernel<kPlanRows>>(b, false, smem, st);
 }
 
 cudaError_t launch_release(const ReleaseArgs& a, cudaStream_t st) {
   const size_t smem = (2 * kPlanWarps + 1 + 2 * (size_t)a.S) * 4;
-  if ((int64_t)a.S * a.max_blocks <= kPlanAloneEntries) return launch_plan<kvq_release_kernel>(a, 1, smem, st);
-  return launch_plan<kvq_release_kernel>(a, kPlanCluster, smem, st);
+  return launch_plan<kvq_release_kernel>(a, (int64_t)a.S * a.max_blocks <= kPlanAloneEntries, smem, st);
 }
 
 }  // namespace kvq
