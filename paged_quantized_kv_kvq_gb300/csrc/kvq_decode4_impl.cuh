@@ -20,7 +20,7 @@
 //    (p - fp16(p)) where the others carry the high parts, so that one product does what
 //    two did.
 // The range of a warp and the partials are as in the general kernel with
-// steps in the place of pages; kvq_join_kernel joins them.
+// steps in the place of pages; kvq_merge_kernel joins them.
 #pragma once
 #include "kvq_decode_impl.cuh"
 
@@ -542,7 +542,7 @@ cudaError_t run_decode4(const DecodeLaunch& l) {
   dc.attrs = da;
   dc.numAttrs = 1;
   const cudaError_t f = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode4_kernel<D, DUP, DIFF>, l.p));
-  return f != cudaSuccess ? f : run_join<D, DIFF>(l);
+  return f != cudaSuccess ? f : run_merge<D, DIFF>(l);
 }
 
 template <bool DIFF>

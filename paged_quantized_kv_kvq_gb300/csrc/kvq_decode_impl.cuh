@@ -1335,86 +1335,33 @@ __device__ __forceinline__ void merge_pieces(const DecodeParams& p, int wf, int 
 // started before the unit, slot 0 otherwise).  Launched as a programmatic
 // dependent of the decode kernel: griddepcontrol.wait returns once the decode
 // grid has completed and its writes are visible.  CH: pieces loaded together
-// (one round trip), 8 or 16 as the plan chooses.
-template <int D, int CH>
-__global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const DecodeParams p) {
-  // A kernel launched after this one as a programmatic dependent (the next
-  // decode-step append) may launch now; it waits for this grid's completion
-  // before touching anything.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float kNegInf = __int_as_float(0xff800000u);
-  constexpr int NW = kMergeThreads / 32;
-  constexpr int NE = D / 32;   // output elements per lane
-  const int lane = threadIdx.x & 31;
-  const int U = p.pool.Hkv * p.n_ht;
-  const int* PS = p.ps;
-  const int Ttot = __ldcg(PS + p.S);
-  const int nwarps = p.grid * kDecodeWarps;
-  const int ppw = p.ppw_fixed > 0 ? p.ppw_fixed : (Ttot + nwarps - 1) / nwarps;
-  if (ppw <= 0) return;
-  // one task per (unit, Q-head row of its tile) that a Q head fills: rows
-  // 0 .. min(8, G) - 1 of each tile (fewer in a ragged last tile); one warp
-  // per task
-  const int rpu = min(kPartRows, p.G);
-  const int64_t ntasks = (int64_t)p.S * U * rpu;
-  for (int64_t task = (int64_t)blockIdx.x * NW + (threadIdx.x >> 5); task < ntasks;
-       task += (int64_t)gridDim.x * NW) {
-    const int64_t u = task / rpu;
-    const int rr = (int)(task % rpu);
-    const int s = (int)(u / U), lu = (int)(u % U);
-    const int ht = lu % p.n_ht;
-    if (rr >= min(8, p.G - 8 * ht)) continue;
-    const int ps0 = __ldcg(PS + s), ps1 = __ldcg(PS + s + 1);
-    const int Ps = (ps1 - ps0) / U;
-    if (Ps == 0) continue;
-    const int U0 = ps0 + lu * Ps;
-    const int wf = U0 / ppw, wl = (U0 + Ps - 1) / ppw;
-    if (wf == wl) continue;  // written directly by its warp
-    const int n_u = wl - wf + 1;
-    const int h = lu / p.n_ht;
-    const int64_t orow = (int64_t)s * p.Hq + h * p.G + 8 * ht + rr;
-    float M = kNegInf, Lsum = 0.f, acc[NE];
-#pragma unroll
-    for (int i = 0; i < NE; ++i) acc[i] = 0.f;
-    if (p.pre != nullptr) {  // cascade: the prefix partial is one more piece
-      const float* pr = p.pre + orow * (D + 2);
-      M = pr[0];
-      Lsum = pr[1];
-#pragma unroll
-      for (int i = 0; i < NE; ++i) acc[i] = pr[2 + lane + 32 * i];
-    }
-    merge_pieces<D, CH>(p, wf, n_u, U0, ppw, rr, lane, M, Lsum, acc);
-    if (p.lse != nullptr && lane == 0) p.lse[orow] = row_lse(M, Lsum);
-    float* dst = p.out + (int64_t)s * p.out_stride + (int64_t)(h * p.G + 8 * ht + rr) * D;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) dst[lane + 32 * i] = Lsum > 0.f ? acc[i] / Lsum : 0.f;
-  }
-}
-
-// The merge of differential attention, and of pools of 4-bit floats: a warp takes a row,
-// or both rows of a differential head, whose normed difference it writes.  A merge is a
-// chain of round trips behind the last warp of the decode, so all that only takes
-// the lengths is done while the decode still runs: every CTA makes the prefix over the
-// sequences itself (up to kJoinSeqs; more are read from the workspace) and looks its first
-// unit up before griddepcontrol.wait; behind it one round trip brings the partials.
-constexpr int kJoinSeqs = 2048;
+// (one round trip), 8 or 16 as the plan chooses.  A warp takes a row, or both rows of a
+// differential head, whose normed difference it writes.
+//
+// A merge is a chain of round trips behind the last warp of the decode, so all that only
+// takes the lengths is done while the decode still runs (they may be read early: the
+// decode does it, too): every CTA makes the prefix over the sequences itself (up to
+// kMergeSeqs; of more it is read from the workspace) and looks its first unit up before
+// griddepcontrol.wait; behind it one round trip brings the partials.  With the prefix read
+// from the workspace after the wait a decode step of 32 layers, 64 x 2048, INT8, took
+// 1.819 ms, so 1.756; the call alone 60.5 and 58.0 us.
+constexpr int kMergeSeqs = 2048;
 
 template <int D, int CH, bool DIFF>
-__global__ void __launch_bounds__(kMergeThreads) kvq_join_kernel(const __grid_constant__ DecodeParams p) {
+__global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const __grid_constant__ DecodeParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int NW = kMergeThreads / 32;
   constexpr int NE = D / 32;  // output elements per lane
   constexpr int RPT = DIFF ? 2 : 1;
   const float kNegInf = __int_as_float(0xff800000u);
-  extern __shared__ int join_smem[];
+  extern __shared__ int merge_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int U = p.pool.Hkv * p.n_ht;
-  const bool own = p.S <= kJoinSeqs;
-  const int* PS = p.ps;
+  const bool own = p.S <= kMergeSeqs;
+  const int* mine = merge_smem + NW;
   if (own) {  // pages (steps) before each sequence, as the decode counts them
-    int* wtot = join_smem;  // [NW]
-    int* mine = join_smem + NW;
+    int* wtot = merge_smem;  // [NW]
+    int* first = merge_smem + NW;
     int carry = 0;
     for (int base = 0; base < p.S; base += kMergeThreads) {
       const int s = base + threadIdx.x;
@@ -1437,17 +1384,17 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_join_kernel(const __grid_co
         before += w < warp ? wtot[w] : 0;
         all += wtot[w];
       }
-      if (s < p.S) mine[s + 1] = carry + before + x;
+      if (s < p.S) first[s + 1] = carry + before + x;
       carry += all;
       __syncthreads();
     }
-    if (threadIdx.x == 0) mine[0] = 0;
+    if (threadIdx.x == 0) first[0] = 0;
     __syncthreads();
-    PS = mine;
   } else {
     asm volatile("griddepcontrol.wait;" ::: "memory");
   }
-  const int Ttot = PS[p.S];
+  auto pages_before = [&](int s) { return own ? mine[s] : __ldcg(p.ps + s); };
+  const int Ttot = pages_before(p.S);
   const int nwarps = p.grid * kDecodeWarps;
   const int ppw = p.ppw_fixed > 0 ? p.ppw_fixed : (Ttot + nwarps - 1) / nwarps;
   const int tpu = min(kPartRows, p.G) / RPT;  // tasks of a head tile
@@ -1461,7 +1408,7 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_join_kernel(const __grid_co
     t.i = static_cast<int>(task - u * tpu);
     t.s = static_cast<int>(u / U);
     t.lu = static_cast<int>(u - (int64_t)t.s * U);
-    const int ps0 = PS[t.s], Ps = (PS[t.s + 1] - ps0) / U;
+    const int ps0 = pages_before(t.s), Ps = (pages_before(t.s + 1) - ps0) / U;
     t.U0 = ps0 + t.lu * Ps;
     t.wf = t.U0 / ppw;
     t.n_u = (t.U0 + Ps - 1) / ppw - t.wf + 1;
@@ -1551,12 +1498,12 @@ cudaError_t launch_merge(const DecodeLaunch& l, Kernel kernel, unsigned grid, in
 }
 
 template <int D, bool DIFF>
-cudaError_t run_join(const DecodeLaunch& l) {
-  const int smem = l.p.S <= kJoinSeqs ? (kMergeThreads / 32 + l.p.S + 1) * 4 : 0;
+cudaError_t run_merge(const DecodeLaunch& l) {
+  const int smem = l.p.S <= kMergeSeqs ? (kMergeThreads / 32 + l.p.S + 1) * 4 : 0;
   // (a differential head is one task for two rows)
   const unsigned grid = DIFF ? (l.merge_grid + 1) / 2 : l.merge_grid;
-  return l.merge_chunk == 16 ? launch_merge(l, kvq_join_kernel<D, 16, DIFF>, grid, smem)
-                             : launch_merge(l, kvq_join_kernel<D, 8, DIFF>, grid, smem);
+  return l.merge_chunk == 16 ? launch_merge(l, kvq_merge_kernel<D, 16, DIFF>, grid, smem)
+                             : launch_merge(l, kvq_merge_kernel<D, 8, DIFF>, grid, smem);
 }
 
 // CTAS: resident CTAs per SM the kernel is compiled for.
@@ -1578,9 +1525,7 @@ cudaError_t run_decode(const DecodeLaunch& l) {
     e = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode_kernel<FMT, D, NG, BS8, CTAS, DIFF>, l.p));
     if (e != cudaSuccess) return e;
   }
-  if constexpr (DIFF) return run_join<D, true>(l);
-  return l.merge_chunk == 16 ? launch_merge(l, kvq_merge_kernel<D, 16>, l.merge_grid, 0)
-                             : launch_merge(l, kvq_merge_kernel<D, 8>, l.merge_grid, 0);
+  return run_merge<D, DIFF>(l);
 }
 
 template <int FMT, bool BS8 = false, bool DIFF = false>

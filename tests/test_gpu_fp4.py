@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_quantized_kv_kvq_gb300 as kvq
-from cache_ops_ref import frequencies, rope, tokens
+from cache_ops_ref import attention, frequencies, rope, tokens
 from fp4_ref import SCALES, Fp4Cache, quantize, values
 from kvq_testutil import TOL
 
@@ -516,4 +516,35 @@ def test_a_wait_that_runs_out():
     kvq.kvq_paged_decode(pool.handle, _t(q), _t(table), _t(lens), 300, 128 ** -0.5, out, ws)
     assert pool.error() == kvq.KVQ_OK
     _near(out.cpu().numpy(), ref.decode(q, table, lens))
+    pool.close()
+
+
+@pytest.mark.parametrize("fmt", [FMT, kvq.KVQ_INT8_PER_BLOCK])
+@pytest.mark.parametrize("S", [2048, 2049])
+def test_many_sequences(fmt, S):
+    """As many sequences as the merge counts itself, and one more; a few long ones that are cut,
+    so that every piece is joined.  Rows drawn from all over against float64."""
+    rng = np.random.default_rng(S)
+    bs, hkv, d, hq = 16, 1, 64, 4
+    lens = rng.integers(0, 12, S).astype(np.int32)
+    lens[[0, 700, S - 1]] = 3000, 1777, 2500
+    per = -(-lens // bs)
+    table = np.zeros((S, int(per.max())), np.int32)
+    at = np.concatenate([[0], np.cumsum(per)])
+    for s in range(S):
+        table[s, :per[s]] = np.arange(at[s], at[s + 1])
+    slots = np.concatenate([tokens(table, lens, s, bs) for s in range(S)])
+    pool = kvq.KVPool(int(at[-1]), bs, hkv, d, fmt, device=DEV)
+    pool.append(_t(_rows(rng, len(slots), hkv, d)), _t(_rows(rng, len(slots), hkv, d)), _t(slots))
+    q = rng.standard_normal((S, hq, d)).astype(np.float16)
+    out = pool.decode(_t(q), _t(table), _t(lens), 3000).cpu().numpy()
+    pick = np.unique(np.concatenate([[0, 1, 699, 700, 701, S - 2, S - 1], rng.integers(0, S, 30)]))
+    codes, scales = (x.double().cpu().numpy() for x in pool.read_slots(_t(slots)))
+    held = np.zeros((int(at[-1]) * bs, 2, hkv, d))
+    if fmt == FMT:
+        held[slots] = values(codes.astype(np.uint8), nearest_bytes(scales))
+    else:
+        held[slots] = codes * scales[..., None]
+    want = attention(lambda i: held[tokens(table, lens, pick[i], bs)], q[pick], lens[pick])[0]
+    _near(out[pick], want)
     pool.close()
