@@ -137,7 +137,6 @@ cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStrea
   l.merge_chunk = plan.merge_chunk;
   l.smem = plan.smem_bytes;
   l.st = st;
-  l.dependent = dependent;
   l.two_ctas = plan.two_ctas;
   if (a.diff.lambda != nullptr) return launch_decode_diff(l);
   if (fmt_block(a.pool.fmt)) return launch_decode_block(l);

@@ -708,7 +708,10 @@ __global__ void __launch_bounds__(kDecodeThreads, CTAS)
 
   // The merge grid may launch now: every CTA of this (persistent) grid is
   // resident once all have passed this point, and the merge reads nothing of
-  // ours before its griddepcontrol.wait returns on this grid's completion.
+  // ours before its griddepcontrol.wait returns on this grid's completion.  It reads the
+  // lengths before that, so where nothing vouches for them (this grid, too, is launched
+  // while the kernel before it ends) it comes after that kernel.
+  if (!p.inputs_early) asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   char* stages = smem + warp * nstage * p.stage_bytes;
@@ -1477,7 +1480,6 @@ struct DecodeLaunch {
   int merge_chunk;  // kvq_merge_kernel's CH
   int smem;
   cudaStream_t st;
-  bool dependent;  // launch as a programmatic dependent of the previous kernel
   bool two_ctas = false;  // planned for two CTAs per SM (per-block formats)
 };
 
@@ -1521,7 +1523,7 @@ cudaError_t run_decode(const DecodeLaunch& l) {
     da[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     da[0].val.programmaticStreamSerializationAllowed = 1;
     dc.attrs = da;
-    dc.numAttrs = l.dependent ? 1 : 0;
+    dc.numAttrs = 1;
     e = phase_mark(l.st, cudaLaunchKernelEx(&dc, kvq_decode_kernel<FMT, D, NG, BS8, CTAS, DIFF>, l.p));
     if (e != cudaSuccess) return e;
   }
