@@ -240,3 +240,98 @@ def test_other_streams_and_devices():
     with pytest.raises(ValueError, match="must be torch.int32"):
         pool.release_blocks(table, lens.long(), _t([0, 3]), free, count)
     pool.close()
+
+
+@pytest.mark.parametrize("S,new,offset", [(3, 20, 1), (40, 100, 0), (40, 100, 1), (40, 101, 2), (600, 9, 3)])
+def test_rows_at_any_address(S, new, offset):
+    """Slots and positions that begin inside a larger tensor, 8 bytes off a 16-byte boundary or
+    on one, calls by one CTA and by a cluster; what lies around them stays."""
+    rng = np.random.default_rng(S + offset)
+    lens, n, table, free, count, total = _case(rng, S, 16, 200, new, 3)
+    rows = int(n.sum()) + 5
+    want, err = blocks_ref.extend(n, table, lens, free, count, 16, total, rows)
+    assert not err
+    pool = _pool(total, 16)
+    s, p = (torch.full((rows + offset + 1,), 77, dtype=I64, device=DEV) for _ in range(2))
+    t, L, c, q = _t(table), _t(lens), _t([count]), torch.empty(S + 1, dtype=I32, device=DEV)
+    kvq.kvq_extend_tables(pool.handle, _t(n), t, L, _t(free), c, L, c, q, s[offset:-1], p[offset:-1])
+    _same({"table": t, "lens": L, "count": c, "q_start": q, "slots": s[offset:-1], "positions": p[offset:-1]}, want)
+    for x in (s, p):
+        assert (x[:offset] == 77).all() and x[-1] == 77
+    assert pool.error() == kvq.KVQ_OK
+    pool.close()
+
+
+def test_sequences_without_tokens_between_distant_ones():
+    """Thousands of sequences that get nothing between the few that do, and that gave nothing back."""
+    S, bs = 16384, 16
+    n, lens = np.zeros(S, np.int32), np.full(S, 16, np.int32)
+    n[[0, 8000, S - 1]] = 1500, 40, 1500
+    total = S + 200
+    table = np.full((S, 100), -1, np.int32)
+    table[:, 0] = np.arange(S)
+    free = np.arange(S, total).astype(np.int32)
+    pool = _pool(total, bs)
+    want, err = blocks_ref.extend(n, table, lens, free, 200, bs, total, 3050)
+    assert not err
+    got = _extend(pool, n, table, lens, free, 200, 3050)
+    _same(got, want)
+    kept = want["lens"].copy()
+    kept[[0, S - 1]] = 0
+    back, count, err = blocks_ref.release(want["table"], want["lens"], kept, np.full(total, -1, np.int32), 0, bs, total)
+    f, c = _t(np.full(total, -1)), _t([0])
+    kvq.kvq_release_blocks(pool.handle, got["table"], got["lens"], _t(kept), f, c, c)
+    np.testing.assert_array_equal(f.cpu().numpy(), back)
+    assert c.item() == count and not err and pool.error() == kvq.KVQ_OK
+    pool.close()
+
+
+def test_many_bad_rows_in_a_cluster():
+    """Ids outside the pool all over a table that a cluster frees, more of them than a turn of its
+    threads: none given back, the others in order; and a list that is too short."""
+    rng = np.random.default_rng(8)
+    S, bs, width = 40, 16, 700
+    old = rng.integers(0, width * bs + 1, S)
+    old[7] = width * bs + 9  # beyond the row
+    table = rng.integers(-3, 20000, (S, width)).astype(np.int32)
+    total = 18000
+    for capacity in (40000, 9000):
+        free = np.full(capacity, -1, np.int32)
+        want, count, err = blocks_ref.release(table, old, np.zeros(S, int), free, 4, bs, total)
+        assert err
+        pool = _pool(total, bs)
+        f, c = _t(free), _t([4])
+        kvq.kvq_release_blocks(pool.handle, _t(table), _t(old), _t(np.zeros(S)), f, c, c)
+        np.testing.assert_array_equal(f.cpu().numpy(), want)
+        assert c.item() == count and pool.error() == kvq.KVQ_ERR_OUT_OF_RANGE
+        pool.close()
+
+
+def test_evicted_blocks_come_back():
+    """An eviction's tables and lengths are what a release takes: the evicted blocks come back, the
+    kept ones stay, and every block is somewhere once."""
+    rng = np.random.default_rng(5)
+    S, bs, nb, budget = 4, 16, 64, 5
+    lens = np.array([200, 33, 0, 81], np.int32)
+    per = -(-lens // bs)
+    ids = rng.permutation(nb).astype(np.int32)
+    table = np.full((S, 14), -1, np.int32)
+    at = np.concatenate([[0], np.cumsum(per)])
+    for s in range(S):
+        table[s, :per[s]] = ids[at[s]:at[s + 1]]
+    free = np.full(nb, -1, np.int32)
+    free[:nb - at[-1]] = ids[at[-1]:]
+    pool = _pool(nb, bs)
+    scores = torch.rand((S, 1, 14 * bs), device=DEV)
+    t2, l2, kept, _ = pool.evict_blocks(scores, _t(table), _t(lens), 200, budget, sink_blocks=1)
+    f, c = _t(free), _t([nb - at[-1]])
+    pool.release_blocks(t2, _t(lens), l2, f, c)
+    new, t2 = l2.cpu().numpy(), t2.cpu().numpy()
+    held = -(-new // bs)
+    assert (held == np.minimum(per, budget)).all() and c.item() == nb - held.sum()
+    here = np.concatenate([t2[s, :held[s]] for s in range(S)] + [f.cpu().numpy()[:c.item()]])
+    assert sorted(here) == list(range(nb))
+    for s in range(S):
+        assert set(t2[s, :held[s]]) <= set(table[s, :per[s]])
+    assert pool.error() == kvq.KVQ_OK
+    pool.close()
