@@ -90,7 +90,7 @@ typedef struct kvq_pool kvq_pool; /* opaque; one per layer */
 typedef struct {
     size_t total_bytes;  /* everything kvq_alloc_pool needs (header + regions)  */
     size_t code_bytes;   /* 2 * num_blocks * block_size * kv_heads * head_dim * elem */
-    size_t scale_bytes;  /* fp32 scales of every format that has them (per-block
+    size_t scale_bytes;  /* scales of every format that has them, fp32 (8-bit: KVQ_FP4_E2M1; per-block
                             formats: 16 per page, two scales and padding)       */
     size_t header_bytes; /* device error word and padding                       */
     size_t page_bytes;   /* bytes of one (block, kv head) page: K+V codes (+ group or block scales,

@@ -26,8 +26,8 @@ namespace kvq {
 constexpr int kAppendThreads = 128;
 // Tokens from which on 4-bit floats take kvq_fp4_rows.cu.  (8 heads of 128, this kernel and
 // that one: 256 tokens of whole blocks 3.8 and 3.1 us, single tokens 3.6 and 4.6; 512 tokens
-// 5.3 and 3.1, 4.3 and 4.9; 2048 tokens 12.9 and 4.6, 10.3 and 8.6; 16384 tokens 74 and 18,
-// 92 and 78.  2 heads of 64: 512 tokens 3.3 and 2.9, 3.1 and 3.8.)
+// 5.3 and 3.0, 4.3 and 5.1; 2048 tokens 12.9 and 3.9, 10.3 and 9.0; 16384 tokens 74 and 17,
+// 92 and 76.  2 heads of 64: 512 tokens 3.3 and 2.9, 3.1 and 3.8.)
 constexpr int kAppend4Tokens = 512;
 
 struct AppendParams {

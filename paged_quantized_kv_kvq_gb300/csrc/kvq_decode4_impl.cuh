@@ -21,6 +21,11 @@
 //    two did.
 // The range of a warp and the partials are as in the general kernel with
 // steps in the place of pages; kvq_merge_kernel joins them.
+// Measured, calls replayed back to back: 64 x 2048 37.7 us (151 MB, 4.0 TB/s, 0.59 of the copy
+// rate), 64 x 512 16.4, 64 x 8192 116.9: some 26 us for 2048 more tokens (0.84 of the copy
+// rate) and 11 us of start, merge and uneven ends; 8 x 16384..32768 in blocks of 32: 47.0.
+// (One stage of 16 warps a CTA instead of two stages for each of 4: more instructions,
+// slower at every length.)
 #pragma once
 #include "kvq_decode_impl.cuh"
 

@@ -78,9 +78,11 @@ def diff_ref(values, q, lens, lam, weight, eps, out_scale, sm_scale=None):
 
 SUMS = 1e-5        # fp32 sums of a map, of its root mean square
 LONG = 3e-4        # where the tensor core's accumulator sums long ranges (formats with scales per token or group)
-# prompts: each weight is an fp16 number, within 2^-12 of itself (uniform: 2^-12 / sqrt(3) on average), and a value is a
-# sum of such independent errors: of the map's root mean square that much on average, eight times that at most
-WEIGHTS = 0.8 * 2.0 ** -12 / 3 ** 0.5
+# prompts: each weight is an fp16 number, within 2^-11 / x of itself, x in [1, 2) its mantissa.  Over mantissas spread
+# as logarithms the mean of 1 / x^2 is (1 - 1/4) / (2 ln 2) = 0.54, so the error is 0.73 2^-11 / sqrt(3) in root mean square,
+# and a value is a sum of such independent errors: of the map's root mean square that much.  (_near allows ten times it;
+# half of it is taken, which holds five of them.)
+WEIGHTS = 0.5 * 0.73 * 2.0 ** -11 / 3 ** 0.5
 
 
 def _near(got, want, maps, lam, weight, out_scale, rel):
