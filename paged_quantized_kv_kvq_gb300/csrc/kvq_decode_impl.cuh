@@ -1473,6 +1473,70 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const __grid_c
   }
 }
 
+// The same with nothing looked up ahead, in fewer registers (80 and 126 a thread against 91 and
+// 147), so that more of it is resident: for merges of more CTAs than two an SM.  Decode steps of
+// 32 layers with that kernel and this one: 64 x 2048, 256 CTAs, 1.756 and 1.819 ms; 100
+// sequences with 32 heads, 400 CTAs, INT8 groups of 64 6.198 and 6.112, e4m3 5.586 and 5.518; 256
+// sequences of 8 kv heads and groups of 4, 1024 CTAs, 7.10 and 6.88.  (That kernel held to 80
+// and 128 registers: 1.789, 6.147 and 6.96 ms.)
+constexpr unsigned kMergeAhead = 304;
+
+template <int D, int CH>
+__global__ void __launch_bounds__(kMergeThreads) kvq_merge_many_kernel(const DecodeParams p) {
+  // A kernel launched after this one as a programmatic dependent (the next
+  // decode-step append) may launch now; it waits for this grid's completion
+  // before touching anything.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float kNegInf = __int_as_float(0xff800000u);
+  constexpr int NW = kMergeThreads / 32;
+  constexpr int NE = D / 32;   // output elements per lane
+  const int lane = threadIdx.x & 31;
+  const int U = p.pool.Hkv * p.n_ht;
+  const int* PS = p.ps;
+  const int Ttot = __ldcg(PS + p.S);
+  const int nwarps = p.grid * kDecodeWarps;
+  const int ppw = p.ppw_fixed > 0 ? p.ppw_fixed : (Ttot + nwarps - 1) / nwarps;
+  if (ppw <= 0) return;
+  // one task per (unit, Q-head row of its tile) that a Q head fills: rows
+  // 0 .. min(8, G) - 1 of each tile (fewer in a ragged last tile); one warp
+  // per task
+  const int rpu = min(kPartRows, p.G);
+  const int64_t ntasks = (int64_t)p.S * U * rpu;
+  for (int64_t task = (int64_t)blockIdx.x * NW + (threadIdx.x >> 5); task < ntasks;
+       task += (int64_t)gridDim.x * NW) {
+    const int64_t u = task / rpu;
+    const int rr = (int)(task % rpu);
+    const int s = (int)(u / U), lu = (int)(u % U);
+    const int ht = lu % p.n_ht;
+    if (rr >= min(8, p.G - 8 * ht)) continue;
+    const int ps0 = __ldcg(PS + s), ps1 = __ldcg(PS + s + 1);
+    const int Ps = (ps1 - ps0) / U;
+    if (Ps == 0) continue;
+    const int U0 = ps0 + lu * Ps;
+    const int wf = U0 / ppw, wl = (U0 + Ps - 1) / ppw;
+    if (wf == wl) continue;  // written directly by its warp
+    const int n_u = wl - wf + 1;
+    const int h = lu / p.n_ht;
+    const int64_t orow = (int64_t)s * p.Hq + h * p.G + 8 * ht + rr;
+    float M = kNegInf, Lsum = 0.f, acc[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) acc[i] = 0.f;
+    if (p.pre != nullptr) {  // cascade: the prefix partial is one more piece
+      const float* pr = p.pre + orow * (D + 2);
+      M = pr[0];
+      Lsum = pr[1];
+#pragma unroll
+      for (int i = 0; i < NE; ++i) acc[i] = pr[2 + lane + 32 * i];
+    }
+    merge_pieces<D, CH>(p, wf, n_u, U0, ppw, rr, lane, M, Lsum, acc);
+    if (p.lse != nullptr && lane == 0) p.lse[orow] = row_lse(M, Lsum);
+    float* dst = p.out + (int64_t)s * p.out_stride + (int64_t)(h * p.G + 8 * ht + rr) * D;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) dst[lane + 32 * i] = Lsum > 0.f ? acc[i] / Lsum : 0.f;
+  }
+}
+
 struct DecodeLaunch {
   DecodeParams p;
   dim3 grid;
@@ -1501,6 +1565,11 @@ cudaError_t launch_merge(const DecodeLaunch& l, Kernel kernel, unsigned grid, in
 
 template <int D, bool DIFF>
 cudaError_t run_merge(const DecodeLaunch& l) {
+  if constexpr (!DIFF) {
+    if (l.merge_grid > kMergeAhead)
+      return l.merge_chunk == 16 ? launch_merge(l, kvq_merge_many_kernel<D, 16>, l.merge_grid, 0)
+                                 : launch_merge(l, kvq_merge_many_kernel<D, 8>, l.merge_grid, 0);
+  }
   const int smem = l.p.S <= kMergeSeqs ? (kMergeThreads / 32 + l.p.S + 1) * 4 : 0;
   // (a differential head is one task for two rows)
   const unsigned grid = DIFF ? (l.merge_grid + 1) / 2 : l.merge_grid;

@@ -14,9 +14,9 @@
 // decode step's) all at once, a lane then holding four tokens of any slots.  A word that
 // a run does not fill is merged into the page (V nibbles by atomics: other warps may
 // hold its other tokens).
-// Bound: HBM (4 bytes a channel in, 1.125 out, for K and V together) and close behind it
-// the instructions, some 700 for the 64 values of a lane (counted: issue slots 60% busy,
-// DRAM 45%).  Measured, 16384 tokens x 8 heads of 128: whole blocks 16.9 us (86 MB, 0.75 of
+// Bound: HBM (4 bytes a channel in, 1.125 out, for K and V together), the instructions (760 of
+// a warp for its 16 tokens, counted) and the wait for the slots, then the rows: issue slots
+// 46% busy from a cold cache, DRAM 40%.  Measured, 16384 tokens x 8 heads of 128: whole blocks 16.9 us (86 MB, 0.75 of
 // the copy rate), from inside a block 17.1, single tokens 76; read back 17.2, 18.2 and 47.  (Sub-tile by sub-tile of the 16 tokens
 // instead of runs: 16.6 us for whole blocks, but 32 from inside a block and 235 for
 // single tokens.)
