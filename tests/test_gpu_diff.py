@@ -150,6 +150,23 @@ def test_decode_precision(fmt):
     pool.close()
 
 
+@pytest.mark.parametrize("fmt", [kvq.KVQ_FP4_E2M1, kvq.KVQ_INT8_PER_BLOCK])
+@pytest.mark.parametrize("S", [2048, 2049])
+def test_decode_of_many_sequences(fmt, S):
+    """As many sequences as the merge counts itself, and one more, a few of them cut."""
+    lens = np.random.default_rng(S).integers(0, 12, S)
+    lens[[0, 700, S - 1]] = 3000, 1777, 2500
+    pool, vals, table, lens, rng = _filled(fmt, 0, 16, 1, 64, list(lens), seed=1)
+    q = rng.standard_normal((S, 2, 64)).astype(np.float16)
+    lam, w = np.array([0.4, 0.7], np.float32), rng.uniform(0.5, 1.5, 64).astype(np.float32)
+    out = pool.diff_decode(_t(q), _t(table), _t(lens), 3000, _t(lam), _t(w)).cpu().numpy()
+    assert pool.error() == kvq.KVQ_OK
+    pick = np.unique(np.concatenate([[0, 1, 699, 700, 701, S - 2, S - 1], rng.integers(0, S, 30)]))
+    want, maps = diff_ref(lambda i: vals[tokens(table, lens, pick[i], 16)], q[pick], lens[pick], lam.astype(np.float64), w, 1e-5, 1.0)
+    _near(out[pick], want, maps, lam, w, 1.0, SUMS)
+    pool.close()
+
+
 @pytest.mark.parametrize("fmt,group", FORMATS)
 @pytest.mark.parametrize("bs,H,hkv,d,lens,n", [
     (16, 4, 2, 128, [40, 0, 17, 200], [40, 0, 5, 130]), (32, 3, 1, 64, [150, 64, 1], [1, 64, 1]), (64, 16, 2, 128, [70, 300], [9, 1]),

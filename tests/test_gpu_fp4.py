@@ -520,12 +520,13 @@ def test_a_wait_that_runs_out():
 
 
 @pytest.mark.parametrize("fmt", [FMT, kvq.KVQ_INT8_PER_BLOCK])
-@pytest.mark.parametrize("S", [2048, 2049])
-def test_many_sequences(fmt, S):
-    """As many sequences as the merge counts itself, and one more; a few long ones that are cut,
-    so that every piece is joined.  Rows drawn from all over against float64."""
+@pytest.mark.parametrize("S,hq", [(2048, 1), (2049, 1), (2048, 4), (2049, 4)])
+def test_many_sequences(fmt, S, hq):
+    """As many sequences as the merge counts itself, and one more (one head), and so many
+    rows that the merge of many takes them (four heads); a few long ones that are cut, so
+    that pieces are joined.  Rows drawn from all over against float64."""
     rng = np.random.default_rng(S)
-    bs, hkv, d, hq = 16, 1, 64, 4
+    bs, hkv, d = 16, 1, 64
     lens = rng.integers(0, 12, S).astype(np.int32)
     lens[[0, 700, S - 1]] = 3000, 1777, 2500
     per = -(-lens // bs)
