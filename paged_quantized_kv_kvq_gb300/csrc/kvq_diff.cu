@@ -5,10 +5,8 @@
 // (kvq_prefill_ws_impl.cuh).  Formats that it does not take (per-channel scales, several scale
 // groups per head): every head becomes two Q rows, one per map with the other map's
 // channels zero, the prefill kernels attend them, and a last kernel takes the
-// difference of the two results of a head, norms it and rounds it.  (8 x 2048, 16 heads over 4
-// kv heads of 4-bit floats: 510 us so, 298 by the form for two maps, which does half the
-// score products, needs no expanded queries and no fp32 results, and rounds a weight to
-// one fp16 number, within 2^-11 of itself like the fp16 output.)
+// difference of the two results of a head, norms it and rounds it.  (The form for two maps
+// does half the score products and needs no expanded queries and no fp32 results.)
 #include <algorithm>
 
 #include "kvq_decode_impl.cuh"

@@ -291,12 +291,13 @@ __device__ __forceinline__ WsItem ws_item(const PrefillWsParams& p, int i) {
 // done each tile's warps read the same rows of both O -- a warp may read the tensor-memory
 // lanes of its quarter whoever wrote them -- take the difference of their half of the
 // columns, swap the halves' sums of squares and write normed fp16 rows: no expanded Q,
-// no fp32 results in memory.  The results are rounded to fp16, so the weights enter P.V as one
-// fp16 number: each is within 2^-11 of itself, 2^-12.2 in root mean square, and so is a
-// result's sum of many such (independent) errors of the map's own length: as much as
-// the rounding of the result itself adds.  That is half the P.V products.  The tiles meet at three more pairs of mbarriers: O and the
-// row's factor there, sums there, O read (only then may the next item's first P.V, which
-// overwrites it, be asked for).
+// no fp32 results in memory.  The weights keep both fp16 parts, although the results are fp16:
+// the maps are there to cancel and the norm divides by what is left of them, so an error
+// counts against the difference, not against the maps.  (300 equal keys but for one, values
+// around means of 4 to 8, lambda 1: results off by up to 6e-3 with the high parts alone, by
+// 4e-5 with both, beyond half an fp16 step.  8 x 2048, 16 heads over 4 kv heads of 4-bit floats: 299 and 354 us.)
+// The tiles meet at three more pairs of mbarriers: O and the row's factor there, sums there,
+// O read (only then may the next item's first P.V, which overwrites it, be asked for).
 template <int FMT, int D, bool DIFF = false>
 __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::channel>::threads, 1)
     kvq_prefill_ws_kernel(const PrefillWsParams p) {
@@ -425,11 +426,9 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
 #pragma unroll
         for (int kk = 0; kk < kTcStep / 16; ++kk)
           tc_mma_f16_ts(to, tp + 8 * kk, sw128_desc(vta + kk * 32), id_o, (!first || kk > 0) ? 1u : 0u);
-        if constexpr (!DIFF) {
 #pragma unroll
-          for (int kk = 0; kk < kTcStep / 16; ++kk)
-            tc_mma_f16_ts(to, tp + 32 + 8 * kk, sw128_desc(vta + kk * 32), id_o, 1u);
-        }
+        for (int kk = 0; kk < kTcStep / 16; ++kk)
+          tc_mma_f16_ts(to, tp + 32 + 8 * kk, sw128_desc(vta + kk * 32), id_o, 1u);
         tc_commit(pv_bar(C, g));
       };
       int gbase = 0, n_done = 0;  // global steps before the item, items with steps done
@@ -709,21 +708,11 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
               f2_unpack(f2_mul(f2_pack(w0, w1), f2_pack(v4.x, v4.y)), w0, w1);
               f2_unpack(f2_mul(f2_pack(w2, w3), f2_pack(v4.z, v4.w)), w2, w3);
             }
-            if constexpr (DIFF) {
-              const __half2 a = __floats2half2_rn(w0, w1), b = __floats2half2_rn(w2, w3);
-              hv[c] = *reinterpret_cast<const uint32_t*>(&a);
-              hv[c + 1] = *reinterpret_cast<const uint32_t*>(&b);
-            } else {
-              tc_split2(w0, w1, hv[c], lv[c]);
-              tc_split2(w2, w3, hv[c + 1], lv[c + 1]);
-            }
+            tc_split2(w0, w1, hv[c], lv[c]);
+            tc_split2(w2, w3, hv[c + 1], lv[c + 1]);
           }
-          if constexpr (DIFF) {
-            tc_st16(tS + 16 * hf, hv);
-          } else {
-            tc_st16(tS + 16 * hf, hv);
-            tc_st16(tS + 32 + 16 * hf, lv);
-          }
+          tc_st16(tS + 16 * hf, hv);
+          tc_st16(tS + 32 + 16 * hf, lv);
         }
         if constexpr (DIFF) {
           // the other tile has read the last item's O, which the P.V to come overwrites
