@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
   int* PS = wtot + kDecodeWarps;                   // [S + 1] steps before each sequence
 
   // tokens of sequence s to attend here (the cascade has seen its first `skip` blocks)
-  auto tokens_of = [&](int s) { return min(p.lens[s], p.max_ctx) - (p.skip << bl); };
+  auto tokens_of = [&](int s) { return tokens_behind(p.lens[s], p.max_ctx, p.skip, pool.bs); };
 
   // ---- steps per sequence and their prefix (every CTA computes the same)
   {
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
       int v = 0;
       if (s < p.S) {
         if (p.lens[s] > p.max_ctx && blockIdx.x == 0) set_error(pool.err, ERR_RANGE);
-        v = (max(tokens_of(s), 0) + kDecode4Span - 1) / kDecode4Span * U;
+        v = (tokens_of(s) + kDecode4Span - 1) / kDecode4Span * U;
       }
       int x = v;
 #pragma unroll

@@ -64,6 +64,13 @@ __device__ __forceinline__ float diff_factor(const DiffOut& o, float ss) {
   return v > 0.f ? o.out_scale * rsqrtf(v) : 0.f;
 }
 
+// Tokens of a sequence behind the blocks that the cascade has attended: none for a negative
+// length, however negative.
+__device__ __forceinline__ int tokens_behind(int len, int max_ctx, int skip, int bs) {
+  const int64_t n = (int64_t)min(len, max_ctx) - (int64_t)skip * bs;
+  return n > 0 ? static_cast<int>(n) : 0;
+}
+
 struct DecodeParams {
   PoolView pool;
   const __half* q;     // [S][Hq][D], rows q_stride elements apart
@@ -1370,8 +1377,7 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const __grid_c
       const int s = base + threadIdx.x;
       int v = 0;
       if (s < p.S) {
-        const int L = min(p.lens[s], p.max_ctx) - p.skip * p.pool.bs;
-        v = L > 0 ? (L + p.span - 1) / p.span * U : 0;
+        v = (tokens_behind(p.lens[s], p.max_ctx, p.skip, p.pool.bs) + p.span - 1) / p.span * U;
       }
       int x = v;
 #pragma unroll
