@@ -52,7 +52,7 @@ cudaError_t launch_prefill_tc(const PoolView& pool, const __half* q, int S, int 
   p.max_ctx = max_ctx;
   p.ntiles = static_cast<int>(ntiles);
   p.ngroups = static_cast<int>(ngroups);
-  p.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  p.scale = TcScale(sm_scale);
   l.grid = dim3(static_cast<unsigned>(grid));
   l.st = st;
   switch (pool.fmt) {
@@ -156,7 +156,7 @@ cudaError_t launch_prefill_ws(const PoolView& pool, const __half* q, int S, int 
   ap.G = G;
   ap.max_ctx = max_ctx;
   ap.max_steps = max_steps;
-  ap.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  ap.scale = TcScale(sm_scale);
   const bool d = diff != nullptr;
   if (d) ap.diff = *diff;
   switch (pool.fmt) {

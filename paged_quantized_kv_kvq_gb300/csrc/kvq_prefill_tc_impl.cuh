@@ -36,6 +36,7 @@
 // the CTA then flags a timeout in the pool's error word, waits (bounded) for
 // its MMAs in flight and frees TMEM.
 #pragma once
+#include <algorithm>
 #include <cstdint>
 #include <cuda_fp16.h>
 
@@ -49,6 +50,26 @@ constexpr int kTcStep = 64;       // key tokens per step
 constexpr int kTcSlack = 8;       // log2 of how far a row may exceed its reference maximum
 constexpr int kTcConv = 128;      // converter threads
 
+// Scale of the scores.  The softmax of the prompt kernels takes the largest raw score for the largest
+// scaled one and scales behind the mask, so the factor is positive: the products with K take
+// -q where the caller's scale is negative, and the smallest normal number stands for a scale
+// of zero, and whatever rounds below it (scores stay below 2^36, all weights are equal).
+// (A q with another sign, or none, in the tile instead: the loads of q and the registers that
+// came with them made the attention of INT8 and 4-bit prompts 2 to 3% longer.)
+struct TcScale {
+  static constexpr float kLeast = 1.17549435e-38f;
+  float factor = 1.f;   // to the base 2
+  uint32_t negate = 0;  // bits of the products' descriptor
+  TcScale() = default;
+  explicit TcScale(float sm_scale) {
+    const float x = sm_scale * 1.4426950408889634f;
+    factor = std::max(x < 0.f ? -x : x, kLeast);
+    negate = x < 0.f ? kTcNegateA : 0;
+  }
+  // For a q that was multiplied by 2^eq.
+  __device__ __forceinline__ float over(int eq) const { return fmaxf(ldexpf(factor, -eq), kLeast); }
+};
+
 struct PrefillTcParams {
   PoolView pool;
   const __half* q;      // [Tq][Hq][D]
@@ -59,7 +80,7 @@ struct PrefillTcParams {
   int S, Hq, G, max_blocks, max_ctx;
   int ntiles;           // 128-row tiles per (sequence, kv head)
   int ngroups;          // CTAs per (sequence, kv head): ceil(ntiles / NT)
-  float sm_scale_log2;
+  TcScale scale;
 };
 
 // Shared-memory plan of a CTA with NT tiles (byte offsets from a 1024-byte
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
   if (warp == 0) tc_alloc(tslot, PL::cols);
 
   // ---- softmax threads: their own Q row into the tile (K-major, swizzled)
-  float csc = p.sm_scale_log2;
+  float csc = p.scale.factor;
   if (is_sm) {
     const __half* src = row_ok ? p.q + orow * D : nullptr;
     char* qx = sm + PL::q + X * PL::QB;
@@ -376,7 +397,7 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
         for (int d = 0; d < D; ++d) amax = fmaxf(amax, fabsf(__half2float(src[d]) * ksc[d]));
       const int eq = amax > 0.f ? 13 - exponent_of(amax) : 0;
       const float up = ldexpf(1.f, eq);
-      csc = ldexpf(csc, -eq);
+      csc = p.scale.over(eq);
       for (int c = 0; c < D / 8; ++c) {
         uint4 hv4 = make_uint4(0, 0, 0, 0), lv4 = make_uint4(0, 0, 0, 0);
         if (src) {
@@ -529,7 +550,7 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
     const uint32_t pla = pha + PL::PB;
     char* p_hi = sm + PL::pw + X * 2 * PL::PB;
     char* p_lo = p_hi + PL::PB;
-    constexpr uint32_t id_s = tc_idesc_f16(128, kTcStep);
+    const uint32_t id_s = tc_idesc_f16(128, kTcStep) | p.scale.negate;
     constexpr uint32_t id_o = tc_idesc_f16(128, D);
     const bool issuer = r == 0;  // thread 0 of the tile
     const int bar_id = 1 + X;
@@ -603,7 +624,7 @@ __global__ void __launch_bounds__(TcPlan<D, NT, FmtTraits<FMT>::channel>::thread
           mx = fmaxf(mx, z[t]);
         }
       }
-      // scores in log2 units are z * csc (csc > 0).  The reference maximum m
+      // scores in log2 units are z * csc (csc > 0, TcScale).  The reference maximum m
       // moves only when the step's maximum passes it by more than kTcSlack,
       // so the TMEM accumulator is rescaled only then (or when E drops).
       const float mxz = mx == kNegInf ? kNegInf : mx * csc;

@@ -168,7 +168,7 @@ struct PrefillWsParams {
   const char* ws;       // staged records
   int S, Hq, G, max_ctx, max_steps;
   int ngroups;          // CTAs per (sequence, kv head): ceil(tiles / NT)
-  float sm_scale_log2;
+  TcScale scale;
   DiffOut diff;         // DIFF: where its rows go, in the place of `out`
 };
 
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
     // ============ control: tile C's MMAs ============
     const int C = warp - 4 * NT;
     if (lane == 0) {
-      constexpr uint32_t id_s = tc_idesc_f16(128, kTcStep);
+      const uint32_t id_s = tc_idesc_f16(128, kTcStep) | p.scale.negate;
       constexpr uint32_t id_o = tc_idesc_f16(128, D);
       const uint32_t qa = smem_u32(sm + PL::q + C * PL::QB);
       const uint32_t qla = smem_u32(sm + PL::q + (NT + C) * PL::QB);
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
           rr < it.rows_total
               ? p.q + ((int64_t)(it.qbase + rr / p.G) * p.Hq + it.h * p.G + rr % p.G) * D
               : nullptr;
-      float csc = p.sm_scale_log2;
+      float csc = p.scale.factor;
       if constexpr (!CH) {
         // the warp loads its 32 rows together: one instruction covers 256 / D
         // whole rows (each row's source address comes from its owner lane);
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
           for (int d = 0; d < D; ++d) amax = fmaxf(amax, fabsf(__half2float(src[d]) * ksc[d]));
         const int eq = amax > 0.f ? 13 - exponent_of(amax) : 0;
         const float up = ldexpf(1.f, eq);
-        csc = ldexpf(csc, -eq);
+        csc = p.scale.over(eq);
         for (int c = 0; c < D / 8; ++c) {
           uint4 hv4 = make_uint4(0, 0, 0, 0), lv4 = make_uint4(0, 0, 0, 0);
           if (src) {
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         }
         mx = mq[0];
         if constexpr (FAST) mx = fmax3(fmaxf(mq[0], mq[1]), mq[2], mq[3]);
-        // scores in log2 units are z * csc (csc > 0); the reference maximum m
+        // scores in log2 units are z * csc (csc > 0, TcScale); the reference maximum m
         // moves only when the step's maximum passes it by more than kTcSlack
         const float mxz = mx == kNegInf ? kNegInf : mx * csc;
         const float mn = (m == kNegInf || mxz > m + kTcSlack) ? mxz : m;
