@@ -291,8 +291,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kDecode4Ctas)
       float ss = 0.f;
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) {
-        o[mt][0] = o[mt][0] * f0 - o[mt][1] * f1l;
-        o[mt][2] = o[mt][2] * f0 - o[mt][3] * f1l;
+        o[mt][0] = diff_of(o[mt][0], f0, o[mt][1], f1l);
+        o[mt][2] = diff_of(o[mt][2], f0, o[mt][3], f1l);
         ss = fmaf(o[mt][0], o[mt][0], fmaf(o[mt][2], o[mt][2], ss));
       }
       const float f = diff_factor<D>(p.diff, warp_sum_over_rows(ss));

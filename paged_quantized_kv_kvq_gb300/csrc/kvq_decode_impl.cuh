@@ -71,6 +71,12 @@ __device__ __forceinline__ int tokens_behind(int len, int max_ctx, int skip, int
   return n > 0 ? static_cast<int>(n) : 0;
 }
 
+// a fa - b fb of two maps, whose products are rounded one by one: equal maps at lambda 1 leave 0,
+// where a fused multiply-add would leave the rounding of one product, which the norm enlarges.
+__device__ __forceinline__ float diff_of(float a, float fa, float b, float fb) {
+  return __fsub_rn(__fmul_rn(a, fa), __fmul_rn(b, fb));
+}
+
 struct DecodeParams {
   PoolView pool;
   const __half* q;     // [S][Hq][D], rows q_stride elements apart
@@ -1025,8 +1031,8 @@ __global__ void __launch_bounds__(kDecodeThreads, CTAS)
       for (int mt = 0; mt < KS; ++mt) {
         const int d0 = 16 * mt + g;
         const float c0 = T::channel ? vch[d0] : 1.f, c8 = T::channel ? vch[d0 + 8] : 1.f;
-        o[mt][0] = (o[mt][0] * f0 - o[mt][1] * f1l) * c0;
-        o[mt][2] = (o[mt][2] * f0 - o[mt][3] * f1l) * c8;
+        o[mt][0] = diff_of(o[mt][0], f0, o[mt][1], f1l) * c0;
+        o[mt][2] = diff_of(o[mt][2], f0, o[mt][3], f1l) * c8;
         ss = fmaf(o[mt][0], o[mt][0], fmaf(o[mt][2], o[mt][2], ss));
       }
       const float f = diff_factor<D>(p.diff, warp_sum_over_rows(ss));
@@ -1460,9 +1466,9 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < NE; ++e) acc[e] = 0.f;
         merge_pieces<D, CH>(p, t.wf, t.n_u, t.U0, ppw, 2 * t.i + r, lane, M, Lsum, acc);
-        const float f = Lsum > 0.f ? (r == 0 ? 1.f : -lam) / Lsum : 0.f;
+        const float f = Lsum > 0.f ? (r == 0 ? 1.f : lam) / Lsum : 0.f;
 #pragma unroll
-        for (int e = 0; e < NE; ++e) y[e] = r == 0 ? acc[e] * f : fmaf(acc[e], f, y[e]);
+        for (int e = 0; e < NE; ++e) y[e] = r == 0 ? acc[e] * f : diff_of(y[e], 1.f, acc[e], f);
       }
 #pragma unroll
       for (int e = 0; e < NE; ++e) ss = fmaf(y[e], y[e], ss);

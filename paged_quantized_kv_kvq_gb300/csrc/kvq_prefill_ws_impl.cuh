@@ -747,7 +747,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
         const int head = it.h * p.G + rr % p.G;
         const float lam = row_ok ? p.diff.lambda[head] : 0.f;
         const float f = l > 0.f ? pow2f(-E) / l : 0.f;
-        facs[X * kTcRows + r] = X == 0 ? f : -lam * f;
+        facs[X * kTcRows + r] = X == 0 ? f : lam * f;
         tc_fence_before();
         warp_arrive(&x_ready[X]);
         if (!warp_wait(&x_ready[X ^ 1], n_done & 1, abort_f)) {
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(WsPlan<D, WsShape<FMT>::NT, FmtTraits<FMT>::ch
           tc_ld32(tmem + 128 + lane_base + X * (D / 2) + 32 * c, o1);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
-            const float v = fmaf(o1[i], f1, o0[i] * f0);
+            const float v = diff_of(o0[i], f0, o1[i], f1);
             y[32 * c + i] = v;
             ss = fmaf(v, v, ss);
           }
