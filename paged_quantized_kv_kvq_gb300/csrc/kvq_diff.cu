@@ -18,12 +18,13 @@ namespace {
 
 constexpr int kDiffThreads = 256;
 
-// q [T][H][D] -> [T][2H][D]: rows 2h and 2h + 1 of a token are the maps of head h.
-__global__ void __launch_bounds__(kDiffThreads) kvq_diff_expand_kernel(const __half* q, __half* out,
-                                                                       int64_t chunks, int cpr_log2) {
+// q [T][H][D] -> [T][2H][D]: rows 2h and 2h + 1 of a token are the maps of head h.  Tokens of
+// the sequences alone: others are not read.
+__global__ void __launch_bounds__(kDiffThreads) kvq_diff_expand_kernel(const __half* q, __half* out, const int* q_start,
+                                                                       int S, int64_t chunks, int H, int cpr_log2) {
   // a thread: 8 channels of one map's half row, and zeros in the other map's row
   const int64_t i = (int64_t)blockIdx.x * kDiffThreads + threadIdx.x;
-  if (i >= chunks) return;
+  if (i >= chunks || i < (int64_t)q_start[0] * H << cpr_log2 || i >= (int64_t)q_start[S] * H << cpr_log2) return;
   const uint4 v = reinterpret_cast<const uint4*>(q)[i];
   const int64_t row = i >> cpr_log2;
   const int c = static_cast<int>(i & ((1 << cpr_log2) - 1)), map = c >> (cpr_log2 - 1);
@@ -32,21 +33,38 @@ __global__ void __launch_bounds__(kDiffThreads) kvq_diff_expand_kernel(const __h
   dst[(map ^ 1) << cpr_log2] = make_uint4(0, 0, 0, 0);
 }
 
-// o [T][2H][D] -> the normed differences [T][H][D], a warp for each; rows from
-// *rows on are left as they were.
+// o [T][2H][D] -> the normed differences [T][H][D], a warp for each.  Rows that the prefill
+// did not write are left as they were: before the first sequence, behind the last, and past
+// max_q_len in one.
 template <int D>
-__global__ void __launch_bounds__(kDiffThreads) kvq_diff_combine_kernel(const float* o, const int* rows,
-                                                                        int H, DiffOut p) {
+__global__ void __launch_bounds__(kDiffThreads) kvq_diff_combine_kernel(const float* o, const int* q_start, int S,
+                                                                        int max_q_len, int64_t heads, int H, DiffOut p) {
   constexpr int NE = D / 32;
   const int lane = threadIdx.x & 31;
   const int64_t i = (int64_t)blockIdx.x * (kDiffThreads / 32) + (threadIdx.x >> 5);
-  if (i >= (int64_t)*rows * H) return;
-  const float lam = p.lambda[i % H];
+  if (i >= heads) return;
   const float* a = o + i * 2 * D + lane * NE;
+  float y0[NE], y1[NE];  // (on their way while the row's sequence is looked up)
+#pragma unroll
+  for (int e = 0; e < NE; ++e) {
+    y0[e] = a[e];
+    y1[e] = a[D + e];
+  }
+  const int row = static_cast<int>(i / H);
+  if (row < q_start[0] || row >= q_start[S]) return;
+  int lo = 0;  // q_start[lo] <= row: of 32 at a time
+  for (int n = S; n > 1;) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const int last = __popc(__ballot_sync(0xffffffffu, at < n && q_start[lo + min(at, n - 1)] <= row)) - 1;
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  if (row - q_start[lo] >= max_q_len) return;
+  const float lam = p.lambda[i - (int64_t)row * H];
   float y[NE], ss = 0.f;
 #pragma unroll
   for (int e = 0; e < NE; ++e) {
-    y[e] = a[e] - lam * a[D + e];
+    y[e] = y0[e] - lam * y1[e];
     ss = fmaf(y[e], y[e], ss);
   }
 #pragma unroll
@@ -99,7 +117,7 @@ cudaError_t launch_diff_prefill(const PoolView& pool, const __half* q, int64_t T
   const int64_t chunks = T * H * (D / 8), heads = T * H;
   const int64_t eg = (chunks + kDiffThreads - 1) / kDiffThreads, cg = (heads + 7) / 8;
   if (eg > 0x7fffffffLL || cg > 0x7fffffffLL) return cudaErrorInvalidValue;
-  kvq_diff_expand_kernel<<<static_cast<unsigned>(eg), kDiffThreads, 0, st>>>(q, qx, chunks, D == 64 ? 3 : 4);
+  kvq_diff_expand_kernel<<<static_cast<unsigned>(eg), kDiffThreads, 0, st>>>(q, qx, q_start, S, chunks, H, D == 64 ? 3 : 4);
   cudaError_t e = phase_mark(st, cudaGetLastError());
   if (e != cudaSuccess) return e;
   e = prefill_ws_bytes(pool, S, max_ctx) > 0
@@ -109,9 +127,9 @@ cudaError_t launch_diff_prefill(const PoolView& pool, const __half* q, int64_t T
                            sm_scale, o, st);
   if (e != cudaSuccess) return e;
   if (D == 64)
-    kvq_diff_combine_kernel<64><<<static_cast<unsigned>(cg), kDiffThreads, 0, st>>>(o, q_start + S, H, diff);
+    kvq_diff_combine_kernel<64><<<static_cast<unsigned>(cg), kDiffThreads, 0, st>>>(o, q_start, S, max_q_len, heads, H, diff);
   else
-    kvq_diff_combine_kernel<128><<<static_cast<unsigned>(cg), kDiffThreads, 0, st>>>(o, q_start + S, H, diff);
+    kvq_diff_combine_kernel<128><<<static_cast<unsigned>(cg), kDiffThreads, 0, st>>>(o, q_start, S, max_q_len, heads, H, diff);
   return phase_mark(st, cudaGetLastError());
 }
 
