@@ -340,7 +340,8 @@ size_t kvq_decode_workspace_bytes(const kvq_pool* pool, int num_seqs, int num_q_
  *   block_table   : int32 [num_seqs][max_blocks_per_seq] physical block ids
  *   context_lens  : int32 [num_seqs] tokens to attend (after this step's append)
  *   max_context_len : host-side upper bound of context_lens, <= max_blocks_per_seq*block_size
- *   sm_scale      : softmax scale (usually 1/sqrt(head_dim))
+ *   sm_scale      : softmax scale (usually 1/sqrt(head_dim)), of any sign; 0 weighs all
+ *                   tokens alike
  *   out           : fp32 [num_seqs][num_q_heads][head_dim]
  *   workspace     : >= kvq_decode_workspace_bytes(..) bytes, 256-byte aligned
  *                   (may be NULL when that is 0)
@@ -636,8 +637,8 @@ size_t kvq_diff_prefill_workspace_bytes(const kvq_pool* pool, int num_seqs, int6
                                         int num_heads, int max_context_len);
 
 /* Prompts and chunks of them.
- *   q, out     : fp16 [num_tokens][num_heads][head_dim]; rows from q_start[num_seqs] on
- *                are not read, and left as they were; 16-byte aligned
+ *   q, out     : fp16 [num_tokens][num_heads][head_dim]; rows before q_start[0] and from
+ *                q_start[num_seqs] on are not read, and left as they were; 16-byte aligned
  *   num_tokens : rows of q and out, >= q_start[num_seqs]
  *   workspace  : >= kvq_diff_prefill_workspace_bytes(..) bytes, 256-byte aligned
  * lambda, norm_weight, eps and out_scale are those of kvq_diff_decode, the other
@@ -697,10 +698,10 @@ kvq_status kvq_extend_tables(const kvq_pool* pool, const int32_t* new_tokens, in
  *                   are not given back
  *   count_out     : int32 [1]; may be free_count
  * A block must not be given back twice, nor while another sequence holds it.  Neither the
- * table nor lengths are changed.  Device errors: a negative length (taken as 0), one
- * beyond the row (clamped), a count outside the list (clamped), an id outside the pool
- * (not given back) and a full list (blocks beyond it are not given back) set
- * OUT_OF_RANGE.  UNSUPPORTED beyond 16384 sequences and from 2^31 - 1 table entries on. */
+ * table nor lengths are changed.  Device errors: a negative length (taken as 0), an old
+ * length beyond the row (clamped; a new one beyond it keeps the whole row), a count outside
+ * the list (clamped), an id outside the pool (not given back) and a full list (blocks
+ * beyond it are not given back) set OUT_OF_RANGE.  UNSUPPORTED beyond 16384 sequences and from 2^31 - 1 table entries on. */
 kvq_status kvq_release_blocks(const kvq_pool* pool, const int32_t* block_table, int max_blocks_per_seq,
                               const int32_t* old_lens, const int32_t* new_lens, int num_seqs,
                               int shared_blocks, int32_t* free_list, int free_capacity,
