@@ -4,7 +4,7 @@
 // dequantized on the way, one pass with a running maximum and sum, long sequences cut
 // over warps and joined by the merge kernel.  What differs is what bounds it.  At 4.5
 // bits a value a page is a quarter of an FP16 one while its tokens want the same products and
-// weights, so the instructions per token decide, not the bytes (64 x 2048 tokens, 8 kv
+// weights, so the work per token decides, not the bytes (64 x 2048 tokens, 8 kv
 // heads of 128: 22 us of HBM time; the general kernel took 53):
 //  * A step is 64 tokens whatever the block size: one barrier, one softmax update, one look
 //    at the bookkeeping for four sub-tiles instead of two or one.
@@ -24,6 +24,8 @@
 // Measured, calls replayed back to back: 64 x 2048 37.7 us (151 MB, 4.0 TB/s, 0.59 of the copy
 // rate), 64 x 512 16.4, 64 x 8192 116.9: some 26 us for 2048 more tokens (0.84 of the copy
 // rate) and 11 us of start, merge and uneven ends; 8 x 16384..32768 in blocks of 32: 47.0.
+// Neither HBM (52%) nor the issue slots (48%) are full: with 2.8 warps a scheduler one is ready in 56% of
+// the cycles, so a step's waits -- conversion, softmax and P.V follow each other in a warp -- bound it.
 // (One stage of 16 warps a CTA instead of two stages for each of 4: more instructions,
 // slower at every length.)
 #pragma once

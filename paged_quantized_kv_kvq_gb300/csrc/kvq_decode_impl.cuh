@@ -1486,7 +1486,9 @@ __global__ void __launch_bounds__(kMergeThreads) kvq_merge_kernel(const __grid_c
 }
 
 // The same with nothing looked up ahead, in fewer registers (80 and 126 a thread against 91 and
-// 147), so that more of it is resident: for merges of more CTAs than two an SM.  Decode steps of
+// 147), so that more of it is resident: for merges of more CTAs than two for each of the GPU's 152
+// SMs.  (Differential merges, half as many CTAs, take that kernel at any size; above the limit the two were
+// not compared for them.)  Decode steps of
 // 32 layers with that kernel and this one: 64 x 2048, 256 CTAs, 1.756 and 1.819 ms; 100
 // sequences with 32 heads, 400 CTAs, INT8 groups of 64 6.198 and 6.112, e4m3 5.586 and 5.518; 256
 // sequences of 8 kv heads and groups of 4, 1024 CTAs, 7.10 and 6.88.  (That kernel held to 80

@@ -5,8 +5,11 @@
 // (kvq_prefill_ws_impl.cuh).  Formats that it does not take (per-channel scales, several scale
 // groups per head): every head becomes two Q rows, one per map with the other map's
 // channels zero, the prefill kernels attend them, and a last kernel takes the
-// difference of the two results of a head, norms it and rounds it.  (The form for two maps
-// does half the score products and needs no expanded queries and no fp32 results.)
+// difference of the two results of a head, norms it and rounds it.  The form for two maps
+// does half the score products and needs no expanded queries and no fp32 results.  Calls of 8 x
+// 2048, 16 heads over 4 kv heads of 128: two maps 359 us over 4-bit floats, 369 over FP16, 399 over INT8
+// blocks and INT8 groups of 128; expanded 1299 per channel (two fp16 parts of q, one tile a CTA), 2930 over INT8
+// groups of 32 and 2550 over INT4 groups of 32 (whose prompts have no tcgen05 kernel).
 #include <algorithm>
 
 #include "kvq_decode_impl.cuh"

@@ -45,7 +45,7 @@
 // P.V before it could write the weights: 8 x 2048, 4-bit floats, 436 us; so 397, and with
 // INT8 groups the attention pass alone 467 us, 589 TFLOP/s.)  What bounds it is each row's
 // chain from tensor memory through the softmax and back (two maps, 4-bit floats: issue slots
-// 36% busy, the tensor pipe 30%), not the tensor cores.  The two
+// 41% busy, the tensor pipe 45%), not the tensor cores.  The two
 // tiles' softmax and tensor work interleave.  The next item's Q
 // rows are loaded before the current item's epilogue, whose output rows go
 // out through a per-warp shared-memory transpose.  The threads meet
