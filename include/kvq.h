@@ -701,7 +701,8 @@ kvq_status kvq_extend_tables(const kvq_pool* pool, const int32_t* new_tokens, in
  * table nor lengths are changed.  Device errors: a negative length (taken as 0), an old
  * length beyond the row (clamped; a new one beyond it keeps the whole row), a count outside
  * the list (clamped), an id outside the pool (not given back) and a full list (blocks
- * beyond it are not given back) set OUT_OF_RANGE.  UNSUPPORTED beyond 16384 sequences and from 2^31 - 1 table entries on. */
+ * beyond it are not given back) set OUT_OF_RANGE.  UNSUPPORTED beyond 16384 sequences and
+ * from 2^31 - 1 table entries on. */
 kvq_status kvq_release_blocks(const kvq_pool* pool, const int32_t* block_table, int max_blocks_per_seq,
                               const int32_t* old_lens, const int32_t* new_lens, int num_seqs,
                               int shared_blocks, int32_t* free_list, int free_capacity,
