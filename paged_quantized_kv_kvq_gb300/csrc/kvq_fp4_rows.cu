@@ -18,9 +18,9 @@
 // a warp for its 16 tokens, counted) and the wait for the slots, then the rows: issue slots
 // 46% busy from a cold cache, DRAM 40%.  Measured, 16384 tokens x 8 heads of 128: whole
 // blocks 16.9 us replayed (86 MB, part of which the L2 keeps between replays; 21.9 from a
-// cold cache, 0.58 of the copy rate), from inside a block 17.1, single tokens 76; read back 17.2, 18.2 and 47.  (Sub-tile by sub-tile of the 16 tokens
-// instead of runs: 16.6 us for whole blocks, but 32 from inside a block and 235 for
-// single tokens.)
+// cold cache, 0.58 of the copy rate), from inside a block 17.1, single tokens 76; read
+// back 17.2, 18.2 and 47.  (Sub-tile by sub-tile of the 16 tokens instead of runs: 16.6 us
+// for whole blocks, but 32 from inside a block and 235 for single tokens.)
 #include "kvq_context.h"
 #include "kvq_f32x2.cuh"
 #include "kvq_fp4.cuh"

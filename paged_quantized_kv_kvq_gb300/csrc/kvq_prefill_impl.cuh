@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kPfThreads) kvq_prefill_kernel(const PrefillPa
   int ctx = p.lens[seq];
   if (ctx > p.max_ctx || ctx < nq) {
     if (tile == 0 && h == 0 && threadIdx.x == 0) set_error(pool.err, ERR_RANGE);
-    ctx = min(ctx, p.max_ctx);
+    ctx = max(0, min(ctx, p.max_ctx));  // (what is below zero would wrap around less nq)
   }
   const int rows_total = nq * p.G;
   if (tile * kPfRows >= rows_total) return;  // past this sequence's chunk (CTA-uniform)
